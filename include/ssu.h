@@ -324,6 +324,174 @@ ssu_status ssu_gdn_decode(const ssu_gdn_dims *dims, const void *hidden_states, c
 int64_t ssu_gdn_workspace_bytes(const ssu_gdn_dims *dims);
 
 /* ------------------------------------------------------------------------
+ * Per-channel selective scan and the short causal convolution in front of it,
+ * for prompts and for single tokens, over paged state pools. Here a decay
+ * belongs to a channel and a state entry (A [dim, dstate], dt per channel),
+ * where ssu_decode and ssu_prefill have one per head. Activations may be
+ * slices of wider tensors: their channel axis is contiguous, the batch and
+ * token strides are given in elements (0 = dense; a token stride is at least
+ * the row's length). All pointers need the alignment of their element unless
+ * stated. Pool rows, negative state_indices and context_lengths are as in
+ * ssu_decode and ssu_prefill.
+ * ---------------------------------------------------------------------- */
+typedef struct ssu_conv_dims {
+    int32_t batch;
+    int32_t channels;
+    int32_t width;       /* W, 1..8 (else SSU_ENOTSUP) */
+    int32_t pool_rows;   /* P: leading extent of conv_state; with no state_indices, batch <= P */
+    int32_t io_dtype;    /* x, out: SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t weight_dtype; /* weight, bias: the same three */
+    int32_t state_dtype; /* conv_state: the same three */
+    int32_t reserved;    /* must be 0 */
+    int64_t x_batch_stride, x_token_stride;
+    int64_t out_batch_stride, out_token_stride;
+    int64_t state_row_stride;  /* element strides of conv_state's logical     */
+    int64_t state_chan_stride; /* [P, channels, W-1] view, any layout whose   */
+    int64_t state_tap_stride;  /* entries do not overlap; all three 0 = dense */
+} ssu_conv_dims;
+
+/* ssu_conv_prefill -- depthwise causal convolution of seq_len tokens. With
+ * r = state_indices[b] (or b), L_b = clamp(context_lengths[b], 0, seq_len) and
+ * win = conv_state[r, c, 0..W-2] followed by x[b, 0.., c] (oldest first):
+ *   out[b,t,c] = act(bias[c] + sum_j weight[c,j] * win[t+j])   for t < L_b
+ *   conv_state[r, c, j] = win[L_b + j]                          (j < W-1)
+ * act is silu when `silu` is non-zero, the identity otherwise. out[b,t] = +0.0
+ * for t >= L_b, where x is not read. With update_state == 0 the pool is only
+ * read (a window of drafted tokens; to commit k of them, call again with
+ * context_lengths = k). out may be NULL when the state is updated (only the
+ * state is wanted then). Padding rows: out[b] = +0.0, no pool access.
+ * Layouts: x, out [batch, seq_len, channels]; weight [channels, W] and bias
+ * [channels] dense. out must not overlap x (x == out is refused). Optional:
+ * bias, out, context_lengths, state_indices; conv_state when W == 1. */
+ssu_status ssu_conv_prefill(const ssu_conv_dims *dims, int32_t seq_len, const void *x,
+                            const void *weight, const void *bias, void *conv_state, void *out,
+                            int32_t silu, int32_t update_state, const int32_t *context_lengths,
+                            const int32_t *state_indices, hipStream_t stream);
+
+/* ssu_conv_decode -- the same for one token: x, out [batch, channels] (the
+ * token strides are ignored). The state is updated. out may be x. */
+ssu_status ssu_conv_decode(const ssu_conv_dims *dims, const void *x, const void *weight,
+                           const void *bias, void *conv_state, void *out, int32_t silu,
+                           const int32_t *state_indices, hipStream_t stream);
+
+typedef struct ssu_scan_dims {
+    int32_t batch;
+    int32_t dim;         /* channels */
+    int32_t dstate;      /* a multiple of 4, 4..256 (else SSU_ENOTSUP) */
+    int32_t ngroups;     /* divides dim; channel d reads group d / (dim / ngroups) */
+    int32_t pool_rows;
+    int32_t state_dtype; /* state: SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t io_dtype;    /* x, z, out */
+    int32_t dt_dtype;    /* dt */
+    int32_t bc_dtype;    /* B, C */
+    int32_t reserved;    /* must be 0 */
+    int64_t state_row_stride; /* elements, a multiple of 4; 0 = dim * dstate */
+    int64_t x_batch_stride, x_token_stride;
+    int64_t z_batch_stride, z_token_stride;
+    int64_t out_batch_stride, out_token_stride;
+    int64_t dt_batch_stride, dt_token_stride;
+    int64_t b_batch_stride, b_token_stride; /* each token's [ngroups, dstate] is dense */
+    int64_t c_batch_stride, c_token_stride;
+} ssu_scan_dims;
+
+/* ssu_scan_decode -- one token. With r = state_indices[b] (or b) and g the
+ * group of channel d:
+ *   dt'         = dt[b,d] + dt_bias[d];  dt' = softplus(dt') if dt_softplus
+ *   state[r,d,n] = state[r,d,n] * exp(A[d,n]*dt') + B[b,g,n] * dt' * x[b,d]
+ *   out[b,d]    = sum_n state[r,d,n]*C[b,g,n] + D[d]*x[b,d], then
+ *                 * silu(z[b,d]) if z is given
+ * Layouts: x, z, out, dt [batch, dim] (the token strides are ignored); B, C
+ * [batch, ngroups, dstate]; A [dim, dstate], dt_bias, D [dim] fp32, dense;
+ * state [pool_rows, dim, dstate], rows dense, updated in place. A and state
+ * are aligned to four elements. Optional: dt_bias, D, z, state_indices.
+ * Padding rows: out[b] = +0.0, no pool access. out may be x or z. */
+ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float *A,
+                           const void *B, const void *C, const void *dt, const float *dt_bias,
+                           const float *D, const void *z, void *state, void *out,
+                           int32_t dt_softplus, const int32_t *state_indices,
+                           hipStream_t stream);
+
+/* ssu_scan_prefill -- seq_len tokens in one launch: row b runs its first
+ * L_b = clamp(context_lengths[b], 0, seq_len) tokens through the step of
+ * ssu_scan_decode in order; out[b,t] = +0.0 for t >= L_b, where no input is
+ * read. x, z, out, dt [batch, seq_len, dim]; B, C [batch, seq_len, ngroups,
+ * dstate]. With update_state == 0 the pool is only read (a window of drafted
+ * tokens; to commit k of them, call again with context_lengths = k). out may be
+ * NULL when the state is updated (C, D and z are not read then, C may be
+ * NULL). out must not overlap an input (equal pointers are refused). Rows with
+ * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
+ * call and rounded once, at its end. */
+ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const void *x,
+                            const float *A, const void *B, const void *C, const void *dt,
+                            const float *dt_bias, const float *D, const void *z, void *state,
+                            void *out, int32_t dt_softplus, int32_t update_state,
+                            const int32_t *context_lengths, const int32_t *state_indices,
+                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens
+ * ---------------------------------------------------------------------- */
+typedef struct ssu_verify_dims {
+    int32_t batch;
+    int32_t num_tokens; /* T: tokens (or tree nodes) fed per row, 1..SSU_MAX_TREE_NODES */
+    int32_t vocab;      /* V, 1..2^24 */
+    int32_t max_accept_len; /* row length of accepted_node_ids; ignored without it */
+    int32_t prob_dtype; /* target_probs, draft_probs: SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t reserved;   /* must be 0 */
+    int64_t target_batch_stride, target_row_stride; /* elements; 0 = dense; */
+    int64_t draft_batch_stride, draft_row_stride;   /* a row stride >= V    */
+} ssu_verify_dims;
+
+/* ssu_draft_verify -- which drafted tokens of a verify window stand, and the
+ * token after them, from given random numbers.
+ * Row b fed tokens[b, 0..L_b-1], L_b = clamp(context_lengths[b], 0, T): token
+ * 0 is certain, the others are drafted; target_probs[b,t] is the target's
+ * distribution after token t (along its path). uniforms[b,t] lies in [0, 1).
+ * Chain with draft_probs [batch, T-1, V] (tokens[b,t] was drawn from row t-1;
+ * no parent_ids): token t is accepted if all before it are and
+ *   uniforms[b,t] * draft_probs[b,t-1,x] < target_probs[b,t-1,x],  x = tokens[b,t].
+ * At the first rejection the next token is drawn from
+ * max(target_probs[b,t-1] - draft_probs[b,t-1], 0); with none it is drawn from
+ * target_probs[b, L_b-1].
+ * Given drafts (no draft_probs): a tree by parent_ids [batch, T] as in
+ * ssu_tree_verify with node 0 its root (a node whose parent is not in [0, node)
+ * hangs nowhere and is never accepted), or a chain when parent_ids is NULL.
+ * At an accepted node with distribution p its children are tried in index
+ * order: child c with token x is accepted, and becomes the node, if
+ *   uniforms[b,c] * (1 - removed) < p[x],
+ * otherwise removed += p[x] and p[x] = 0 (a token that a sibling tried before
+ * has p[x] = 0). When no child is left, or max_accept_len nodes are accepted,
+ * the next token is drawn from p as it is then. Either way the drawn tokens follow the
+ * target's distribution.
+ * Drawing from weights w: the lowest v with sum_{i<=v} w_i > uniforms[b,0] *
+ * sum_i w_i; weights without mass are replaced by the target row itself, and
+ * with no mass there either the token is -1. Negative and NaN weights count
+ * as 0. Sums and tests are in fp64. A token outside [0, V) is rejected.
+ * Results: accepted_lengths[b] = accepted tokens including token 0, as
+ * ssu_replay and context_lengths take it (0 when L_b == 0);
+ * accepted_node_ids [batch, max_accept_len] (optional) = the accepted path,
+ * root first, then -1; next_tokens[b] (-1 when L_b == 0). Padding rows
+ * (state_indices[b] < 0) are as L_b == 0. Distributions of tokens >= L_b are
+ * not read. tokens, parent_ids, uniforms dense; probabilities' vocabulary
+ * axis contiguous. Optional: draft_probs, parent_ids (not both),
+ * context_lengths, state_indices, accepted_node_ids.
+ * workspace: caller-owned device scratch of at least
+ * ssu_verify_workspace_bytes(dims) bytes, 16-byte aligned (partial sums from
+ * the first of the two launches to the second); contents on entry ignored, on
+ * return unspecified; calls sharing a workspace must be ordered (one stream). */
+ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
+                            const void *target_probs, const void *draft_probs,
+                            const float *uniforms, const int32_t *parent_ids,
+                            const int32_t *context_lengths, const int32_t *state_indices,
+                            int32_t *accepted_lengths, int32_t *accepted_node_ids,
+                            int32_t *next_tokens, void *workspace, int64_t workspace_bytes,
+                            hipStream_t stream);
+
+/* Bytes of workspace ssu_draft_verify needs: 8 * batch * (ceil(V / 2048) + 1);
+ * -1 if dims is NULL or batch or vocab is out of range. No HIP call. */
+int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims);
+
+/* ------------------------------------------------------------------------
  * Row movement between a resident pool and contiguous working rows. A row is
  * row_bytes bytes (the trailing dimensions of one pool row, any dtype); rows
  * of a buffer are `stride` bytes apart (0 = row_bytes, >= row_bytes

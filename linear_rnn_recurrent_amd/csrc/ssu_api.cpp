@@ -473,6 +473,340 @@ ssu_status ssu_gdn_decode(const ssu_gdn_dims *dims, const void *hidden_states, c
 
 namespace {
 
+// Batch and token strides of one activation: 0 selects dense, and a token's
+// row may not reach into the next one's (nor a batch row into the next).
+ssu_status check_strides(const char *fn, const char *name, int64_t bs, int64_t ts, int64_t row,
+                         int64_t tokens, int64_t *out_bs, int64_t *out_ts)
+{
+    if (ts == 0)
+        ts = row;
+    if (ts < row)
+        return fail(SSU_EINVAL, "%s: %s token stride %lld < %lld", fn, name, (long long)ts,
+                    (long long)row);
+    const int64_t span = tokens > 0 ? (tokens - 1) * ts + row : 0;
+    if (bs == 0)
+        bs = tokens * ts;
+    if (bs < span)
+        return fail(SSU_EINVAL, "%s: %s batch stride %lld < %lld", fn, name, (long long)bs,
+                    (long long)span);
+    *out_bs = bs;
+    *out_ts = ts;
+    return SSU_OK;
+}
+
+ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len, const void *x,
+                     const void *weight, const void *bias, void *conv_state, void *out,
+                     int32_t silu, int32_t update_state, const int32_t *context_lengths,
+                     const int32_t *state_indices, bool step, hipStream_t stream)
+{
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_conv_dims &d = *dims;
+    if (d.reserved != 0)
+        return fail(SSU_EINVAL, "%s: dims.reserved must be 0", fn);
+    if (d.batch < 0 || seq_len < 0)
+        return fail(SSU_EINVAL, "%s: batch %d and seq_len %d must be >= 0", fn, d.batch, seq_len);
+    if (d.channels <= 0 || d.pool_rows <= 0 || d.width <= 0)
+        return fail(SSU_EINVAL, "%s: channels/width/pool_rows must be > 0 (got %d/%d/%d)", fn,
+                    d.channels, d.width, d.pool_rows);
+    if (d.width > 8)
+        return fail(SSU_ENOTSUP, "%s: width %d > 8", fn, d.width);
+    if (!compute_dtype(d.io_dtype) || !compute_dtype(d.weight_dtype) || !compute_dtype(d.state_dtype))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype (io %d, weight %d, state %d)", fn,
+                    d.io_dtype, d.weight_dtype, d.state_dtype);
+    if (!state_indices && d.batch > d.pool_rows)
+        return fail(SSU_EINVAL, "%s: batch %d > pool_rows %d with no state_indices", fn, d.batch,
+                    d.pool_rows);
+    ssu::ConvParams p = {};
+    ssu_status st = check_strides(fn, "x", d.x_batch_stride, step ? 0 : d.x_token_stride,
+                                  d.channels, seq_len, &p.x_bs, &p.x_ts);
+    if (st != SSU_OK)
+        return st;
+    st = check_strides(fn, "out", d.out_batch_stride, step ? 0 : d.out_token_stride, d.channels,
+                       seq_len, &p.out_bs, &p.out_ts);
+    if (st != SSU_OK)
+        return st;
+    const int64_t taps = d.width - 1;
+    p.st_row = d.state_row_stride;
+    p.st_chan = d.state_chan_stride;
+    p.st_tap = d.state_tap_stride;
+    if (p.st_row < 0 || p.st_chan < 0 || p.st_tap < 0)
+        return fail(SSU_EINVAL, "%s: negative conv_state stride", fn);
+    if (p.st_row == 0 && p.st_chan == 0 && p.st_tap == 0) {
+        p.st_row = d.channels * taps;
+        p.st_chan = taps;
+        p.st_tap = 1;
+    }
+    // entries of one row are distinct for every layout with the channels of a
+    // tap, or the taps of a channel, apart from each other
+    if (taps > 0 && !((p.st_tap >= 1 || taps == 1) && (p.st_chan >= 1 || d.channels == 1) &&
+                      (p.st_chan > (taps - 1) * p.st_tap || p.st_tap > (d.channels - 1) * p.st_chan)))
+        return fail(SSU_EINVAL, "%s: conv_state strides (%lld, %lld) overlap", fn,
+                    (long long)p.st_chan, (long long)p.st_tap);
+    if (taps > 0 && d.pool_rows > 1 &&
+        p.st_row < (d.channels - 1) * p.st_chan + (taps - 1) * p.st_tap + 1)
+        return fail(SSU_EINVAL, "%s: conv_state row stride %lld too small", fn,
+                    (long long)p.st_row);
+    if ((int64_t)d.batch * ((d.channels + 255) / 256) * ((seq_len + 15) / 16) > 0x7fffffff)
+        return fail(SSU_ENOTSUP, "%s: problem too large", fn);
+    if (d.batch == 0 || seq_len == 0)
+        return ok();
+    const size_t io = io_bytes(d.io_dtype);
+    SSU_REQUIRE_PTR(x, io, fn);
+    SSU_REQUIRE_PTR(weight, io_bytes(d.weight_dtype), fn);
+    SSU_OPTIONAL_PTR(bias, io_bytes(d.weight_dtype), fn);
+    if (taps > 0)
+        SSU_REQUIRE_PTR(conv_state, io_bytes(d.state_dtype), fn);
+    if (step || !update_state)
+        SSU_REQUIRE_PTR(out, io, fn);
+    SSU_OPTIONAL_PTR(out, io, fn);
+    SSU_OPTIONAL_PTR(context_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(state_indices, 4, fn);
+    if (!step && out == x)
+        return fail(SSU_EINVAL, "%s: out must not overlap x", fn);
+    p.x = x;
+    p.weight = weight;
+    p.bias = bias;
+    p.state = conv_state;
+    p.out = out;
+    p.ctx = context_lengths;
+    p.idx = state_indices;
+    p.batch = d.batch;
+    p.channels = d.channels;
+    p.width = d.width;
+    p.seq_len = seq_len;
+    p.io_dtype = d.io_dtype;
+    p.weight_dtype = d.weight_dtype;
+    p.state_dtype = d.state_dtype;
+    p.silu = silu ? 1 : 0;
+    p.update = update_state ? 1 : 0;
+    return hip_status(ssu::launch_conv(p, stream), fn);
+}
+
+ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len, const void *x,
+                     const float *A, const void *B, const void *C, const void *dt,
+                     const float *dt_bias, const float *D, const void *z, void *state, void *out,
+                     int32_t dt_softplus, int32_t update_state, const int32_t *context_lengths,
+                     const int32_t *state_indices, bool step, hipStream_t stream)
+{
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_scan_dims &d = *dims;
+    if (d.reserved != 0)
+        return fail(SSU_EINVAL, "%s: dims.reserved must be 0", fn);
+    if (d.batch < 0 || seq_len < 0)
+        return fail(SSU_EINVAL, "%s: batch %d and seq_len %d must be >= 0", fn, d.batch, seq_len);
+    if (d.dim <= 0 || d.dstate <= 0 || d.ngroups <= 0 || d.pool_rows <= 0)
+        return fail(SSU_EINVAL, "%s: dim/dstate/ngroups/pool_rows must be > 0 (got %d/%d/%d/%d)",
+                    fn, d.dim, d.dstate, d.ngroups, d.pool_rows);
+    if (d.dim % d.ngroups != 0)
+        return fail(SSU_EINVAL, "%s: dim %d is not a multiple of ngroups %d", fn, d.dim, d.ngroups);
+    if (d.dstate % 4 != 0 || d.dstate > 256)
+        return fail(SSU_ENOTSUP, "%s: dstate %d is not a multiple of 4 in [4, 256]", fn, d.dstate);
+    if (!compute_dtype(d.state_dtype) || !compute_dtype(d.io_dtype) ||
+        !compute_dtype(d.dt_dtype) || !compute_dtype(d.bc_dtype))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype (state %d, io %d, dt %d, bc %d)", fn,
+                    d.state_dtype, d.io_dtype, d.dt_dtype, d.bc_dtype);
+    if (!state_indices && d.batch > d.pool_rows)
+        return fail(SSU_EINVAL, "%s: batch %d > pool_rows %d with no state_indices", fn, d.batch,
+                    d.pool_rows);
+    ssu::ScanParams p = {};
+    const int64_t tile = (int64_t)d.dim * d.dstate;
+    p.row_stride = d.state_row_stride ? d.state_row_stride : tile;
+    if (p.row_stride < tile)
+        return fail(SSU_EINVAL, "%s: state_row_stride %lld < dim*dstate %lld", fn,
+                    (long long)d.state_row_stride, (long long)tile);
+    if (p.row_stride % 4 != 0)
+        return fail(SSU_EINVAL, "%s: state_row_stride %lld is not a multiple of 4", fn,
+                    (long long)p.row_stride);
+    const int64_t gn = (int64_t)d.ngroups * d.dstate;
+    struct { const char *name; int64_t bs, ts, row; int64_t *obs, *ots; } const views[] = {
+        {"x", d.x_batch_stride, d.x_token_stride, d.dim, &p.x_bs, &p.x_ts},
+        {"z", d.z_batch_stride, d.z_token_stride, d.dim, &p.z_bs, &p.z_ts},
+        {"out", d.out_batch_stride, d.out_token_stride, d.dim, &p.out_bs, &p.out_ts},
+        {"dt", d.dt_batch_stride, d.dt_token_stride, d.dim, &p.dt_bs, &p.dt_ts},
+        {"B", d.b_batch_stride, d.b_token_stride, gn, &p.b_bs, &p.b_ts},
+        {"C", d.c_batch_stride, d.c_token_stride, gn, &p.c_bs, &p.c_ts},
+    };
+    for (const auto &v : views) {
+        const ssu_status st = check_strides(fn, v.name, v.bs, step ? 0 : v.ts, v.row, seq_len,
+                                            v.obs, v.ots);
+        if (st != SSU_OK)
+            return st;
+    }
+    if ((int64_t)d.batch * d.dim > 0x7fffffff)
+        return fail(SSU_ENOTSUP, "%s: batch * dim too large", fn);
+    if (d.batch == 0 || seq_len == 0)
+        return ok();
+    const size_t io = io_bytes(d.io_dtype);
+    SSU_REQUIRE_PTR(x, io, fn);
+    SSU_REQUIRE_PTR(A, 16, fn);
+    SSU_REQUIRE_PTR(B, io_bytes(d.bc_dtype), fn);
+    if (step || !update_state)
+        SSU_REQUIRE_PTR(out, io, fn);
+    SSU_OPTIONAL_PTR(out, io, fn);
+    if (out)
+        SSU_REQUIRE_PTR(C, io_bytes(d.bc_dtype), fn);
+    SSU_REQUIRE_PTR(dt, io_bytes(d.dt_dtype), fn);
+    SSU_REQUIRE_PTR(state, 4 * dtype_bytes(d.state_dtype), fn);
+    SSU_OPTIONAL_PTR(dt_bias, 4, fn);
+    SSU_OPTIONAL_PTR(D, 4, fn);
+    SSU_OPTIONAL_PTR(z, io, fn);
+    SSU_OPTIONAL_PTR(context_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(state_indices, 4, fn);
+    if (!step && out && (out == x || out == z || out == dt || out == B || out == C))
+        return fail(SSU_EINVAL, "%s: out must not overlap an input", fn);
+    p.x = x;
+    p.A = A;
+    p.B = B;
+    p.C = C;
+    p.dt = dt;
+    p.dt_bias = dt_bias;
+    p.D = D;
+    p.z = z;
+    p.state = state;
+    p.out = out;
+    p.ctx = context_lengths;
+    p.idx = state_indices;
+    p.batch = d.batch;
+    p.dim = d.dim;
+    p.dstate = d.dstate;
+    p.ngroups = d.ngroups;
+    p.seq_len = seq_len;
+    p.state_dtype = d.state_dtype;
+    p.io_dtype = d.io_dtype;
+    p.dt_dtype = d.dt_dtype;
+    p.bc_dtype = d.bc_dtype;
+    p.dt_softplus = dt_softplus ? 1 : 0;
+    p.update = update_state ? 1 : 0;
+    p.cu_count = current_cu_count();
+    return hip_status(ssu::launch_scan(p, stream), fn);
+}
+
+}  // namespace
+
+ssu_status ssu_conv_prefill(const ssu_conv_dims *dims, int32_t seq_len, const void *x,
+                            const void *weight, const void *bias, void *conv_state, void *out,
+                            int32_t silu, int32_t update_state, const int32_t *context_lengths,
+                            const int32_t *state_indices, hipStream_t stream)
+{
+    return conv_call("ssu_conv_prefill", dims, seq_len, x, weight, bias, conv_state, out, silu,
+                     update_state, context_lengths, state_indices, false, stream);
+}
+
+ssu_status ssu_conv_decode(const ssu_conv_dims *dims, const void *x, const void *weight,
+                           const void *bias, void *conv_state, void *out, int32_t silu,
+                           const int32_t *state_indices, hipStream_t stream)
+{
+    return conv_call("ssu_conv_decode", dims, 1, x, weight, bias, conv_state, out, silu, 1,
+                     nullptr, state_indices, true, stream);
+}
+
+ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float *A,
+                           const void *B, const void *C, const void *dt, const float *dt_bias,
+                           const float *D, const void *z, void *state, void *out,
+                           int32_t dt_softplus, const int32_t *state_indices,
+                           hipStream_t stream)
+{
+    return scan_call("ssu_scan_decode", dims, 1, x, A, B, C, dt, dt_bias, D, z, state, out,
+                     dt_softplus, 1, nullptr, state_indices, true, stream);
+}
+
+ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const void *x,
+                            const float *A, const void *B, const void *C, const void *dt,
+                            const float *dt_bias, const float *D, const void *z, void *state,
+                            void *out, int32_t dt_softplus, int32_t update_state,
+                            const int32_t *context_lengths, const int32_t *state_indices,
+                            hipStream_t stream)
+{
+    return scan_call("ssu_scan_prefill", dims, seq_len, x, A, B, C, dt, dt_bias, D, z, state, out,
+                     dt_softplus, update_state, context_lengths, state_indices, false, stream);
+}
+
+int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims)
+{
+    if (!dims || dims->batch < 0 || dims->vocab < 1 || dims->vocab > (1 << 24))
+        return -1;
+    const int64_t chunks = ((int64_t)dims->vocab + ssu::kVerifyChunk - 1) / ssu::kVerifyChunk;
+    return 8 * (int64_t)dims->batch * (chunks + 1);
+}
+
+ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
+                            const void *target_probs, const void *draft_probs,
+                            const float *uniforms, const int32_t *parent_ids,
+                            const int32_t *context_lengths, const int32_t *state_indices,
+                            int32_t *accepted_lengths, int32_t *accepted_node_ids,
+                            int32_t *next_tokens, void *workspace, int64_t workspace_bytes,
+                            hipStream_t stream)
+{
+    const char *fn = "ssu_draft_verify";
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_verify_dims &d = *dims;
+    if (d.reserved != 0)
+        return fail(SSU_EINVAL, "%s: dims.reserved must be 0", fn);
+    if (d.batch < 0 || d.batch > 65535)
+        return fail(SSU_EINVAL, "%s: batch %d outside [0, 65535]", fn, d.batch);
+    if (d.num_tokens < 1 || d.num_tokens > SSU_MAX_TREE_NODES)
+        return fail(SSU_EINVAL, "%s: num_tokens %d outside [1, %d]", fn, d.num_tokens,
+                    SSU_MAX_TREE_NODES);
+    if (d.vocab < 1 || d.vocab > (1 << 24))
+        return fail(SSU_EINVAL, "%s: vocab %d outside [1, 2^24]", fn, d.vocab);
+    if (!compute_dtype(d.prob_dtype))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype %d", fn, d.prob_dtype);
+    if (draft_probs && parent_ids)
+        return fail(SSU_ENOTSUP, "%s: draft_probs and parent_ids exclude each other", fn);
+    if (accepted_node_ids && d.max_accept_len < 1)
+        return fail(SSU_EINVAL, "%s: max_accept_len %d < 1 with accepted_node_ids", fn,
+                    d.max_accept_len);
+    ssu::VerifyParams p = {};
+    ssu_status st = check_strides(fn, "target_probs", d.target_batch_stride, d.target_row_stride,
+                                  d.vocab, d.num_tokens, &p.t_bs, &p.t_rs);
+    if (st != SSU_OK)
+        return st;
+    st = check_strides(fn, "draft_probs", d.draft_batch_stride, d.draft_row_stride, d.vocab,
+                       d.num_tokens - 1, &p.d_bs, &p.d_rs);
+    if (st != SSU_OK)
+        return st;
+    if (d.batch == 0)
+        return ok();
+    const size_t es = io_bytes(d.prob_dtype);
+    SSU_REQUIRE_PTR(tokens, 4, fn);
+    SSU_REQUIRE_PTR(target_probs, es, fn);
+    SSU_OPTIONAL_PTR(draft_probs, es, fn);
+    SSU_REQUIRE_PTR(uniforms, 4, fn);
+    SSU_OPTIONAL_PTR(parent_ids, 4, fn);
+    SSU_OPTIONAL_PTR(context_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(state_indices, 4, fn);
+    SSU_REQUIRE_PTR(accepted_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(accepted_node_ids, 4, fn);
+    SSU_REQUIRE_PTR(next_tokens, 4, fn);
+    SSU_REQUIRE_PTR(workspace, 16, fn);
+    const int64_t need = ssu_verify_workspace_bytes(dims);
+    if (workspace_bytes < need)
+        return fail(SSU_EINVAL, "%s: workspace_bytes %lld < %lld required", fn,
+                    (long long)workspace_bytes, (long long)need);
+    p.tokens = tokens;
+    p.target = target_probs;
+    p.draft = draft_probs;
+    p.uniforms = uniforms;
+    p.parents = parent_ids;
+    p.ctx = context_lengths;
+    p.idx = state_indices;
+    p.accepted = accepted_lengths;
+    p.path = accepted_node_ids;
+    p.next = next_tokens;
+    p.partial = static_cast<double *>(workspace);
+    p.batch = d.batch;
+    p.num_tokens = d.num_tokens;
+    p.vocab = d.vocab;
+    p.max_accept = accepted_node_ids ? d.max_accept_len : d.num_tokens;
+    p.prob_dtype = d.prob_dtype;
+    return hip_status(ssu::launch_verify(p, stream), fn);
+}
+
+namespace {
+
 ssu_status check_rows(const char *fn, int32_t rows, int64_t stride, int64_t row_bytes,
                       int32_t batch, int64_t *eff_stride)
 {

@@ -101,6 +101,52 @@ struct GdnParams {
 int64_t gdn_workspace_floats(int64_t batch, int64_t hidden, int64_t hq, int64_t hv, int64_t d);
 hipError_t launch_gdn(const GdnParams &p, hipStream_t stream);
 
+// Causal convolution over seq_len tokens (1 for a single token). Strides in
+// elements, all filled in.
+struct ConvParams {
+    const void *x, *weight, *bias;
+    void *state, *out;  // out null: only the state is updated
+    const int32_t *ctx, *idx;
+    int64_t x_bs, x_ts, out_bs, out_ts;
+    int64_t st_row, st_chan, st_tap;
+    int32_t batch, channels, width, seq_len;
+    int32_t io_dtype, weight_dtype, state_dtype;
+    int32_t silu, update;
+};
+hipError_t launch_conv(const ConvParams &p, hipStream_t stream);
+
+// Per-channel selective scan over seq_len tokens (1 for a single token).
+struct ScanParams {
+    const void *x;
+    const float *A;
+    const void *B, *C, *dt;
+    const float *dt_bias, *D;
+    const void *z;
+    void *state, *out;  // out null: only the state is updated
+    const int32_t *ctx, *idx;
+    int64_t row_stride;
+    int64_t x_bs, x_ts, z_bs, z_ts, out_bs, out_ts, dt_bs, dt_ts, b_bs, b_ts, c_bs, c_ts;
+    int32_t batch, dim, dstate, ngroups, seq_len;
+    int32_t state_dtype, io_dtype, dt_dtype, bc_dtype;
+    int32_t dt_softplus, update;
+    int32_t cu_count;  // compute units of the device
+};
+hipError_t launch_scan(const ScanParams &p, hipStream_t stream);
+
+// Verification of drafted tokens.
+constexpr int kVerifyChunk = 2048;  // vocabulary entries per partial sum
+struct VerifyParams {
+    const int32_t *tokens;
+    const void *target, *draft;
+    const float *uniforms;
+    const int32_t *parents, *ctx, *idx;
+    int32_t *accepted, *path, *next;
+    double *partial;  // [batch][chunks + 1]: weight sums per chunk
+    int64_t t_bs, t_rs, d_bs, d_rs;
+    int32_t batch, num_tokens, vocab, max_accept, prob_dtype;
+};
+hipError_t launch_verify(const VerifyParams &p, hipStream_t stream);
+
 // One set of row moves: for b < rows, dst row (dst_idx ? dst_idx[b] : b) gets
 // src row (src_idx ? src_idx[b] : b); a negative destination index skips the
 // row, a negative source index (or src == null) writes zeros; with skip_same,

@@ -7,6 +7,7 @@ kernels of libssu.so; there is no fallback. If the library has not been built
 the first call raises RuntimeError (build it with
 `python -m linear_rnn_recurrent_amd.build`).
 """
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -23,7 +24,8 @@ _DT = {torch.float32: SSU_F32, torch.float16: SSU_F16, torch.bfloat16: SSU_BF16,
 EXPORTS = ("ssu_decode", "ssu_prefill", "ssu_replay", "ssu_tree_verify",
            "ssu_tree_verify_noalloc", "ssu_replay_layers",
            "ssu_state_clear_layers", "ssu_state_gather", "ssu_state_scatter", "ssu_state_pack",
-           "ssu_state_unpack", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
+           "ssu_state_unpack", "ssu_conv_prefill", "ssu_conv_decode", "ssu_scan_prefill",
+           "ssu_scan_decode", "ssu_draft_verify", "ssu_verify_workspace_bytes", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
            "ssu_pool_bytes_per_slot", "ssu_pool_slab_bytes", "ssu_pool_spec", "ssu_pool_specs",
            "ssu_pool_name", "ssu_pool_owns_memory",
            "ssu_pool_alloc", "ssu_pool_free", "ssu_pool_info", "ssu_pool_state_ptr",
@@ -63,6 +65,36 @@ class ssu_gdn_dims(ctypes.Structure):
                 ("pool_rows", ctypes.c_int32), ("use_qk_l2norm", ctypes.c_int32),
                 ("ssm_row_stride", ctypes.c_int64), ("conv_slot_stride", ctypes.c_int64),
                 ("conv_chan_stride", ctypes.c_int64), ("conv_tap_stride", ctypes.c_int64)]
+
+
+class ssu_conv_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "channels", "width", "pool_rows",
+                                               "io_dtype", "weight_dtype", "state_dtype",
+                                               "reserved")]
+                + [(n, ctypes.c_int64) for n in ("x_batch_stride", "x_token_stride",
+                                                 "out_batch_stride", "out_token_stride",
+                                                 "state_row_stride", "state_chan_stride",
+                                                 "state_tap_stride")])
+
+
+class ssu_scan_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "dim", "dstate", "ngroups", "pool_rows",
+                                               "state_dtype", "io_dtype", "dt_dtype", "bc_dtype",
+                                               "reserved")]
+                + [(n, ctypes.c_int64) for n in ("state_row_stride",
+                                                 "x_batch_stride", "x_token_stride",
+                                                 "z_batch_stride", "z_token_stride",
+                                                 "out_batch_stride", "out_token_stride",
+                                                 "dt_batch_stride", "dt_token_stride",
+                                                 "b_batch_stride", "b_token_stride",
+                                                 "c_batch_stride", "c_token_stride")])
+
+
+class ssu_verify_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_tokens", "vocab", "max_accept_len",
+                                               "prob_dtype", "reserved")]
+                + [(n, ctypes.c_int64) for n in ("target_batch_stride", "target_row_stride",
+                                                 "draft_batch_stride", "draft_row_stride")])
 
 
 class ssu_state_spec(ctypes.Structure):
@@ -105,6 +137,15 @@ def load_library(path: Optional[str] = None):
         "ssu_state_pack": [_P, _I32, ctypes.c_int64, ctypes.c_int64, _P, _I32, _P, _I32, _P, _P],
         "ssu_gdn_decode": [ctypes.POINTER(ssu_gdn_dims), _P, _P, _P, _P, _P, _P, _P, _P,
                            ctypes.c_float, _P, _P, _P, _P, ctypes.c_int64, _P],
+        "ssu_conv_prefill": [ctypes.POINTER(ssu_conv_dims), _I32, _P, _P, _P, _P, _P, _I32, _I32,
+                             _P, _P, _P],
+        "ssu_conv_decode": [ctypes.POINTER(ssu_conv_dims), _P, _P, _P, _P, _P, _I32, _P, _P],
+        "ssu_scan_prefill": [ctypes.POINTER(ssu_scan_dims), _I32, _P, _P, _P, _P, _P, _P, _P, _P,
+                             _P, _P, _I32, _I32, _P, _P, _P],
+        "ssu_scan_decode": [ctypes.POINTER(ssu_scan_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                            _I32, _P, _P],
+        "ssu_draft_verify": [ctypes.POINTER(ssu_verify_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                             _P, _P, ctypes.c_int64, _P],
         "ssu_state_unpack": [_P, _I32, ctypes.c_int64, ctypes.c_int64, _P, _I32, _P, _I32, _P, _P],
         "ssu_pool_bytes_per_slot": [S, _I32, ctypes.POINTER(ctypes.c_size_t)],
         "ssu_pool_slab_bytes": [S, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)],
@@ -135,6 +176,8 @@ def load_library(path: Optional[str] = None):
     lib.ssu_tree_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_gdn_workspace_bytes.argtypes = [ctypes.POINTER(ssu_gdn_dims)]
     lib.ssu_gdn_workspace_bytes.restype = ctypes.c_int64
+    lib.ssu_verify_workspace_bytes.argtypes = [ctypes.POINTER(ssu_verify_dims)]
+    lib.ssu_verify_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_last_error.argtypes = []
     lib.ssu_last_error.restype = ctypes.c_char_p
     lib.ssu_version.argtypes = []
@@ -654,6 +697,255 @@ def gdn_workspace_bytes(batch, hidden, num_q_heads, num_v_heads, head_dim):
     """Bytes of the workspace ssu_gdn_decode needs (no GPU needed)."""
     d = ssu_gdn_dims(batch, hidden, num_q_heads, num_v_heads, head_dim, 1, 1, 1, 0, 0, 0, 0)
     return int(load_library().ssu_gdn_workspace_bytes(ctypes.byref(d)))
+
+
+# ---------------------------------------------------------------------------
+# Per-channel scan, causal convolution, draft verification
+# ---------------------------------------------------------------------------
+def _activation(t, name, dtype, shape):
+    """Shape, type and strides of an activation [batch, (tokens,) *row]: rows
+    dense, batch and token strides free. Returns (batch stride, token stride),
+    0 where the axis has one entry."""
+    _need(t.is_cuda, f"{name} must be a GPU tensor")
+    _need(t.dtype is dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
+    _need(t.shape == shape, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.stride()
+
+
+def _outer(stride, shape, name, step):
+    """(batch stride, token stride) of an activation for the C call."""
+    n = 1 if step else 2
+    bs, ts = stride[0], 0 if step else stride[1]
+    width = 1
+    for k in range(len(shape) - 1, n - 1, -1):
+        _need(stride[k] == width or shape[k] <= 1, f"{name} must be dense in its last axes")
+        width *= shape[k]
+    if shape[0] <= 1:
+        bs = 0
+    else:
+        _need(bs > 0, f"{name} must not be broadcast over the batch")
+    if not step:
+        if shape[1] <= 1:
+            ts = 0
+        else:
+            _need(ts > 0, f"{name} must not be broadcast over the tokens")
+            if not bs:  # one row: the C side derives the batch stride
+                return 0, ts
+    return bs, ts
+
+
+def _on(device):
+    """A context with `device` current; none where it is already."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
+               state_indices, stream, step):
+    lib = load_library()
+    _need(x.dtype in _DT and x.dim() == (2 if step else 3),
+          "x must be [batch, channels]" if step else "x must be [batch, seq_len, channels]")
+    shape = x.shape
+    batch, channels = shape[0], shape[-1]
+    xs = _outer(_activation(x, "x", x.dtype, shape), shape, "x", step)
+    os_ = (0, 0)
+    if out is not None:
+        os_ = _outer(_activation(out, "out", x.dtype, shape), shape, "out", step)
+    _dense(weight, "weight", _FLOAT)
+    _need(weight.dim() == 2 and weight.shape[0] == channels, "weight must be [channels, width]")
+    width = weight.shape[1]
+    if bias is not None:
+        _dense(bias, "bias", (weight.dtype,), (channels,))
+    rows, sdt, ss = batch, x.dtype, (0, 0, 0)
+    if conv_state is not None:
+        _dev(conv_state, "conv_state", _FLOAT)
+        _need(conv_state.dim() == 3 and tuple(conv_state.shape[1:]) == (channels, width - 1),
+              "conv_state must be a [rows, channels, width-1] view")
+        rows, sdt, ss = conv_state.shape[0], conv_state.dtype, conv_state.stride()
+    else:
+        _need(width == 1, "conv_state is required")
+    _opt_idx(state_indices, "state_indices", batch)
+    _opt_idx(context_lengths, "context_lengths", batch)
+    d = ssu_conv_dims(batch, channels, width, rows, _DT[x.dtype], _DT[weight.dtype], _DT[sdt], 0,
+                      *xs, *os_, *ss)
+    with _on(x.device):
+        st = _stream(x.device, stream)
+        if step:
+            rc = lib.ssu_conv_decode(d, _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_state),
+                                     _ptr(out), 1 if silu else 0, _ptr(state_indices), st)
+        else:
+            rc = lib.ssu_conv_prefill(d, shape[1], _ptr(x), _ptr(weight), _ptr(bias),
+                                      _ptr(conv_state), _ptr(out), 1 if silu else 0,
+                                      1 if update_state else 0, _ptr(context_lengths),
+                                      _ptr(state_indices), st)
+    _check(rc)
+    return out
+
+
+def ssu_conv_prefill(x, weight, bias, conv_state, out, *, silu=True, context_lengths=None,
+                     state_indices=None, update_state=True, stream=None):
+    """Causal convolution of seq_len tokens, the last width-1 inputs kept in a pool.
+
+    x, out [batch, seq_len, channels] (slices of wider tensors are fine: channels dense,
+    other strides free); weight [channels, width]; bias [channels] or None; conv_state
+    [rows, channels, width-1], any strides, updated in place unless update_state is False;
+    context_lengths, state_indices [batch] int32. out may be None when only the state is
+    wanted (commit of a window: context_lengths = accepted lengths).
+    """
+    return _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
+                      state_indices, stream, False)
+
+
+def ssu_conv_decode(x, weight, bias, conv_state, out, *, silu=True, state_indices=None,
+                    stream=None):
+    """The causal convolution of one token: x, out [batch, channels]; the rest as
+    ssu_conv_prefill. out may be x."""
+    return _conv_call(x, weight, bias, conv_state, out, silu, True, None, state_indices, stream,
+                      True)
+
+
+def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
+               context_lengths, state_indices, stream, step):
+    lib = load_library()
+    _need(x.dtype in _DT and x.dim() == (2 if step else 3),
+          "x must be [batch, dim]" if step else "x must be [batch, seq_len, dim]")
+    shape = x.shape
+    batch, dim = shape[0], shape[-1]
+    lead = shape[:-1]
+    xs = _outer(_activation(x, "x", x.dtype, shape), shape, "x", step)
+    _need(dt.dtype in _DT, f"dt has dtype {dt.dtype}")
+    ds = _outer(_activation(dt, "dt", dt.dtype, shape), shape, "dt", step)
+    _need(B.dtype in _DT and B.dim() == len(shape) + 1 and B.shape[:-2] == lead,
+          "B must be [batch, ngroups, dstate]" if step else
+          "B must be [batch, seq_len, ngroups, dstate]")
+    ngroups, dstate = B.shape[-2], B.shape[-1]
+    bs = _outer(_activation(B, "B", B.dtype, B.shape), B.shape, "B", step)
+    cs = zs = os_ = (0, 0)
+    if C is not None:
+        cs = _outer(_activation(C, "C", B.dtype, B.shape), B.shape, "C", step)
+    if z is not None:
+        zs = _outer(_activation(z, "z", x.dtype, shape), shape, "z", step)
+    if out is not None:
+        _need(C is not None, "C is required")
+        os_ = _outer(_activation(out, "out", x.dtype, shape), shape, "out", step)
+    f32 = (torch.float32,)
+    _dense(A, "A", f32, (dim, dstate))
+    if dt_bias is not None:
+        _dense(dt_bias, "dt_bias", f32, (dim,))
+    if D is not None:
+        _dense(D, "D", f32, (dim,))
+    _dev(state, "state", _FLOAT)
+    st = state.stride()
+    _need(state.dim() == 3 and state.shape[1] == dim and state.shape[2] == dstate,
+          f"state has shape {tuple(state.shape)}, expected [rows, {dim}, {dstate}]")
+    _need((st[2] == 1 or dstate == 1) and (st[1] == dstate or dim == 1),
+          "state rows must be dense ([dim, dstate] contiguous)")
+    _need(st[0] >= dim * dstate or state.shape[0] == 1, "state row stride too small")
+    row = st[0] if state.shape[0] > 1 else dim * dstate
+    _opt_idx(state_indices, "state_indices", batch)
+    _opt_idx(context_lengths, "context_lengths", batch)
+    d = ssu_scan_dims(batch, dim, dstate, ngroups, state.shape[0], _DT[state.dtype],
+                      _DT[x.dtype], _DT[dt.dtype], _DT[B.dtype], 0, row, *xs, *zs, *os_, *ds, *bs,
+                      *cs)
+    with _on(x.device):
+        sm = _stream(x.device, stream)
+        if step:
+            rc = lib.ssu_scan_decode(d, _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(dt),
+                                     _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
+                                     1 if dt_softplus else 0, _ptr(state_indices), sm)
+        else:
+            rc = lib.ssu_scan_prefill(d, shape[1], _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(dt),
+                                      _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
+                                      1 if dt_softplus else 0, 1 if update_state else 0,
+                                      _ptr(context_lengths), _ptr(state_indices), sm)
+    _check(rc)
+    return out
+
+
+def ssu_scan_prefill(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
+                     dt_softplus=True, context_lengths=None, state_indices=None,
+                     update_state=True, stream=None):
+    """Per-channel selective scan of seq_len tokens.
+
+    x, z, out, dt [batch, seq_len, dim]; B, C [batch, seq_len, ngroups, dstate] (slices of
+    wider tensors are fine: a token's entries dense, other strides free); A [dim, dstate],
+    dt_bias, D [dim] fp32; state [rows, dim, dstate], updated in place unless update_state is
+    False; context_lengths, state_indices [batch] int32. out (and C) may be None when only
+    the state is wanted (commit of a window: context_lengths = accepted lengths).
+    """
+    return _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
+                      context_lengths, state_indices, stream, False)
+
+
+def ssu_scan_decode(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
+                    dt_softplus=True, state_indices=None, stream=None):
+    """One token of the per-channel selective scan: x, z, out, dt [batch, dim]; B, C
+    [batch, ngroups, dstate]; the rest as ssu_scan_prefill. out may be x or z."""
+    return _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, True, None,
+                      state_indices, stream, True)
+
+
+def verify_workspace_bytes(batch, vocab):
+    """Bytes of the workspace ssu_draft_verify needs (no GPU needed)."""
+    d = ssu_verify_dims(batch, 1, vocab, 0, 0, 0, 0, 0, 0, 0)
+    return int(load_library().ssu_verify_workspace_bytes(ctypes.byref(d)))
+
+
+def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_tokens, *,
+                     draft_probs=None, parent_ids=None, context_lengths=None, state_indices=None,
+                     accepted_node_ids=None, workspace=None, stream=None):
+    """Which drafted tokens of a verify window stand, and the token drawn after them.
+
+    tokens [batch, num_tokens] int32 (entry 0 certain, the others drafted); target_probs
+    [batch, num_tokens, vocab]; uniforms [batch, num_tokens] fp32 in [0, 1) (entry 0 draws the
+    next token); draft_probs [batch, num_tokens-1, vocab] (a chain drawn from them), or
+    parent_ids [batch, num_tokens] int32 (a draft tree), or neither (a given chain).
+    accepted_lengths, next_tokens [batch] int32 and accepted_node_ids [batch, max_accept_len]
+    int32 are written: ssu_replay takes the lengths and node ids, the prefill calls take the
+    lengths as context_lengths. workspace: a uint8 GPU tensor of at least
+    verify_workspace_bytes(batch, vocab) bytes (allocated here when None).
+    """
+    lib = load_library()
+    i32 = (torch.int32,)
+    _dense(tokens, "tokens", i32)
+    _need(tokens.dim() == 2, "tokens must be [batch, num_tokens]")
+    batch, n = tokens.shape
+    _dev(target_probs, "target_probs", _FLOAT)
+    _need(target_probs.dim() == 3 and tuple(target_probs.shape[:2]) == (batch, n),
+          "target_probs must be [batch, num_tokens, vocab]")
+    vocab = target_probs.shape[2]
+    ts = _outer(target_probs.stride(), target_probs.shape, "target_probs", False)
+    ds = (0, 0)
+    if draft_probs is not None:
+        _dev(draft_probs, "draft_probs", (target_probs.dtype,), (batch, n - 1, vocab))
+        ds = _outer(draft_probs.stride(), draft_probs.shape, "draft_probs", False)
+    _dense(uniforms, "uniforms", (torch.float32,), (batch, n))
+    if parent_ids is not None:
+        _dense(parent_ids, "parent_ids", i32, (batch, n))
+    _opt_idx(context_lengths, "context_lengths", batch)
+    _opt_idx(state_indices, "state_indices", batch)
+    _dense(accepted_lengths, "accepted_lengths", i32, (batch,))
+    _dense(next_tokens, "next_tokens", i32, (batch,))
+    most = 0
+    if accepted_node_ids is not None:
+        _dense(accepted_node_ids, "accepted_node_ids", i32)
+        _need(accepted_node_ids.dim() == 2 and accepted_node_ids.shape[0] == batch,
+              "accepted_node_ids must be [batch, max_accept_len]")
+        most = accepted_node_ids.shape[1]
+    d = ssu_verify_dims(batch, n, vocab, most, _DT[target_probs.dtype], 0, *ts, *ds)
+    device = tokens.device
+    if workspace is None:
+        need = int(lib.ssu_verify_workspace_bytes(d))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _dense(workspace, "workspace", (torch.uint8,))
+    with _on(device):
+        _check(lib.ssu_draft_verify(d, _ptr(tokens), _ptr(target_probs), _ptr(draft_probs),
+                                    _ptr(uniforms), _ptr(parent_ids), _ptr(context_lengths),
+                                    _ptr(state_indices), _ptr(accepted_lengths),
+                                    _ptr(accepted_node_ids), _ptr(next_tokens), _ptr(workspace),
+                                    workspace.numel(), _stream(device, stream)))
+    return accepted_lengths, next_tokens
 
 
 # ---------------------------------------------------------------------------

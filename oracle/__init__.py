@@ -17,6 +17,8 @@ shape list; invokeSelectiveStateUpdatePrefill; MambaReplayLayerInfo):
            invokeMambaStateClear)
   gdn    : the fused gated-delta-rule decode step of FlashInfer's
            gdn_fused_decode_step page (gdn_oracle.c)
+  conv, scan, verify: the causal convolution, the per-channel scan and draft
+           verification (sequence.py)
   state  : [rows, h, d, n], or a flat buffer with `row_stride` elements per row
 
 `state`, `out` and the stash arrays are updated in place.
@@ -27,6 +29,7 @@ import os
 import numpy as np
 
 from . import build as _build
+from .sequence import causal_conv, channel_scan, draft_verify  # noqa: F401
 
 _LIB = None
 _F64P = ctypes.POINTER(ctypes.c_double)
