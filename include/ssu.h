@@ -420,13 +420,23 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
  * NULL when the state is updated (C, D and z are not read then, C may be
  * NULL). out must not overlap an input (equal pointers are refused). Rows with
  * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
- * call and rounded once, at its end. */
+ * call and rounded once, at its end. Long calls run the tokens in chunks side by
+ * side: they agree with the token-by-token recurrence to fp32 rounding, not
+ * bitwise.
+ * workspace: caller-owned device scratch of at least
+ * ssu_scan_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
+ * that is 0); contents on entry ignored, on return unspecified; calls sharing a
+ * workspace must be ordered (one stream). */
 ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const void *x,
                             const float *A, const void *B, const void *C, const void *dt,
                             const float *dt_bias, const float *D, const void *z, void *state,
                             void *out, int32_t dt_softplus, int32_t update_state,
                             const int32_t *context_lengths, const int32_t *state_indices,
-                            hipStream_t stream);
+                            void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace ssu_scan_prefill needs for these dims and seq_len (0 for a
+ * few tokens); -1 if dims is NULL or a size is out of range. No HIP call. */
+int64_t ssu_scan_workspace_bytes(const ssu_scan_dims *dims, int32_t seq_len);
 
 /* ------------------------------------------------------------------------
  * Verification of drafted tokens

@@ -12,7 +12,7 @@ from .ssu import (SsuError, SsuPool, DeviceArray, ReplayLayerTable, StateLayerTa
                   ssu_replay_layers, ssu_state_clear_layers, ssu_state_gather,
                   ssu_state_scatter, ssu_state_pack, ssu_state_unpack, pack_workspace_bytes,
                   ssu_conv_prefill, ssu_conv_decode, ssu_scan_prefill, ssu_scan_decode,
-                  ssu_draft_verify, verify_workspace_bytes,
+                  ssu_draft_verify, scan_workspace_bytes, verify_workspace_bytes,
                   ssu_gdn_decode, gdn_workspace_bytes, tree_workspace_bytes,
                   LIB_PATH, EXPORTS)
 
@@ -22,5 +22,5 @@ __all__ = ["SsuError", "SsuPool", "DeviceArray", "ReplayLayerTable", "StateLayer
            "ssu_replay_layers", "ssu_state_clear_layers", "ssu_state_gather", "ssu_state_scatter",
            "ssu_state_pack", "ssu_state_unpack", "pack_workspace_bytes", "ssu_gdn_decode", "gdn_workspace_bytes",
            "ssu_conv_prefill", "ssu_conv_decode", "ssu_scan_prefill", "ssu_scan_decode",
-           "ssu_draft_verify", "verify_workspace_bytes", "tree_workspace_bytes",
+           "ssu_draft_verify", "scan_workspace_bytes", "verify_workspace_bytes", "tree_workspace_bytes",
            "LIB_PATH", "EXPORTS"]

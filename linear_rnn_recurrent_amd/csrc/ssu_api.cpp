@@ -587,7 +587,8 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
                      const float *A, const void *B, const void *C, const void *dt,
                      const float *dt_bias, const float *D, const void *z, void *state, void *out,
                      int32_t dt_softplus, int32_t update_state, const int32_t *context_lengths,
-                     const int32_t *state_indices, bool step, hipStream_t stream)
+                     const int32_t *state_indices, void *workspace, int64_t workspace_bytes,
+                     bool step, hipStream_t stream)
 {
     if (!dims)
         return fail(SSU_EINVAL, "%s: dims is NULL", fn);
@@ -656,6 +657,15 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
     SSU_OPTIONAL_PTR(state_indices, 4, fn);
     if (!step && out && (out == x || out == z || out == dt || out == B || out == C))
         return fail(SSU_EINVAL, "%s: out must not overlap an input", fn);
+    if (!step) {
+        const int64_t need = ssu_scan_workspace_bytes(dims, seq_len);
+        if (need > 0)
+            SSU_REQUIRE_PTR(workspace, 16, fn);
+        if (workspace_bytes < need)
+            return fail(SSU_EINVAL, "%s: workspace_bytes %lld < %lld required", fn,
+                        (long long)workspace_bytes, (long long)need);
+        p.workspace = static_cast<float *>(workspace);
+    }
     p.x = x;
     p.A = A;
     p.B = B;
@@ -679,7 +689,6 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
     p.bc_dtype = d.bc_dtype;
     p.dt_softplus = dt_softplus ? 1 : 0;
     p.update = update_state ? 1 : 0;
-    p.cu_count = current_cu_count();
     return hip_status(ssu::launch_scan(p, stream), fn);
 }
 
@@ -709,7 +718,7 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
                            hipStream_t stream)
 {
     return scan_call("ssu_scan_decode", dims, 1, x, A, B, C, dt, dt_bias, D, z, state, out,
-                     dt_softplus, 1, nullptr, state_indices, true, stream);
+                     dt_softplus, 1, nullptr, state_indices, nullptr, 0, true, stream);
 }
 
 ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const void *x,
@@ -717,10 +726,20 @@ ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const vo
                             const float *dt_bias, const float *D, const void *z, void *state,
                             void *out, int32_t dt_softplus, int32_t update_state,
                             const int32_t *context_lengths, const int32_t *state_indices,
-                            hipStream_t stream)
+                            void *workspace, int64_t workspace_bytes, hipStream_t stream)
 {
     return scan_call("ssu_scan_prefill", dims, seq_len, x, A, B, C, dt, dt_bias, D, z, state, out,
-                     dt_softplus, update_state, context_lengths, state_indices, false, stream);
+                     dt_softplus, update_state, context_lengths, state_indices, workspace,
+                     workspace_bytes, false, stream);
+}
+
+int64_t ssu_scan_workspace_bytes(const ssu_scan_dims *dims, int32_t seq_len)
+{
+    if (!dims || dims->batch < 0 || dims->dim <= 0 || dims->dstate <= 0 || dims->ngroups <= 0 ||
+        dims->dim % dims->ngroups != 0 || seq_len < 0)
+        return -1;
+    return 4 * ssu::scan_workspace_floats(dims->batch, dims->dim, dims->dstate, dims->ngroups,
+                                          seq_len);
 }
 
 int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims)

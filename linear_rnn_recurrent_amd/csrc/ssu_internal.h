@@ -129,8 +129,10 @@ struct ScanParams {
     int32_t batch, dim, dstate, ngroups, seq_len;
     int32_t state_dtype, io_dtype, dt_dtype, bc_dtype;
     int32_t dt_softplus, update;
-    int32_t cu_count;  // compute units of the device
+    float *workspace;  // scan_workspace_floats() fp32, 16-byte aligned
 };
+int64_t scan_workspace_floats(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups,
+                              int64_t seq_len);
 hipError_t launch_scan(const ScanParams &p, hipStream_t stream);
 
 // Verification of drafted tokens.

@@ -25,7 +25,7 @@ EXPORTS = ("ssu_decode", "ssu_prefill", "ssu_replay", "ssu_tree_verify",
            "ssu_tree_verify_noalloc", "ssu_replay_layers",
            "ssu_state_clear_layers", "ssu_state_gather", "ssu_state_scatter", "ssu_state_pack",
            "ssu_state_unpack", "ssu_conv_prefill", "ssu_conv_decode", "ssu_scan_prefill",
-           "ssu_scan_decode", "ssu_draft_verify", "ssu_verify_workspace_bytes", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
+           "ssu_scan_decode", "ssu_scan_workspace_bytes", "ssu_draft_verify", "ssu_verify_workspace_bytes", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
            "ssu_pool_bytes_per_slot", "ssu_pool_slab_bytes", "ssu_pool_spec", "ssu_pool_specs",
            "ssu_pool_name", "ssu_pool_owns_memory",
            "ssu_pool_alloc", "ssu_pool_free", "ssu_pool_info", "ssu_pool_state_ptr",
@@ -141,7 +141,7 @@ def load_library(path: Optional[str] = None):
                              _P, _P, _P],
         "ssu_conv_decode": [ctypes.POINTER(ssu_conv_dims), _P, _P, _P, _P, _P, _I32, _P, _P],
         "ssu_scan_prefill": [ctypes.POINTER(ssu_scan_dims), _I32, _P, _P, _P, _P, _P, _P, _P, _P,
-                             _P, _P, _I32, _I32, _P, _P, _P],
+                             _P, _P, _I32, _I32, _P, _P, _P, ctypes.c_int64, _P],
         "ssu_scan_decode": [ctypes.POINTER(ssu_scan_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                             _I32, _P, _P],
         "ssu_draft_verify": [ctypes.POINTER(ssu_verify_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -176,6 +176,8 @@ def load_library(path: Optional[str] = None):
     lib.ssu_tree_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_gdn_workspace_bytes.argtypes = [ctypes.POINTER(ssu_gdn_dims)]
     lib.ssu_gdn_workspace_bytes.restype = ctypes.c_int64
+    lib.ssu_scan_workspace_bytes.argtypes = [ctypes.POINTER(ssu_scan_dims), _I32]
+    lib.ssu_scan_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_verify_workspace_bytes.argtypes = [ctypes.POINTER(ssu_verify_dims)]
     lib.ssu_verify_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_last_error.argtypes = []
@@ -806,7 +808,7 @@ def ssu_conv_decode(x, weight, bias, conv_state, out, *, silu=True, state_indice
 
 
 def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
-               context_lengths, state_indices, stream, step):
+               context_lengths, state_indices, workspace, stream, step):
     lib = load_library()
     _need(x.dtype in _DT and x.dim() == (2 if step else 3),
           "x must be [batch, dim]" if step else "x must be [batch, seq_len, dim]")
@@ -855,27 +857,41 @@ def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_st
                                      _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
                                      1 if dt_softplus else 0, _ptr(state_indices), sm)
         else:
+            if workspace is None:
+                need = lib.ssu_scan_workspace_bytes(d, shape[1])
+                if need > 0:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            else:
+                _dense(workspace, "workspace", (torch.uint8,))
             rc = lib.ssu_scan_prefill(d, shape[1], _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(dt),
                                       _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
                                       1 if dt_softplus else 0, 1 if update_state else 0,
-                                      _ptr(context_lengths), _ptr(state_indices), sm)
+                                      _ptr(context_lengths), _ptr(state_indices), _ptr(workspace),
+                                      0 if workspace is None else workspace.numel(), sm)
     _check(rc)
     return out
 
 
 def ssu_scan_prefill(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
                      dt_softplus=True, context_lengths=None, state_indices=None,
-                     update_state=True, stream=None):
+                     update_state=True, workspace=None, stream=None):
     """Per-channel selective scan of seq_len tokens.
 
     x, z, out, dt [batch, seq_len, dim]; B, C [batch, seq_len, ngroups, dstate] (slices of
     wider tensors are fine: a token's entries dense, other strides free); A [dim, dstate],
     dt_bias, D [dim] fp32; state [rows, dim, dstate], updated in place unless update_state is
     False; context_lengths, state_indices [batch] int32. out (and C) may be None when only
-    the state is wanted (commit of a window: context_lengths = accepted lengths).
+    the state is wanted (commit of a window: context_lengths = accepted lengths). workspace: a
+    uint8 GPU tensor of at least scan_workspace_bytes(...) bytes (allocated here when None).
     """
     return _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
-                      context_lengths, state_indices, stream, False)
+                      context_lengths, state_indices, workspace, stream, False)
+
+
+def scan_workspace_bytes(batch, seq_len, dim, dstate, ngroups=1):
+    """Bytes of the workspace ssu_scan_prefill needs (no GPU needed)."""
+    d = ssu_scan_dims(batch, dim, dstate, ngroups)
+    return int(load_library().ssu_scan_workspace_bytes(d, seq_len))
 
 
 def ssu_scan_decode(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
@@ -883,7 +899,7 @@ def ssu_scan_decode(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None,
     """One token of the per-channel selective scan: x, z, out, dt [batch, dim]; B, C
     [batch, ngroups, dstate]; the rest as ssu_scan_prefill. out may be x or z."""
     return _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, True, None,
-                      state_indices, stream, True)
+                      state_indices, None, stream, True)
 
 
 def verify_workspace_bytes(batch, vocab):

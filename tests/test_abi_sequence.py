@@ -103,14 +103,14 @@ def scan_dims(**kw):
     return S.ssu_scan_dims(*d.values())
 
 
-def scan(lib, d, seq_len=8, update=1, step=False, **ptrs):
+def scan(lib, d, seq_len=8, update=1, step=False, ws=FAKE, ws_bytes=1 << 40, **ptrs):
     p = dict(x=FAKE, A=FAKE, B=FAKE, C=FAKE, dt=FAKE, dt_bias=None, D=None, z=None, state=FAKE,
              out=FAKE + 64, ctx=None, idx=None)
     p.update(ptrs)
     head = [p[k] for k in ("x", "A", "B", "C", "dt", "dt_bias", "D", "z", "state", "out")]
     if step:
         return lib.ssu_scan_decode(d, *head, 1, p["idx"], None)
-    return lib.ssu_scan_prefill(d, seq_len, *head, 1, update, p["ctx"], p["idx"], None)
+    return lib.ssu_scan_prefill(d, seq_len, *head, 1, update, p["ctx"], p["idx"], ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,status,needle", [
@@ -143,6 +143,18 @@ def test_scan_pointers(lib):
     assert scan(lib, scan_dims(), seq_len=-1) == 1
     for rc in (scan(lib, scan_dims(batch=0), x=None), scan(lib, scan_dims(), seq_len=0, x=None)):
         assert rc == 0 and err(lib) == ""
+
+
+def test_scan_workspace(lib):
+    d = scan_dims(dim=96, ngroups=2, dstate=40)
+    need = lib.ssu_scan_workspace_bytes(d, 1000)
+    assert need == S.scan_workspace_bytes(2, 1000, 96, 40, 2) > 4 * 2 * 1000 * 2 * 48 * 2
+    assert scan(lib, d, seq_len=1000, ws_bytes=need - 1) == 1 and "workspace_bytes" in err(lib)
+    assert scan(lib, d, seq_len=1000, ws=None) == 1 and "'workspace'" in err(lib)
+    assert scan(lib, d, seq_len=1000, ws=FAKE + 8) == 1 and "'workspace'" in err(lib)
+    assert lib.ssu_scan_workspace_bytes(d, 1) == 0
+    assert lib.ssu_scan_workspace_bytes(None, 1) == -1
+    assert lib.ssu_scan_workspace_bytes(scan_dims(ngroups=3), 100) == -1
 
 
 def verify_dims(**kw):
