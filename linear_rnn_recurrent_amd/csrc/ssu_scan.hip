@@ -20,13 +20,16 @@
 //   pack    B and C of every token in fp32, padded to 16 states (scalar loads)
 //   ends    every chunk's state from a zero start, and its sum of dt'
 //           (the chunk's decay is exp(A sum dt'))
-//   carry   every chunk's start from the ends before it, in order
-//   tokens  every chunk's tokens from its start: the outputs, the last state
-// (a single chunk is pack and tokens; without outputs the carry leaves the
-// last state and the tokens are not run)
+//   tokens  every chunk's start from the pool's state and the ends before it, in
+//           order, then its tokens: the outputs, the last state
+// (a single chunk needs no ends; without outputs a small kernel folds the ends
+// into the last state and the tokens are not run)
 // The chunks' decays are computed twice (11 slots instead of 6), against 1/16
 // of the SIMDs busy without the cut at one sequence of 5,120 channels. dstate
 // above 16 takes ceil(dstate / 16) waves, whose partial outputs meet in LDS.
+#include <atomic>
+#include <type_traits>
+
 #include "ssu_device.h"
 #include "ssu_dpp.h"
 #include "ssu_internal.h"
@@ -36,32 +39,18 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStates = 16;  // state entries of a lane in the chunk kernels
-constexpr int kBatch = 8;    // tokens loaded together
+constexpr int kBatch = 4;    // tokens loaded together
 
-// Elements by size: 4 bytes fp32, 2 bytes bf16 or fp16 (a uniform choice).
-template <int SZ>
-__device__ __forceinline__ uint32_t ld_bits(const void *p, int64_t i)
+// Rounds to nearest even in one instruction (bf16: v_cvt_pk_bf16_f32).
+template <typename T>
+__device__ __forceinline__ void put(void *at, float v)
 {
-    if constexpr (SZ == 4)
-        return static_cast<const uint32_t *>(p)[i];
+    if constexpr (sizeof(T) == 4)
+        *static_cast<float *>(at) = v;
+    else if constexpr (__is_same(T, bf16_t))
+        *static_cast<__bf16 *>(at) = (__bf16)v;
     else
-        return static_cast<const uint16_t *>(p)[i];
-}
-template <int SZ>
-__device__ __forceinline__ float cvt_bits(uint32_t w, bool bf)
-{
-    if constexpr (SZ == 4)
-        return __uint_as_float(w);
-    else
-        return bf ? __uint_as_float(w << 16) : f16_to_f32(w);
-}
-template <int SZ>
-__device__ __forceinline__ void st_bits(void *p, int64_t i, float v, bool bf)
-{
-    if constexpr (SZ == 4)
-        static_cast<float *>(p)[i] = v;
-    else
-        static_cast<uint16_t *>(p)[i] = (uint16_t)(bf ? f32_to_bf16(v) : f32_to_f16(v));
+        *static_cast<_Float16 *>(at) = (_Float16)v;
 }
 
 // v sigmoid(v) on the hardware exp2 and reciprocal (1 ulp each).
@@ -159,27 +148,31 @@ hipError_t launch_scan_lanes(const ScanParams &p, hipStream_t stream)
 // Chunks
 // ---------------------------------------------------------------------------
 // Workspace, in floats: packed B | C [batch][seq_len][ngroups][tiles][2][16],
-// chunk starts [batch][chunks][blocks][tiles][16][64] (slot c + 1 holds chunk
-// c's end until the carry kernel replaces it by chunk c + 1's start), chunk
-// sums of dt' [batch][chunks][blocks][64]. A block is 64 channels of one group.
+// and a line of 32 zeros; chunk ends [batch][chunks + 1][blocks][tiles][16][64]
+// (slot 0 a copy of the pool's state, so that the kernel that writes the pool
+// does not read it; slot c + 1 chunk c's end); chunk sums of dt'
+// [batch][chunks + 1][blocks][64], slot c + 1 likewise. A block is 64 channels
+// of one group.
 struct ChunkShape {
     int32_t tiles, per_group, blocks, chunk, chunks;
+    int32_t team;  // chunks of one block that share a workgroup: 1, 2 or 4
+    int64_t zeros;  // offset of the zero line in bc
     float *bc, *start, *sum;
 };
 
-// The block of channels and the chunk of a workgroup.
+// The block of channels, the batch row and the team of chunks of a workgroup.
 struct Place {
-    int b, c, blk, g, d, dl;  // batch row, chunk, block, group, channel (clamped), its lane is live
+    int b, team, blk, g, d, dl;  // .., group, channel (clamped), whether its lane is live
 };
 
-__device__ __forceinline__ Place place(const ScanParams &p, const ChunkShape &s, int chunks)
+__device__ __forceinline__ Place place(const ScanParams &p, const ChunkShape &s, int teams)
 {
     Place q;
     int i = blockIdx.x;
     q.blk = i % s.blocks;
     i /= s.blocks;
-    q.c = i % chunks;
-    q.b = i / chunks;
+    q.team = i % teams;
+    q.b = i / teams;
     q.g = q.blk / s.per_group;
     const int width = p.dim / p.ngroups;
     const int local = (q.blk - q.g * s.per_group) * 64 + (int)(threadIdx.x & 63);
@@ -193,6 +186,8 @@ __global__ __launch_bounds__(256) void ssu_scan_pack_kernel(const ScanParams p, 
                                                             int64_t total)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (blockIdx.x == 0 && threadIdx.x < 2 * kStates)
+        s.bc[s.zeros + threadIdx.x] = 0.0f;
     if (i >= total)
         return;
     const int n16 = s.tiles * kStates;
@@ -228,87 +223,179 @@ __device__ __forceinline__ void load_a(const ScanParams &p, int d, int tile, flo
     }
 }
 
-// A batch of tokens' inputs as raw bits.
-template <int IOSZ, int DTSZ>
-struct Inputs {
-    uint32_t x[kBatch], dt[kBatch];
-    __device__ __forceinline__ void load(const ScanParams &p, const Place &q, int t0, int t1)
+// One activation [.., seq_len, dim] read a batch of tokens at a time: a scalar
+// base that moves by batches, and a byte offset per token of the batch and lane,
+// so that a load costs no address arithmetic. (Host: 4 token strides < 2^31 bytes.)
+template <typename T>
+struct Stream {
+    static constexpr int SZ = sizeof(T) == 4 ? 4 : 2;
+    using E = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+    const char *base;
+    int64_t step;
+    uint32_t off[kBatch];
+
+    __device__ __forceinline__ Stream(const void *p, int64_t first, int64_t ts, int d)
+        : base(static_cast<const char *>(p) + first * SZ), step(ts * (kBatch * SZ))
     {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int t = min(t0 + i, t1 - 1);
-            x[i] = ld_bits<IOSZ>(p.x, q.b * p.x_bs + t * p.x_ts + q.d);
-            dt[i] = ld_bits<DTSZ>(p.dt, q.b * p.dt_bs + t * p.dt_ts + q.d);
+        for (int i = 0; i < kBatch; ++i)
+            off[i] = (uint32_t)(i * ts * SZ) + (uint32_t)d * SZ;
+    }
+    // `n` tokens are left: the ones past them read the last of them
+    __device__ __forceinline__ void load(int n, uint32_t (&w)[kBatch])
+    {
+        if (n < kBatch) {
+#pragma unroll
+            for (int i = 1; i < kBatch; ++i)
+                off[i] = i < n ? off[i] : off[i - 1];
         }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            w[i] = *reinterpret_cast<const E *>(base + off[i]);
+        base += step;
     }
 };
 
-template <int DTSZ>
-__device__ __forceinline__ float step_size(uint32_t bits, float bias, const ScanParams &p, bool bf)
+// dt' and dt' x of a batch; tokens from `n` on are neutral (dt' = 0 leaves the
+// state as it is), so that every batch runs the same straight code.
+template <typename IOT, typename DTT>
+__device__ __forceinline__ void step_sizes(const uint32_t (&x)[kBatch], const uint32_t (&dt)[kBatch],
+                                           float bias, bool softplus, int n, float (&v)[kBatch],
+                                           float (&u)[kBatch])
 {
-    const float v = cvt_bits<DTSZ>(bits, bf) + bias;
-    return p.dt_softplus ? softplus_f32(v) : v;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        v[i] = cvt_raw1<DTT>(dt[i]) + bias;
+    if (softplus) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            v[i] = softplus_f32(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        v[i] = i < n ? v[i] : 0.0f;
+        u[i] = i < n ? v[i] * cvt_raw1<IOT>(x[i]) : 0.0f;
+    }
 }
 
 // Every chunk's end from a zero start (all but a row's last chunk, or all of
-// them where only the state is wanted).
-template <int IOSZ, int DTSZ>
-__global__ __launch_bounds__(64, 4) void ssu_scan_ends_kernel(const ScanParams p, const ChunkShape s,
-                                                              const float *__restrict__ packed)
+// them where only the state is wanted), and the copy of the pool's state.
+template <typename IOT, typename DTT>
+__global__ __launch_bounds__(256, 4) void ssu_scan_ends_kernel(const ScanParams p,
+                                                               const ChunkShape s,
+                                                               const float *__restrict__ packed)
 {
-    const Place q = place(p, s, s.chunks);
+    const Place q = place(p, s, (s.chunks + s.team - 1) / s.team);
+    const int c = q.team * s.team + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile = blockIdx.y;
+    const int lane = threadIdx.x & 63;
     int row;
     const int len = row_tokens(p, q.b, &row);
-    const int t0 = q.c * s.chunk, t1 = min(t0 + s.chunk, len);
-    if (t0 >= len || (p.out && t1 == len))
+    const int t0 = c * s.chunk, t1 = min(t0 + s.chunk, len);
+    const int64_t at = ((int64_t)q.b * (s.chunks + 1) + c) * s.blocks + q.blk;
+    float *e = s.start + (at * s.tiles + tile) * (kStates * 64) + lane;
+    if (t0 >= len)
         return;
-    const float *bc = packed + ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) *
-                                 (2 * kStates);
+    if (c == 0) {
+        const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + tile * kStates;
+#pragma unroll
+        for (int j = 0; j < kStates; ++j)
+            e[j * 64] = tile * kStates + (j & ~3) < p.dstate ? ld_io(p.state, so + j, p.state_dtype)
+                                                              : 0.0f;
+    }
+    if (p.out && t1 == len)
+        return;
+    e += (int64_t)s.blocks * s.tiles * (kStates * 64);
     const int64_t bc_step = (int64_t)p.ngroups * s.tiles * 2 * kStates;
-    const bool io_bf = p.io_dtype == kBF16, dt_bf = p.dt_dtype == kBF16;
+    int64_t bc = ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) * (2 * kStates);
     const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.0f;
+    Stream<IOT> xs(p.x, q.b * p.x_bs + t0 * p.x_ts, p.x_ts, q.d);
+    Stream<DTT> ds(p.dt, q.b * p.dt_bs + t0 * p.dt_ts, p.dt_ts, q.d);
     float a[kStates], h[kStates] = {}, sum = 0.0f;
+    uint32_t x[kBatch], dt[kBatch];
+    xs.load(t1 - t0, x);
+    ds.load(t1 - t0, dt);
     load_a(p, q.d, tile, a);
-    Inputs<IOSZ, DTSZ> in;
-    in.load(p, q, t0, t1);
+    float bs[kStates];  // the next token's B
+#pragma unroll
+    for (int j = 0; j < kStates; ++j)
+        bs[j] = packed[bc + j];
     for (int t = t0; t < t1; t += kBatch) {
-        const Inputs<IOSZ, DTSZ> now = in;
-        if (t + kBatch < t1)
-            in.load(p, q, t + kBatch, t1);
-        auto token = [&](int i) {
-            const float v = step_size<DTSZ>(now.dt[i], bias, p, dt_bf);
-            const float u = v * cvt_bits<IOSZ>(now.x[i], io_bf);
-            sum += v;
+        float v[kBatch], u[kBatch];
+        step_sizes<IOT, DTT>(x, dt, bias, p.dt_softplus, t1 - t, v, u);
+        if (t + kBatch < t1) {
+            xs.load(t1 - t - kBatch, x);
+            ds.load(t1 - t - kBatch, dt);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
+            float bn[kStates];
 #pragma unroll
             for (int j = 0; j < kStates; ++j)
-                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v), u * bc[i * bc_step + j]);
-        };
-        if (t + kBatch <= t1) {
+                bn[j] = packed[bc + j];
+            sum += v[i];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                token(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (t + i < t1)
-                    token(i);
+            for (int j = 0; j < kStates; ++j) {
+                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
+                bs[j] = bn[j];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        bc += kBatch * bc_step;
     }
-    const int lane = threadIdx.x;
-    const int64_t at = ((int64_t)q.b * (s.chunks + 1) + q.c + 1) * s.blocks + q.blk;
-    float *e = s.start + (at * s.tiles + tile) * (kStates * 64) + lane;
 #pragma unroll
     for (int j = 0; j < kStates; ++j)
         e[j * 64] = h[j];
     if (tile == 0)
-        s.sum[at * 64 + lane] = sum;
+        s.sum[(at + s.blocks) * 64 + lane] = sum;
 }
 
-// Every chunk's start, from the pool's state and the ends in order; with no
-// outputs also the row's last state. A wave has four state entries of a tile.
-__global__ __launch_bounds__(256) void ssu_scan_carry_kernel(const ScanParams p, const ChunkShape s)
+// Runs the starts of chunks first, first + 1, .. of NS state entries (from j0
+// of a tile) through the ends in order: use(c, h) sees the start of chunk c for
+// c = from .. to.
+template <int NS, typename Use>
+__device__ __forceinline__ void fold_ends(const ScanParams &p, const ChunkShape &s, const Place &q,
+                                          int tile, int j0, int from, int to, Use use)
+{
+    const int64_t step = (int64_t)s.blocks * s.tiles * (kStates * 64), sum_step = s.blocks * 64;
+    const int64_t first = (int64_t)q.b * (s.chunks + 1) * s.blocks + q.blk;
+    const float *e = s.start + (first * s.tiles + tile) * (kStates * 64) + j0 * 64 + (threadIdx.x & 63);
+    const float *sum = s.sum + first * 64 + (threadIdx.x & 63);
+    float a[NS], h[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        const int n = tile * kStates + j0 + j;
+        a[j] = n < p.dstate ? p.A[(int64_t)q.d * p.dstate + n] * kLog2e : 0.0f;
+        h[j] = e[j * 64];
+    }
+    constexpr int F = 32 / NS;  // ends in flight
+    for (int c = 0; c < to; c += F) {
+        float end[F][NS], total[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int k = min(c + i, to - 1) + 1;
+            total[i] = sum[k * sum_step];
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                end[i][j] = e[k * step + j * 64];
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            if (c + i < to) {
+                if (c + i >= from)
+                    use(c + i, h);
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * total[i]), end[i][j]);
+            }
+        }
+    }
+    use(to, h);
+}
+
+// The last state where no outputs are wanted; a wave has one state entry of a
+// tile.
+__global__ __launch_bounds__(1024) void ssu_scan_last_kernel(const ScanParams p, const ChunkShape s)
 {
     const Place q = place(p, s, 1);
     const int tile = blockIdx.y;
@@ -316,172 +403,178 @@ __global__ __launch_bounds__(256) void ssu_scan_carry_kernel(const ScanParams p,
     const int len = row_tokens(p, q.b, &row);
     if (len == 0)
         return;
-    const int lane = threadIdx.x & 63;
-    const int j0 = (threadIdx.x >> 6) * 4, n0 = tile * kStates + j0;
-    const bool own = n0 < p.dstate;
-    const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + n0;
-    float a[4] = {}, h[4] = {};
-    if (own) {
-        const float4 w = *reinterpret_cast<const float4 *>(p.A + (int64_t)q.d * p.dstate + n0);
-        a[0] = w.x * kLog2e, a[1] = w.y * kLog2e, a[2] = w.z * kLog2e, a[3] = w.w * kLog2e;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            h[j] = ld_io(p.state, so + j, p.state_dtype);
-    }
-    const int n = (len + s.chunk - 1) / s.chunk;  // the row's chunks
-    const int ends = p.out ? n - 1 : n;
-    const int64_t step = (int64_t)s.blocks * s.tiles * (kStates * 64);
-    float *e = s.start + ((((int64_t)q.b * (s.chunks + 1)) * s.blocks + q.blk) * s.tiles + tile) *
-                             (kStates * 64) + j0 * 64 + lane;
-    const float *sum = s.sum + (((int64_t)q.b * (s.chunks + 1)) * s.blocks + q.blk) * 64 + lane;
-    if (p.out) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            e[j * 64] = h[j];
-    }
-    constexpr int F = 4;  // ends in flight
-    for (int c = 0; c < ends; c += F) {
-        float end[F][4], total[F];
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            const int k = min(c + i, ends - 1) + 1;
-            total[i] = sum[(int64_t)k * s.blocks * 64];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                end[i][j] = e[k * step + j * 64];
-        }
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            if (c + i < ends) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * total[i]), end[i][j]);
-                    if (p.out)
-                        e[(c + i + 1) * step + j * 64] = h[j];
-                }
-            }
-        }
-    }
-    if (!p.out && p.update && own && q.dl) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st_io(p.state, so + j, h[j], p.state_dtype);
-    }
+    const int j0 = threadIdx.x >> 6, n0 = tile * kStates + j0;
+    const int chunks = (len + s.chunk - 1) / s.chunk;
+    fold_ends<1>(p, s, q, tile, j0, chunks, chunks, [&](int, const float (&h)[1]) {
+        if (p.update && n0 < p.dstate && q.dl)
+            st_io(p.state, (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + n0, h[0],
+                  p.state_dtype);
+    });
 }
 
-// The tokens of every chunk from its start. tiles waves, one per 16 state
-// entries; with more than one, a batch's partial outputs are summed through
-// LDS (two buffers, so one barrier a batch) and its tokens finished by the
-// waves in turn.
-template <int IOSZ, int DTSZ, bool ONE>
-__global__ __launch_bounds__(ONE ? 64 : 1024, 4) void ssu_scan_tokens_kernel(
+// The tokens of a team of chunks: tiles waves a chunk, one per 16 state
+// entries. The team's waves first share the fold of the ends before it (each
+// folds its part of every tile's entries; the starts meet in LDS). With more
+// than one tile a batch's partial outputs are summed through LDS (two buffers,
+// so one barrier a batch) and its tokens finished by the chunk's waves in turn.
+template <typename IOT, typename DTT, bool ONE>
+__global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
     const ScanParams p, const ChunkShape s, const float *__restrict__ packed,
     void *__restrict__ out)
 {
-    extern __shared__ float part[];  // [2][tiles][kBatch][64] unless ONE
-    const Place q = place(p, s, s.chunks);
+    // [team][tiles][16][64] starts, then unless ONE [2][team][tiles][kBatch][64]
+    extern __shared__ float lds[];
     const int lane = threadIdx.x & 63;
-    const int tile = ONE ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = ONE ? 0 : wave % s.tiles;
+    const int mate = ONE ? wave : wave / s.tiles;
+    const Place q = place(p, s, (s.chunks + s.team - 1) / s.team);
+    const int c0 = q.team * s.team, c = c0 + mate;
     int row;
     const int len = row_tokens(p, q.b, &row);
-    const int t0 = q.c * s.chunk, t_end = min(t0 + s.chunk, p.seq_len), t1 = min(t_end, len);
-    const bool io_bf = p.io_dtype == kBF16, dt_bf = p.dt_dtype == kBF16;
-    const int64_t oo = q.b * p.out_bs + q.d;
-    if (out && q.dl)
-        for (int t = max(t0, len) + tile; t < t_end; t += ONE ? 1 : s.tiles)
-            st_bits<IOSZ>(out, oo + t * p.out_ts, 0.0f, io_bf);
-    if (t0 >= len)
+    const int t0 = c * s.chunk, t_end = min(t0 + s.chunk, p.seq_len), t1 = min(t_end, len);
+    // lanes past the last channel repeat it: they store the same values
+    constexpr int SZ = Stream<IOT>::SZ;
+    char *o = static_cast<char *>(out) + (q.b * p.out_bs + t0 * p.out_ts) * SZ;
+    uint32_t off[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        off[i] = (uint32_t)(i * p.out_ts * SZ) + (uint32_t)q.d * SZ;
+    for (int t = max(t0, len) + tile; t < t_end; t += ONE ? 1 : s.tiles)
+        put<IOT>(o + (t - t0) * p.out_ts * SZ + off[0], 0.0f);
+    if (c0 * s.chunk >= len)  // the whole team
         return;
 
-    const float *bc = packed + ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) *
-                                 (2 * kStates);
+    const bool live = t0 < len;
     const int64_t bc_step = (int64_t)p.ngroups * s.tiles * 2 * kStates;
+    int64_t bc = ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) * (2 * kStates);
     const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.0f;
     const float skip = p.D ? p.D[q.d] : 0.0f;
     const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + tile * kStates;
+    const bool gated = p.z != nullptr;  // without a gate x is loaded in z's place and not used
+    Stream<IOT> xs(p.x, q.b * p.x_bs + t0 * p.x_ts, p.x_ts, q.d);
+    Stream<IOT> zs(gated ? p.z : p.x, gated ? q.b * p.z_bs + t0 * p.z_ts : q.b * p.x_bs + t0 * p.x_ts,
+                   gated ? p.z_ts : p.x_ts, q.d);
+    Stream<DTT> ds(p.dt, q.b * p.dt_bs + t0 * p.dt_ts, p.dt_ts, q.d);
+    uint32_t x[kBatch], dt[kBatch], z[kBatch];
+    auto load = [&](int n) {
+        xs.load(n, x);
+        ds.load(n, dt);
+        zs.load(n, z);
+    };
+    if (live)
+        load(t1 - t0);
     float a[kStates], h[kStates] = {};
     load_a(p, q.d, tile, a);
     if (s.chunks > 1) {
-        const int64_t at = ((int64_t)q.b * (s.chunks + 1) + q.c) * s.blocks + q.blk;
-        const float *e = s.start + (at * s.tiles + tile) * (kStates * 64) + lane;
+        // the team's last chunk with tokens
+        const int to = min(c0 + s.team, (len + s.chunk - 1) / s.chunk) - 1;
+        auto share = [&](auto ns) {
+            constexpr int NS = decltype(ns)::value;
+            const int j0 = mate * NS;
+            fold_ends<NS>(p, s, q, tile, j0, c0, to, [&](int k, const float (&st)[NS]) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    lds[(((k - c0) * s.tiles + tile) * kStates + j0 + j) * 64 + lane] = st[j];
+            });
+        };
+        if (s.team == 4)
+            share(std::integral_constant<int, 4>());
+        else if (s.team == 2)
+            share(std::integral_constant<int, 8>());
+        else
+            share(std::integral_constant<int, 16>());
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < kStates; ++j)
-            h[j] = e[j * 64];
+            h[j] = lds[((mate * s.tiles + tile) * kStates + j) * 64 + lane];
     } else {
 #pragma unroll
         for (int j = 0; j < kStates; ++j)
             if (tile * kStates + (j & ~3) < p.dstate)
                 h[j] = ld_io(p.state, so + j, p.state_dtype);
     }
-    const void *zsrc = p.z ? p.z : p.x;  // without a gate: loaded and not used
-    const int64_t zb = p.z ? p.z_bs : p.x_bs, zt = p.z ? p.z_ts : p.x_ts;
-    Inputs<IOSZ, DTSZ> in;
-    uint32_t zin[kBatch];
-    auto load = [&](int t) {
-        in.load(p, q, t, t1);
+    if (ONE && !live)
+        return;
+    // the batches of the team's first chunk, the longest (every wave meets the
+    // barriers)
+    const int batches = (min(s.chunk, len - (ONE ? t0 : c0 * s.chunk)) + kBatch - 1) / kBatch;
+    float *part = lds + (s.chunks > 1 ? s.team * s.tiles * kStates * 64 : 0);
+    if (!live)
+        bc = s.zeros;
+    float bs[kStates];  // the next token's B
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            zin[i] = ld_bits<IOSZ>(zsrc, q.b * zb + min(t + i, t1 - 1) * zt + q.d);
-    };
-    auto finish = [&](float y, float x, uint32_t zbits, int t) {
-        y = fmaf(skip, x, y);
-        if (p.z)
-            y *= silu_hw(cvt_bits<IOSZ>(zbits, io_bf));
-        if (out && q.dl)
-            st_bits<IOSZ>(out, oo + t * p.out_ts, y, io_bf);
-    };
-    load(t0);
+    for (int j = 0; j < kStates; ++j)
+        bs[j] = packed[bc + j];
     int buf = 0;
-    for (int t = t0; t < t1; t += kBatch) {
-        const Inputs<IOSZ, DTSZ> now = in;
-        uint32_t znow[kBatch];
+    for (int t = t0; t < t0 + batches * kBatch; t += kBatch) {
+        if (!ONE && t >= t1) {
+            __syncthreads();
+            continue;
+        }
+        float v[kBatch], u[kBatch], sk[kBatch], gate[kBatch], y[kBatch];
+        step_sizes<IOT, DTT>(x, dt, bias, p.dt_softplus, t1 - t, v, u);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            znow[i] = zin[i];
+        for (int i = 0; i < kBatch; ++i) {
+            sk[i] = skip * cvt_raw1<IOT>(x[i]);
+            gate[i] = cvt_raw1<IOT>(z[i]);
+        }
         if (t + kBatch < t1)
-            load(t + kBatch);
-        auto token = [&](int i) {
-            const float v = step_size<DTSZ>(now.dt[i], bias, p, dt_bf);
-            const float x = cvt_bits<IOSZ>(now.x[i], io_bf);
-            const float u = v * x;
-            const float *w = bc + i * bc_step;
-            float y[2] = {0.0f, 0.0f};
+            load(t1 - t - kBatch);
+        // token i's C and token i + 1's B (scalar loads) are on their way while
+        // token i's states are computed; the barriers keep that order
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float cs[kStates], bn[kStates];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                cs[j] = packed[bc + kStates + j];
+            bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                bn[j] = packed[bc + j];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            float y2[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < kStates; ++j) {
-                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v), u * w[j]);
-                y[j & 1] = fmaf(h[j], w[kStates + j], y[j & 1]);
+                y2[j & 1] = fmaf(h[j], cs[j], y2[j & 1]);
+                bs[j] = bn[j];
             }
-            if constexpr (ONE)
-                finish(y[0] + y[1], x, znow[i], t + i);
-            else
-                part[((buf * s.tiles + tile) * kBatch + i) * 64 + lane] = y[0] + y[1];
-        };
-        if (t + kBatch <= t1) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                token(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (t + i < t1)
-                    token(i);
+            y[i] = y2[0] + y2[1];
+            __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!ONE) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                part[(((buf * s.team + mate) * s.tiles + tile) * kBatch + i) * 64 + lane] = y[i];
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (t + i < t1 && i % s.tiles == tile) {
-                    float y = 0.0f;
+                y[i] = 0.0f;
+                if (i % s.tiles == tile)
                     for (int k = 0; k < s.tiles; ++k)
-                        y += part[((buf * s.tiles + k) * kBatch + i) * 64 + lane];
-                    finish(y, cvt_bits<IOSZ>(now.x[i], io_bf), znow[i], t + i);
-                }
+                        y[i] += part[(((buf * s.team + mate) * s.tiles + k) * kBatch + i) * 64 + lane];
             }
             buf ^= 1;
         }
-        bc += kBatch * bc_step;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            y[i] += sk[i];
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                y[i] *= silu_hw(gate[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (t + i < t1 && (ONE || i % s.tiles == tile))
+                put<IOT>(o + off[i], y[i]);
+        o += p.out_ts * (kBatch * SZ);
     }
-    if (p.update && t1 == len && q.dl) {
+    if (p.update && live && t1 == len) {
 #pragma unroll
         for (int j = 0; j < kStates; ++j)
             if (tile * kStates + (j & ~3) < p.dstate)
@@ -489,15 +582,21 @@ __global__ __launch_bounds__(ONE ? 64 : 1024, 4) void ssu_scan_tokens_kernel(
     }
 }
 
-// Which evaluation a call takes, and its cut. The target is four waves on each
-// SIMD of a full GPU (256 compute units, 4 SIMDs).
+// Which evaluation a call takes, and its cut. Chunks are as long as leaves about
+// three waves for each of the GPU's 1,024 SIMDs: every chunk costs its end, its
+// fold and 4 KiB of traffic, and too few leave SIMDs idle (1 x 2048 x 5120: 113 us
+// at 2,560 waves, 102 at 3,072, 104 at 4,096, 109 at 8,192). With context_lengths
+// rows end early and unevenly, and shorter chunks fill the gaps (8 x 777 x 2560
+// with lengths from an eighth up: 135 us at 3,072, 93 at 6,144, 86 at 8,192, 87 at
+// 10,000).
 struct Plan {
     bool rows;
     ChunkShape s;
     int64_t bc_floats, start_floats, sum_floats;
 };
 
-Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int64_t seq_len)
+Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int64_t seq_len,
+               bool ragged)
 {
     Plan q = {};
     q.rows = seq_len <= 16;
@@ -506,8 +605,8 @@ Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int6
     q.s.tiles = (int32_t)((dstate + kStates - 1) / kStates);
     q.s.per_group = (int32_t)((dim / ngroups + 63) / 64);
     q.s.blocks = (int32_t)(q.s.per_group * ngroups);
-    const int64_t waves = batch * q.s.blocks * q.s.tiles, target = 4096;
-    int64_t chunks = waves >= target ? 1 : (target + waves - 1) / waves;
+    const int64_t waves = batch * q.s.blocks * q.s.tiles, target = ragged ? 8192 : 3072;
+    int64_t chunks = waves * 2 > target ? 1 : target / waves;
     int64_t len = (seq_len + chunks - 1) / chunks;
     len = (len + kBatch - 1) / kBatch * kBatch;
     if (len < 32)
@@ -515,45 +614,73 @@ Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int6
     chunks = (seq_len + len - 1) / len;
     q.s.chunk = (int32_t)(len > seq_len ? seq_len : len);
     q.s.chunks = (int32_t)chunks;
-    q.bc_floats = batch * seq_len * ngroups * q.s.tiles * (2 * kStates);
-    if (chunks > 1) {
-        q.start_floats = batch * (chunks + 1) * q.s.blocks * q.s.tiles * (kStates * 64);
-        q.sum_floats = batch * (chunks + 1) * q.s.blocks * 64;
-    }
+    const int most = q.s.tiles <= 4 ? 4 : q.s.tiles <= 8 ? 2 : 1;
+    q.s.team = chunks == 1 ? 1 : (chunks == 2 && most > 2) ? 2 : most;
+    q.bc_floats = (batch * seq_len * ngroups * q.s.tiles + 1) * (2 * kStates);
+    q.start_floats = batch * (chunks + 1) * q.s.blocks * q.s.tiles * (kStates * 64);
+    q.sum_floats = batch * (chunks + 1) * q.s.blocks * 64;
     return q;
 }
 
-template <int IOSZ, int DTSZ>
+template <typename IOT, typename DTT>
 hipError_t launch_chunks(const ScanParams &p, const Plan &q, hipStream_t stream)
 {
     const ChunkShape &s = q.s;
-    const int64_t cells = (int64_t)p.batch * s.blocks * s.chunks;
-    const int64_t packed = q.bc_floats / 2;
+    const int64_t cells = (int64_t)p.batch * s.blocks * ((s.chunks + s.team - 1) / s.team);
+    const int64_t packed = q.bc_floats / 2 - kStates;
     if (cells > 0x7fffffff || (packed + 255) / 256 > 0x7fffffff)
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(ssu_scan_pack_kernel, dim3((unsigned)((packed + 255) / 256)), dim3(256), 0,
                        stream, p, s, packed);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && s.chunks > 1) {
-        hipLaunchKernelGGL((ssu_scan_ends_kernel<IOSZ, DTSZ>), dim3((unsigned)cells, s.tiles),
-                           dim3(64), 0, stream, p, s, s.bc);
+    if (e == hipSuccess && (s.chunks > 1 || !p.out)) {
+        hipLaunchKernelGGL((ssu_scan_ends_kernel<IOT, DTT>), dim3((unsigned)cells, s.tiles),
+                           dim3(64 * s.team), 0, stream, p, s, s.bc);
         e = hipGetLastError();
-        if (e == hipSuccess) {
-            hipLaunchKernelGGL(ssu_scan_carry_kernel, dim3((unsigned)(p.batch * s.blocks), s.tiles),
-                               dim3(256), 0, stream, p, s);
-            e = hipGetLastError();
+    }
+    if (e != hipSuccess)
+        return e;
+    if (!p.out) {
+        hipLaunchKernelGGL(ssu_scan_last_kernel, dim3((unsigned)(p.batch * s.blocks), s.tiles),
+                           dim3(1024), 0, stream, p, s);
+        return hipGetLastError();
+    }
+    const int lds = 4 * 64 * s.team * s.tiles *
+                    ((s.chunks > 1 ? kStates : 0) + (s.tiles > 1 ? 2 * kBatch : 0));
+    if (s.tiles == 1) {
+        hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOT, DTT, true>), dim3((unsigned)cells),
+                           dim3(64 * s.team), lds, stream, p, s, s.bc, p.out);
+        return hipGetLastError();
+    }
+    // up to 96 KiB (16 waves): past the default limit, raised once per device
+    if (lds > 65536) {
+        const void *fn = reinterpret_cast<const void *>(ssu_scan_tokens_kernel<IOT, DTT, false>);
+        static std::atomic<uint64_t> raised{0};
+        int dev = 0;
+        e = hipGetDevice(&dev);
+        if (e != hipSuccess)
+            return e;
+        if (dev >= 64 || !((raised.load(std::memory_order_relaxed) >> dev) & 1)) {
+            e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 98304);
+            if (e != hipSuccess)
+                return e;
+            if (dev < 64)
+                raised.fetch_or(1ull << dev, std::memory_order_relaxed);
         }
     }
-    if (e != hipSuccess || (s.chunks > 1 && !p.out))
-        return e;
-    if (s.tiles == 1)
-        hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOSZ, DTSZ, true>), dim3((unsigned)cells),
-                           dim3(64), 0, stream, p, s, s.bc, p.out);
-    else
-        hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOSZ, DTSZ, false>), dim3((unsigned)cells),
-                           dim3(64 * s.tiles), 2 * s.tiles * kBatch * 64 * 4, stream, p, s, s.bc,
-                           p.out);
+    hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOT, DTT, false>), dim3((unsigned)cells),
+                       dim3(64 * s.tiles * s.team), lds, stream, p, s, s.bc, p.out);
     return hipGetLastError();
+}
+
+template <typename IOT>
+hipError_t launch_chunks_dt(const ScanParams &p, const Plan &q, hipStream_t stream)
+{
+    switch (p.dt_dtype) {
+    case kF32: return launch_chunks<IOT, float>(p, q, stream);
+    case kF16: return launch_chunks<IOT, _Float16>(p, q, stream);
+    default: return launch_chunks<IOT, bf16_t>(p, q, stream);
+    }
 }
 
 }  // namespace
@@ -561,22 +688,24 @@ hipError_t launch_chunks(const ScanParams &p, const Plan &q, hipStream_t stream)
 int64_t scan_workspace_floats(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups,
                               int64_t seq_len)
 {
-    const Plan q = scan_plan(batch, dim, dstate, ngroups, seq_len);
+    const Plan q = scan_plan(batch, dim, dstate, ngroups, seq_len, true);  // the finer cut
     return q.bc_floats + q.start_floats + q.sum_floats;
 }
 
 hipError_t launch_scan(const ScanParams &p, hipStream_t stream)
 {
     (void)hipGetLastError();  // report only this launch's status
-    Plan q = scan_plan(p.batch, p.dim, p.dstate, p.ngroups, p.seq_len);
+    Plan q = scan_plan(p.batch, p.dim, p.dstate, p.ngroups, p.seq_len, p.ctx != nullptr);
     if (!q.rows) {
         q.s.bc = p.workspace;
+        q.s.zeros = q.bc_floats - 2 * kStates;
         q.s.start = q.s.bc + q.bc_floats;
         q.s.sum = q.s.start + q.start_floats;
-        const bool io4 = p.io_dtype == kF32, dt4 = p.dt_dtype == kF32;
-        if (io4)
-            return dt4 ? launch_chunks<4, 4>(p, q, stream) : launch_chunks<4, 2>(p, q, stream);
-        return dt4 ? launch_chunks<2, 4>(p, q, stream) : launch_chunks<2, 2>(p, q, stream);
+        switch (p.io_dtype) {
+        case kF32: return launch_chunks_dt<float>(p, q, stream);
+        case kF16: return launch_chunks_dt<_Float16>(p, q, stream);
+        default: return launch_chunks_dt<bf16_t>(p, q, stream);
+        }
     }
     if (p.dstate <= 4) return launch_scan_lanes<1>(p, stream);
     if (p.dstate <= 8) return launch_scan_lanes<2>(p, stream);
