@@ -7,7 +7,6 @@ kernels of libssu.so; there is no fallback. If the library has not been built
 the first call raises RuntimeError (build it with
 `python -m linear_rnn_recurrent_amd.build`).
 """
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -210,17 +209,19 @@ def _need(cond, msg):
 
 
 def _dev(t, name, dtypes=None, shape=None):
-    _need(t.is_cuda, f"{name} must be a GPU tensor")
-    if dtypes is not None:
-        _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if shape is not None:
-        _need(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
 
 def _dense(t, name, dtypes=None, shape=None):
     _dev(t, name, dtypes, shape)
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t
 
 
@@ -704,84 +705,113 @@ def gdn_workspace_bytes(batch, hidden, num_q_heads, num_v_heads, head_dim):
 # ---------------------------------------------------------------------------
 # Per-channel scan, causal convolution, draft verification
 # ---------------------------------------------------------------------------
-def _activation(t, name, dtype, shape):
-    """Shape, type and strides of an activation [batch, (tokens,) *row]: rows
-    dense, batch and token strides free. Returns (batch stride, token stride),
-    0 where the axis has one entry."""
-    _need(t.is_cuda, f"{name} must be a GPU tensor")
-    _need(t.dtype is dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
-    _need(t.shape == shape, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.stride()
+def _fail(msg):
+    raise ValueError(msg)
 
 
 def _outer(stride, shape, name, step):
-    """(batch stride, token stride) of an activation for the C call."""
-    n = 1 if step else 2
-    bs, ts = stride[0], 0 if step else stride[1]
-    width = 1
-    for k in range(len(shape) - 1, n - 1, -1):
-        _need(stride[k] == width or shape[k] <= 1, f"{name} must be dense in its last axes")
-        width *= shape[k]
+    """(batch stride, token stride) of an activation [batch, (tokens,) *row] for the
+    C call, 0 where the axis has one entry; rows must be dense, the outer axes may
+    have any stride but no broadcast."""
+    n = len(shape)
+    row = 1 if step else 2
+    if stride[-1] != 1 and shape[-1] > 1:
+        _fail(f"{name} must be dense in its last axes")
+    if n > row + 1 and stride[-2] != shape[-1] and shape[-2] > 1:
+        _fail(f"{name} must be dense in its last axes")
+    bs, ts = stride[0], 0
     if shape[0] <= 1:
         bs = 0
-    else:
-        _need(bs > 0, f"{name} must not be broadcast over the batch")
-    if not step:
-        if shape[1] <= 1:
-            ts = 0
-        else:
-            _need(ts > 0, f"{name} must not be broadcast over the tokens")
-            if not bs:  # one row: the C side derives the batch stride
-                return 0, ts
+    elif bs <= 0:
+        _fail(f"{name} must not be broadcast over the batch")
+    if not step and shape[1] > 1:
+        ts = stride[1]
+        if ts <= 0:
+            _fail(f"{name} must not be broadcast over the tokens")
     return bs, ts
 
 
-def _on(device):
-    """A context with `device` current; none where it is already."""
+def _view(t, name, dtype, shape, device, step):
+    """_outer of an activation after its checks."""
+    if t.device != device or t.dtype is not dtype or t.shape != shape:
+        _fail(f"{name}: expected a {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+              f"{tuple(t.shape)} on {t.device}")
+    return _outer(t.stride(), shape, name, step)
+
+
+def _vector(t, name, dtype, shape, device):
+    """Address of a dense tensor (0 if absent) after its checks."""
+    if t is None:
+        return 0
+    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _fail(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+              f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _first(t, name, dims, what):
+    """Device of a call's first tensor after its checks."""
+    if not t.is_cuda:
+        _fail(f"{name} must be a GPU tensor")
+    if t.dtype not in _DT or t.dtype is torch.uint8 or t.dim() != dims:
+        _fail(f"{name} must be {what}, fp32, fp16 or bf16")
+    return t.device
+
+
+def _raw_stream(device, stream):
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _launch(device, fn, *args):
+    """fn(*args) with `device` current; a failure raises."""
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != SSU_OK:
+        _check(rc)
 
 
 def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
                state_indices, stream, step):
-    lib = load_library()
-    _need(x.dtype in _DT and x.dim() == (2 if step else 3),
-          "x must be [batch, channels]" if step else "x must be [batch, seq_len, channels]")
-    shape = x.shape
+    lib = _LIB or load_library()
+    device = _first(x, "x", 2 if step else 3, "[batch, channels]" if step else
+                    "[batch, seq_len, channels]")
+    shape, dtype = x.shape, x.dtype
     batch, channels = shape[0], shape[-1]
-    xs = _outer(_activation(x, "x", x.dtype, shape), shape, "x", step)
-    os_ = (0, 0)
-    if out is not None:
-        os_ = _outer(_activation(out, "out", x.dtype, shape), shape, "out", step)
-    _dense(weight, "weight", _FLOAT)
-    _need(weight.dim() == 2 and weight.shape[0] == channels, "weight must be [channels, width]")
+    xs = _outer(x.stride(), shape, "x", step)
+    os_ = (0, 0) if out is None else _view(out, "out", dtype, shape, device, step)
+    if weight.dim() != 2 or weight.shape[0] != channels or weight.dtype not in _FLOAT:
+        _fail("weight must be [channels, width], fp32, fp16 or bf16")
+    wdt = weight.dtype
     width = weight.shape[1]
-    if bias is not None:
-        _dense(bias, "bias", (weight.dtype,), (channels,))
-    rows, sdt, ss = batch, x.dtype, (0, 0, 0)
+    wp = _vector(weight, "weight", wdt, weight.shape, device)
+    bp = _vector(bias, "bias", wdt, (channels,), device)
     if conv_state is not None:
-        _dev(conv_state, "conv_state", _FLOAT)
-        _need(conv_state.dim() == 3 and tuple(conv_state.shape[1:]) == (channels, width - 1),
-              "conv_state must be a [rows, channels, width-1] view")
-        rows, sdt, ss = conv_state.shape[0], conv_state.dtype, conv_state.stride()
+        sdt, rows, ss, sp = (conv_state.dtype, conv_state.shape[0], conv_state.stride(),
+                             conv_state.data_ptr())
+        if (conv_state.device != device or conv_state.dim() != 3 or sdt not in _FLOAT
+                or conv_state.shape[1] != channels or conv_state.shape[2] != width - 1):
+            _fail(f"conv_state must be a [rows, {channels}, {width - 1}] view on {device}")
     else:
-        _need(width == 1, "conv_state is required")
-    _opt_idx(state_indices, "state_indices", batch)
-    _opt_idx(context_lengths, "context_lengths", batch)
-    d = ssu_conv_dims(batch, channels, width, rows, _DT[x.dtype], _DT[weight.dtype], _DT[sdt], 0,
-                      *xs, *os_, *ss)
-    with _on(x.device):
-        st = _stream(x.device, stream)
-        if step:
-            rc = lib.ssu_conv_decode(d, _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_state),
-                                     _ptr(out), 1 if silu else 0, _ptr(state_indices), st)
-        else:
-            rc = lib.ssu_conv_prefill(d, shape[1], _ptr(x), _ptr(weight), _ptr(bias),
-                                      _ptr(conv_state), _ptr(out), 1 if silu else 0,
-                                      1 if update_state else 0, _ptr(context_lengths),
-                                      _ptr(state_indices), st)
-    _check(rc)
+        if width != 1:
+            _fail("conv_state is required")
+        rows, sdt, ss, sp = batch, dtype, (0, 0, 0), 0
+    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), device)
+    d = ssu_conv_dims(batch, channels, width, rows, _DT[dtype], _DT[wdt], _DT[sdt], 0, *xs, *os_,
+                      *ss)
+    st = _raw_stream(device, stream)
+    op = 0 if out is None else out.data_ptr()
+    if step:
+        _launch(device, lib.ssu_conv_decode, d, x.data_ptr(), wp, bp, sp, op, 1 if silu else 0, ip,
+                st)
+    else:
+        cp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), device)
+        _launch(device, lib.ssu_conv_prefill, d, shape[1], x.data_ptr(), wp, bp, sp, op,
+                1 if silu else 0, 1 if update_state else 0, cp, ip, st)
     return out
 
 
@@ -809,66 +839,62 @@ def ssu_conv_decode(x, weight, bias, conv_state, out, *, silu=True, state_indice
 
 def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
                context_lengths, state_indices, workspace, stream, step):
-    lib = load_library()
-    _need(x.dtype in _DT and x.dim() == (2 if step else 3),
-          "x must be [batch, dim]" if step else "x must be [batch, seq_len, dim]")
-    shape = x.shape
+    lib = _LIB or load_library()
+    device = _first(x, "x", 2 if step else 3, "[batch, dim]" if step else "[batch, seq_len, dim]")
+    shape, dtype = x.shape, x.dtype
     batch, dim = shape[0], shape[-1]
-    lead = shape[:-1]
-    xs = _outer(_activation(x, "x", x.dtype, shape), shape, "x", step)
-    _need(dt.dtype in _DT, f"dt has dtype {dt.dtype}")
-    ds = _outer(_activation(dt, "dt", dt.dtype, shape), shape, "dt", step)
-    _need(B.dtype in _DT and B.dim() == len(shape) + 1 and B.shape[:-2] == lead,
-          "B must be [batch, ngroups, dstate]" if step else
-          "B must be [batch, seq_len, ngroups, dstate]")
-    ngroups, dstate = B.shape[-2], B.shape[-1]
-    bs = _outer(_activation(B, "B", B.dtype, B.shape), B.shape, "B", step)
+    bshape, bdt, ddt, sdt = B.shape, B.dtype, dt.dtype, state.dtype
+    if bdt not in _FLOAT or ddt not in _FLOAT or sdt not in _FLOAT:
+        _fail("B, C, dt and state are fp32, fp16 or bf16")
+    if len(bshape) != len(shape) + 1 or bshape[:-2] != shape[:-1]:
+        _fail("B must be [batch, ngroups, dstate]" if step else
+              "B must be [batch, seq_len, ngroups, dstate]")
+    ngroups, dstate = bshape[-2], bshape[-1]
+    xs = _outer(x.stride(), shape, "x", step)
+    ds = _view(dt, "dt", ddt, shape, device, step)
+    bs = _view(B, "B", bdt, bshape, device, step)
     cs = zs = os_ = (0, 0)
+    cp = zp = op = 0
     if C is not None:
-        cs = _outer(_activation(C, "C", B.dtype, B.shape), B.shape, "C", step)
+        cs, cp = _view(C, "C", bdt, bshape, device, step), C.data_ptr()
     if z is not None:
-        zs = _outer(_activation(z, "z", x.dtype, shape), shape, "z", step)
+        zs, zp = _view(z, "z", dtype, shape, device, step), z.data_ptr()
     if out is not None:
-        _need(C is not None, "C is required")
-        os_ = _outer(_activation(out, "out", x.dtype, shape), shape, "out", step)
-    f32 = (torch.float32,)
-    _dense(A, "A", f32, (dim, dstate))
-    if dt_bias is not None:
-        _dense(dt_bias, "dt_bias", f32, (dim,))
-    if D is not None:
-        _dense(D, "D", f32, (dim,))
-    _dev(state, "state", _FLOAT)
-    st = state.stride()
-    _need(state.dim() == 3 and state.shape[1] == dim and state.shape[2] == dstate,
-          f"state has shape {tuple(state.shape)}, expected [rows, {dim}, {dstate}]")
-    _need((st[2] == 1 or dstate == 1) and (st[1] == dstate or dim == 1),
-          "state rows must be dense ([dim, dstate] contiguous)")
-    _need(st[0] >= dim * dstate or state.shape[0] == 1, "state row stride too small")
-    row = st[0] if state.shape[0] > 1 else dim * dstate
-    _opt_idx(state_indices, "state_indices", batch)
-    _opt_idx(context_lengths, "context_lengths", batch)
-    d = ssu_scan_dims(batch, dim, dstate, ngroups, state.shape[0], _DT[state.dtype],
-                      _DT[x.dtype], _DT[dt.dtype], _DT[B.dtype], 0, row, *xs, *zs, *os_, *ds, *bs,
-                      *cs)
-    with _on(x.device):
-        sm = _stream(x.device, stream)
-        if step:
-            rc = lib.ssu_scan_decode(d, _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(dt),
-                                     _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
-                                     1 if dt_softplus else 0, _ptr(state_indices), sm)
-        else:
-            if workspace is None:
-                need = lib.ssu_scan_workspace_bytes(d, shape[1])
-                if need > 0:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-            else:
-                _dense(workspace, "workspace", (torch.uint8,))
-            rc = lib.ssu_scan_prefill(d, shape[1], _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(dt),
-                                      _ptr(dt_bias), _ptr(D), _ptr(z), _ptr(state), _ptr(out),
-                                      1 if dt_softplus else 0, 1 if update_state else 0,
-                                      _ptr(context_lengths), _ptr(state_indices), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), sm)
-    _check(rc)
+        if C is None:
+            _fail("C is required")
+        os_, op = _view(out, "out", dtype, shape, device, step), out.data_ptr()
+    f32 = torch.float32
+    ap = _vector(A, "A", f32, (dim, dstate), device)
+    hp = _vector(dt_bias, "dt_bias", f32, (dim,), device)
+    kp = _vector(D, "D", f32, (dim,), device)
+    sshape, st = state.shape, state.stride()
+    if (state.device != device or len(sshape) != 3 or sshape[1] != dim or sshape[2] != dstate):
+        _fail(f"state must be [rows, {dim}, {dstate}] on {device}, got {tuple(sshape)} on "
+              f"{state.device}")
+    rows = sshape[0]
+    if (st[2] != 1 and dstate > 1) or (st[1] != dstate and dim > 1):
+        _fail("state rows must be dense ([dim, dstate] contiguous)")
+    if rows > 1 and st[0] < dim * dstate:
+        _fail("state row stride too small")
+    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), device)
+    d = ssu_scan_dims(batch, dim, dstate, ngroups, rows, _DT[sdt], _DT[dtype], _DT[ddt], _DT[bdt],
+                      0, st[0] if rows > 1 else 0, *xs, *zs, *os_, *ds, *bs, *cs)
+    sm = _raw_stream(device, stream)
+    soft = 1 if dt_softplus else 0
+    if step:
+        _launch(device, lib.ssu_scan_decode, d, x.data_ptr(), ap, B.data_ptr(), cp, dt.data_ptr(),
+                hp, kp, zp, state.data_ptr(), op, soft, ip, sm)
+        return out
+    lp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), device)
+    need = lib.ssu_scan_workspace_bytes(d, shape[1])
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    else:
+        _dense(workspace, "workspace", (torch.uint8,))
+    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _launch(device, lib.ssu_scan_prefill, d, shape[1], x.data_ptr(), ap, B.data_ptr(), cp,
+            dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, 1 if update_state else 0, lp, ip,
+            wp, wn, sm)
     return out
 
 
@@ -922,45 +948,42 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
     lengths as context_lengths. workspace: a uint8 GPU tensor of at least
     verify_workspace_bytes(batch, vocab) bytes (allocated here when None).
     """
-    lib = load_library()
-    i32 = (torch.int32,)
-    _dense(tokens, "tokens", i32)
-    _need(tokens.dim() == 2, "tokens must be [batch, num_tokens]")
-    batch, n = tokens.shape
-    _dev(target_probs, "target_probs", _FLOAT)
-    _need(target_probs.dim() == 3 and tuple(target_probs.shape[:2]) == (batch, n),
-          "target_probs must be [batch, num_tokens, vocab]")
+    lib = _LIB or load_library()
+    if not tokens.is_cuda:
+        _fail("tokens must be a GPU tensor")
+    if tokens.dim() != 2:
+        _fail("tokens must be [batch, num_tokens]")
+    device, i32, shape, dtype = tokens.device, torch.int32, tokens.shape, target_probs.dtype
+    batch, n = shape
+    if dtype not in _FLOAT or target_probs.dim() != 3:
+        _fail("target_probs must be [batch, num_tokens, vocab], fp32, fp16 or bf16")
     vocab = target_probs.shape[2]
-    ts = _outer(target_probs.stride(), target_probs.shape, "target_probs", False)
-    ds = (0, 0)
+    ts = _view(target_probs, "target_probs", dtype, (batch, n, vocab), device, False)
+    ds, qp = (0, 0), 0
     if draft_probs is not None:
-        _dev(draft_probs, "draft_probs", (target_probs.dtype,), (batch, n - 1, vocab))
-        ds = _outer(draft_probs.stride(), draft_probs.shape, "draft_probs", False)
-    _dense(uniforms, "uniforms", (torch.float32,), (batch, n))
-    if parent_ids is not None:
-        _dense(parent_ids, "parent_ids", i32, (batch, n))
-    _opt_idx(context_lengths, "context_lengths", batch)
-    _opt_idx(state_indices, "state_indices", batch)
-    _dense(accepted_lengths, "accepted_lengths", i32, (batch,))
-    _dense(next_tokens, "next_tokens", i32, (batch,))
-    most = 0
+        ds = _view(draft_probs, "draft_probs", dtype, (batch, n - 1, vocab), device, False)
+        qp = draft_probs.data_ptr()
+        if n == 1:
+            qp = 0  # no row
+    tp = _vector(tokens, "tokens", i32, shape, device)
+    up = _vector(uniforms, "uniforms", torch.float32, shape, device)
+    pp = _vector(parent_ids, "parent_ids", i32, shape, device)
+    cp = _vector(context_lengths, "context_lengths", i32, (batch,), device)
+    ip = _vector(state_indices, "state_indices", i32, (batch,), device)
+    ap = _vector(accepted_lengths, "accepted_lengths", i32, (batch,), device)
+    np_ = _vector(next_tokens, "next_tokens", i32, (batch,), device)
+    most = kp = 0
     if accepted_node_ids is not None:
-        _dense(accepted_node_ids, "accepted_node_ids", i32)
-        _need(accepted_node_ids.dim() == 2 and accepted_node_ids.shape[0] == batch,
-              "accepted_node_ids must be [batch, max_accept_len]")
-        most = accepted_node_ids.shape[1]
-    d = ssu_verify_dims(batch, n, vocab, most, _DT[target_probs.dtype], 0, *ts, *ds)
-    device = tokens.device
+        most = accepted_node_ids.shape[-1]
+        kp = _vector(accepted_node_ids, "accepted_node_ids", i32, (batch, most), device)
+    d = ssu_verify_dims(batch, n, vocab, most, _DT[dtype], 0, *ts, *ds)
     if workspace is None:
-        need = int(lib.ssu_verify_workspace_bytes(d))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _dense(workspace, "workspace", (torch.uint8,))
-    with _on(device):
-        _check(lib.ssu_draft_verify(d, _ptr(tokens), _ptr(target_probs), _ptr(draft_probs),
-                                    _ptr(uniforms), _ptr(parent_ids), _ptr(context_lengths),
-                                    _ptr(state_indices), _ptr(accepted_lengths),
-                                    _ptr(accepted_node_ids), _ptr(next_tokens), _ptr(workspace),
-                                    workspace.numel(), _stream(device, stream)))
+        workspace = torch.empty(max(int(lib.ssu_verify_workspace_bytes(d)), 16), dtype=torch.uint8,
+                                device=device)
+    else:
+        _dense(workspace, "workspace", (torch.uint8,))
+    _launch(device, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip, ap, kp,
+            np_, workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream))
     return accepted_lengths, next_tokens
 
 
