@@ -486,8 +486,8 @@ typedef struct ssu_verify_dims {
  * axis contiguous. Optional: draft_probs, parent_ids (not both),
  * context_lengths, state_indices, accepted_node_ids.
  * workspace: caller-owned device scratch of at least
- * ssu_verify_workspace_bytes(dims) bytes, 16-byte aligned (partial sums from
- * the first of the two launches to the second); contents on entry ignored, on
+ * ssu_verify_workspace_bytes(dims) bytes, 16-byte aligned (partial sums of a
+ * large vocabulary, from the first of two launches to the second); contents on entry ignored, on
  * return unspecified; calls sharing a workspace must be ordered (one stream). */
 ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
                             const void *target_probs, const void *draft_probs,
@@ -497,7 +497,7 @@ ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
                             int32_t *next_tokens, void *workspace, int64_t workspace_bytes,
                             hipStream_t stream);
 
-/* Bytes of workspace ssu_draft_verify needs: 8 * batch * (ceil(V / 2048) + 1);
+/* Bytes of workspace ssu_draft_verify needs: 8 * batch * (ceil(V / 512) + 1);
  * -1 if dims is NULL or batch or vocab is out of range. No HIP call. */
 int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims);
 

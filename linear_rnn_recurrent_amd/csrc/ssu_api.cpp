@@ -749,8 +749,8 @@ int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims)
 {
     if (!dims || dims->batch < 0 || dims->vocab < 1 || dims->vocab > (1 << 24))
         return -1;
-    const int64_t chunks = ((int64_t)dims->vocab + ssu::kVerifyChunk - 1) / ssu::kVerifyChunk;
-    return 8 * (int64_t)dims->batch * (chunks + 1);
+    const int64_t segments = ((int64_t)dims->vocab + ssu::kVerifySegment - 1) / ssu::kVerifySegment;
+    return 8 * (int64_t)dims->batch * (segments + 1);
 }
 
 ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,

@@ -136,14 +136,15 @@ int64_t scan_workspace_floats(int64_t batch, int64_t dim, int64_t dstate, int64_
 hipError_t launch_scan(const ScanParams &p, hipStream_t stream);
 
 // Verification of drafted tokens.
-constexpr int kVerifyChunk = 2048;  // vocabulary entries per partial sum
+constexpr int kVerifySegment = 512;      // vocabulary entries per partial sum
+constexpr int kVerifyRowSegments = 128;  // rows of at most so many take one launch
 struct VerifyParams {
     const int32_t *tokens;
     const void *target, *draft;
     const float *uniforms;
     const int32_t *parents, *ctx, *idx;
     int32_t *accepted, *path, *next;
-    double *partial;  // [batch][chunks + 1]: weight sums per chunk
+    double *partial;  // [batch][segments + 1]: weight sums per segment
     int64_t t_bs, t_rs, d_bs, d_rs;
     int32_t batch, num_tokens, vocab, max_accept, prob_dtype;
 };
