@@ -25,10 +25,25 @@ static_assert(kVerifySegment == 64 * kPer, "a segment is a wave's load");
 // What the walk leaves: accepted tokens, the last accepted one, whether the
 // weights subtract the draft's row, the path, and the rejected children.
 struct Walk {
-    int count, last, subtract, removed_n;
+    int count, last, subtract, removed_n, tried;
     int path[kNodes];
     int removed[kNodes];
 };
+
+// The tokens of node at's children (lane i holds nodes i and i + 64), in `to`;
+// returns how many.
+__device__ __forceinline__ int list_children(const int (&par)[2], const int (&tok)[2], int at, int *to)
+{
+    int n = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const uint64_t kids = __ballot(par[s] == at);
+        if (par[s] == at)
+            to[n + __popcll(kids & ((1ull << (threadIdx.x & 63)) - 1))] = tok[s];
+        n += __popcll(kids);
+    }
+    return n;
+}
 
 __device__ __forceinline__ double bcast(double v, int lane)
 {
@@ -38,6 +53,31 @@ __device__ __forceinline__ double bcast(double v, int lane)
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// v of the lanes that CTRL shifts from, 0 where there is none or the row is
+// masked off.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive sums over the wave's lanes: within rows of 16, then lane 15 to the
+// odd rows, then lane 31 to the upper half.
+__device__ __forceinline__ double wave_scan(double v)
+{
+    v += dpp_f64<0x111, 0xF>(v);  // row_shr:1
+    v += dpp_f64<0x112, 0xF>(v);  // row_shr:2
+    v += dpp_f64<0x114, 0xF>(v);  // row_shr:4
+    v += dpp_f64<0x118, 0xF>(v);  // row_shr:8
+    v += dpp_f64<0x142, 0xA>(v);  // row_bcast:15
+    v += dpp_f64<0x143, 0xC>(v);  // row_bcast:31
+    return v;
+}
+__device__ __forceinline__ double wave_total(double v) { return bcast(wave_scan(v), 63); }
+
 // The walk of row b by one wave (all 64 lanes); lane i holds nodes i and i+64.
 template <typename T>
 __device__ __forceinline__ void walk_row(const VerifyParams &p, int b, int len, Walk &w)
@@ -46,13 +86,22 @@ __device__ __forceinline__ void walk_row(const VerifyParams &p, int b, int len, 
     const int n = p.num_tokens;
     int par[2], tok[2];
     double prob[2], u[2], q[2];
+    // the row's tokens are loaded whole, beside its length, and masked after
+    float uf[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int64_t i = (int64_t)b * n + min(lane + 64 * s, n - 1);
+        tok[s] = p.tokens[i];
+        par[s] = p.parents ? p.parents[i] : lane + 64 * s - 1;
+        uf[s] = p.uniforms[i];
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int m = lane + 64 * s;
         const bool in = m >= 1 && m < len;
-        tok[s] = in ? p.tokens[(int64_t)b * n + m] : -1;
-        par[s] = in ? (p.parents ? p.parents[(int64_t)b * n + m] : m - 1) : -1;
-        u[s] = in ? (double)p.uniforms[(int64_t)b * n + m] : 0.0;
+        tok[s] = in ? tok[s] : -1;
+        par[s] = in ? par[s] : -1;
+        u[s] = in ? (double)uf[s] : 0.0;
         if (par[s] < 0 || par[s] >= m)
             par[s] = -1;
         const bool ok = par[s] >= 0 && tok[s] >= 0 && tok[s] < p.vocab;
@@ -84,49 +133,59 @@ __device__ __forceinline__ void walk_row(const VerifyParams &p, int b, int len, 
         for (int m = lane; m < count; m += 64)
             w.path[m] = m;
     } else {
+        // A node's children are tried all at once: child c stands if u (1 - the
+        // p of the children before it) < p, and the first that stands is taken.
         int at = 0;
-        double left = 1.0;
-        uint64_t kids[2];
-        auto children = [&]() {
+        while (count < p.max_accept) {
+            uint64_t kids[2], stand[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 kids[s] = __ballot(par[s] == at);
-        };
-        children();
-        while (count < p.max_accept && (kids[0] | kids[1])) {
-            const int s = kids[0] ? 0 : 1;
-            const int l = __ffsll((unsigned long long)kids[s]) - 1;
-            kids[s] &= kids[s] - 1;
-            const int x = __builtin_amdgcn_readlane(s ? tok[1] : tok[0], l);
-            const int m = l + 64 * s;
-            const double uc = bcast(s ? u[1] : u[0], l);
-            double pc = bcast(s ? prob[1] : prob[0], l);
-            // a sibling before it had the same token: nothing of it is left
-            const uint64_t again0 = __ballot(par[0] == at && tok[0] == x && lane < m);
-            const uint64_t again1 = __ballot(par[1] == at && tok[1] == x && lane + 64 < m);
-            if (again0 | again1)
-                pc = 0.0;
-            if (uc * left < pc) {
-                if (lane == 0)
-                    w.path[count] = m;
-                ++count;
-                at = m;
-                left = 1.0;
-                removed_n = 0;
-                children();
-            } else {
-                left -= pc;
-                if (lane == 0)
-                    w.removed[removed_n] = x;
-                ++removed_n;
+            if (!(kids[0] | kids[1]))
+                break;
+            // of a token that a sibling has before, nothing is left
+            double left[2] = {prob[0], prob[1]};
+            for (uint64_t k0 = kids[0], k1 = kids[1]; (k0 & (k0 - 1)) | k1;) {
+                const int c = k0 ? 0 : 1, l = __ffsll((unsigned long long)(k0 ? k0 : k1)) - 1;
+                k0 &= k0 - 1;  // 0 stays 0
+                if (c)
+                    k1 &= k1 - 1;
+                const int x = __builtin_amdgcn_readlane(c ? tok[1] : tok[0], l), m = l + 64 * c;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    left[s] = par[s] == at && tok[s] == x && lane + 64 * s > m ? 0.0 : left[s];
             }
+            double before = 0.0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const double mine = par[s] == at ? left[s] : 0.0;
+                double sum = 0.0;
+                if (kids[s] & (kids[s] - 1))  // more than one
+                    sum = wave_scan(mine);
+                else
+                    sum = mine;
+                stand[s] = __ballot(par[s] == at && u[s] * (1.0 - (before + (sum - mine))) < mine);
+                if (s == 0 && kids[0])
+                    before = kids[0] & (kids[0] - 1)
+                                 ? bcast(sum, 63)
+                                 : bcast(mine, __ffsll((unsigned long long)kids[0]) - 1);
+            }
+            if (!(stand[0] | stand[1]))
+                break;
+            at = stand[0] ? __ffsll((unsigned long long)stand[0]) - 1
+                          : 63 + __ffsll((unsigned long long)stand[1]);
+            if (lane == 0)
+                w.path[count] = at;
+            ++count;
         }
+        removed_n = count < p.max_accept ? list_children(par, tok, at, w.removed) : 0;
         last = at;
     }
     if (lane == 0) {
         w.count = count;
         w.last = last;
         w.subtract = subtract;
+        w.tried = count < p.max_accept;
         w.removed_n = removed_n;
     }
 }
@@ -181,24 +240,25 @@ __device__ __forceinline__ double sum8(const double (&w)[kPer])
     return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
 }
 
-// Inclusive sums over the wave's lanes.
-__device__ __forceinline__ double wave_scan(double v)
+// Sums of segments k0, k0 + step, .. below `end`, by one wave, U loaded together.
+template <typename T, bool VEC, int U>
+__device__ __forceinline__ void sum_segments(const Row &r, int k0, int step, int end, double *sums)
 {
-    const int lane = threadIdx.x & 63;
+    for (int k = k0; k < end; k += U * step) {
+        double t[U];
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(v, m, 64);
-        if (lane >= m)
-            v += o;
+        for (int i = 0; i < U; ++i) {
+            double e[kPer];
+            weights8<T, VEC>(r, min(k + i * step, end - 1), e);
+            t[i] = sum8(e);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            t[i] = wave_total(t[i]);
+            if ((threadIdx.x & 63) == 0 && k + i * step < end)
+                sums[k + i * step] = t[i];
+        }
     }
-    return v;
-}
-__device__ __forceinline__ double wave_total(double v)
-{
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1)
-        v += __shfl_xor(v, m, 64);
-    return v;
 }
 
 // Draws from the row given its segments' sums, by one wave. -1 without mass.
@@ -274,13 +334,7 @@ __device__ int draw_or_target(Row r, double *sums, int segments, double u)
     r.q = nullptr;
     r.removed_n = 0;
     __threadfence_block();  // this wave's reads of sums are done before it rewrites them
-    for (int k = 0; k < segments; ++k) {
-        double w[kPer];
-        weights8<T, VEC>(r, k, w);
-        const double t = wave_total(sum8(w));
-        if ((threadIdx.x & 63) == 0)
-            sums[k] = t;
-    }
+    sum_segments<T, VEC, 1>(r, 0, 1, segments, sums);
     __threadfence_block();
     return draw<T, VEC>(r, sums, segments, u);
 }
@@ -325,7 +379,8 @@ __global__ __launch_bounds__(1024) void ssu_verify_row_kernel(const VerifyParams
     __shared__ double sums[kVerifyRowSegments];
     const int b = blockIdx.x;
     const int len = row_length(p, b);
-    if (len > 0 && threadIdx.x < 64)
+    const double u = (double)p.uniforms[(int64_t)b * p.num_tokens];
+    if (threadIdx.x < 64)
         walk_row<T>(p, b, len, w);
     __syncthreads();
     write_path(p, b, len, w);
@@ -335,17 +390,10 @@ __global__ __launch_bounds__(1024) void ssu_verify_row_kernel(const VerifyParams
         return;
     }
     const Row r = row_of<T>(p, b, w);
-    for (int k = threadIdx.x >> 6; k < segments; k += 16) {
-        double e[kPer];
-        weights8<T, VEC>(r, k, e);
-        const double t = wave_total(sum8(e));
-        if ((threadIdx.x & 63) == 0)
-            sums[k] = t;
-    }
+    sum_segments<T, VEC, 4>(r, threadIdx.x >> 6, 16, segments, sums);
     __syncthreads();
     if (threadIdx.x < 64) {
-        const int v = draw_or_target<T, VEC>(r, sums, segments,
-                                             (double)p.uniforms[(int64_t)b * p.num_tokens]);
+        const int v = draw_or_target<T, VEC>(r, sums, segments, u);
         if (threadIdx.x == 0)
             p.next[b] = v;
     }
@@ -360,7 +408,7 @@ __global__ __launch_bounds__(256) void ssu_verify_sums_kernel(const VerifyParams
     __shared__ Walk w;
     const int b = blockIdx.y;
     const int len = row_length(p, b);
-    if (len > 0 && threadIdx.x < 64)
+    if (threadIdx.x < 64)
         walk_row<T>(p, b, len, w);
     __syncthreads();
     if (blockIdx.x == 0)
@@ -369,14 +417,10 @@ __global__ __launch_bounds__(256) void ssu_verify_sums_kernel(const VerifyParams
         return;
     const Row r = row_of<T>(p, b, w);
     double *sums = p.partial + (int64_t)b * (segments + 1);
+    if (blockIdx.x == 0 && threadIdx.x == 0)  // for the draw
+        reinterpret_cast<uint64_t *>(sums)[segments] = w.last | (w.subtract ? 256 : 0) | (w.tried ? 512 : 0);
     const int k0 = (blockIdx.x * 4 + (int)(threadIdx.x >> 6)) * each;
-    for (int k = k0; k < min(k0 + each, segments); ++k) {
-        double e[kPer];
-        weights8<T, VEC>(r, k, e);
-        const double t = wave_total(sum8(e));
-        if ((threadIdx.x & 63) == 0)
-            sums[k] = t;
-    }
+    sum_segments<T, VEC, 1>(r, k0, 1, min(k0 + each, segments), sums);
 }
 
 // .. and the draw, a wave a row.
@@ -391,10 +435,32 @@ __global__ __launch_bounds__(64) void ssu_verify_draw_kernel(const VerifyParams 
             p.next[b] = -1;
         return;
     }
-    walk_row<T>(p, b, len, w);
+    double *sums = p.partial + (int64_t)b * (segments + 1);
+    const uint64_t word = reinterpret_cast<const uint64_t *>(sums)[segments];
+    const int last = (int)(word & 255);
+    int par[2], tok[2], removed_n = 0;
+    if (!p.draft) {  // the last node's children, if they were tried, were all rejected
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int m = threadIdx.x + 64 * s;
+            const bool in = m >= 1 && m < len;
+            const int64_t i = (int64_t)b * p.num_tokens + m;
+            tok[s] = in ? p.tokens[i] : -1;
+            par[s] = in ? (p.parents ? p.parents[i] : m - 1) : -1;
+            if (par[s] >= m)
+                par[s] = -1;
+        }
+        if (word & 512)
+            removed_n = list_children(par, tok, last, w.removed);
+    }
+    if (threadIdx.x == 0) {
+        w.last = last;
+        w.subtract = (word & 256) != 0;
+        w.removed_n = removed_n;
+    }
     __syncthreads();
     const Row r = row_of<T>(p, b, w);
-    const int v = draw_or_target<T, VEC>(r, p.partial + (int64_t)b * (segments + 1), segments,
+    const int v = draw_or_target<T, VEC>(r, sums, segments,
                                          (double)p.uniforms[(int64_t)b * p.num_tokens]);
     if (threadIdx.x == 0)
         p.next[b] = v;
@@ -404,18 +470,12 @@ template <typename T, bool VEC>
 hipError_t launch_verify_type(const VerifyParams &p, hipStream_t stream)
 {
     const int segments = (p.vocab + kVerifySegment - 1) / kVerifySegment;
-#ifndef ROWSEG
-#define ROWSEG kVerifyRowSegments
-#endif
-    if (segments <= ROWSEG) {
+    if (segments <= kVerifyRowSegments) {
         hipLaunchKernelGGL((ssu_verify_row_kernel<T, VEC>), dim3((unsigned)p.batch), dim3(1024), 0,
                            stream, p, segments);
         return hipGetLastError();
     }
-#ifndef VWG
-#define VWG 2048
-#endif
-    int each = (int)(((int64_t)segments * p.batch + VWG * 4 - 1) / (VWG * 4));
+    int each = (int)(((int64_t)segments * p.batch + 1024 * 4 - 1) / (1024 * 4));
     each = each < 1 ? 1 : each > 16 ? 16 : each;
     const int blocks = (segments + 4 * each - 1) / (4 * each);
     hipLaunchKernelGGL((ssu_verify_sums_kernel<T, VEC>), dim3((unsigned)blocks, (unsigned)p.batch),
