@@ -422,7 +422,7 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
  * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
  * call and rounded once, at its end. Long calls run the tokens in chunks side by
  * side: they agree with the token-by-token recurrence to fp32 rounding, not
- * bitwise.
+ * bitwise. dim and the activations' token strides up to 2^25 (else SSU_ENOTSUP).
  * workspace: caller-owned device scratch of at least
  * ssu_scan_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
  * that is 0); contents on entry ignored, on return unspecified; calls sharing a

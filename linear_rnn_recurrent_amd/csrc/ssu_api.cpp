@@ -637,9 +637,9 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
     }
     if ((int64_t)d.batch * d.dim > 0x7fffffff)
         return fail(SSU_ENOTSUP, "%s: batch * dim too large", fn);
-    if (p.x_ts > (1 << 26) || p.z_ts > (1 << 26) || p.out_ts > (1 << 26) || p.dt_ts > (1 << 26) ||
-        d.dim > (1 << 26))
-        return fail(SSU_ENOTSUP, "%s: dim and token strides above 2^26", fn);
+    if (p.x_ts > (1 << 25) || p.z_ts > (1 << 25) || p.out_ts > (1 << 25) || p.dt_ts > (1 << 25) ||
+        d.dim > (1 << 25))
+        return fail(SSU_ENOTSUP, "%s: dim and token strides above 2^25", fn);
     if (d.batch == 0 || seq_len == 0)
         return ok();
     const size_t io = io_bytes(d.io_dtype);

@@ -29,6 +29,7 @@
 // above 16 takes ceil(dstate / 16) waves, whose partial outputs meet in LDS.
 #include <atomic>
 #include <type_traits>
+#include <utility>
 
 #include "ssu_device.h"
 #include "ssu_dpp.h"
@@ -862,6 +863,254 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
     }
 }
 
+// ---------------------------------------------------------------------------
+// Sweep
+// ---------------------------------------------------------------------------
+constexpr int kSub = 16;             // tokens of a wave's part of a step
+constexpr int kSweepWaves = 8;
+constexpr int kSweep = kSub * kSweepWaves;  // tokens of a step
+constexpr int kVuPitch = 2 * kSub + 4;      // floats: the 16 channels' rows 4 banks apart
+
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// Lane I of each row of 16, in all of the row's lanes.
+template <int I>
+__device__ __forceinline__ float row_lane(float v)
+{
+    const int u = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, 0x150 + I, 0xF, 0xF, true));
+}
+
+// Four adjacent B or C entries of one token as floats.
+template <int BC>
+__device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, float (&v)[4])
+{
+    if constexpr (BC == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = cvt1<0>(raw1<0>(base + off, j, dt), dt);
+    } else {
+        cvt4<BC>(raw4<BC>(base + off, 0, dt), dt, v);
+    }
+}
+
+// A workgroup sweeps 16 channels through a row's tokens, 128 a step. Lane (r, c)
+// of a wave has four state entries (4r ..) of channel c and the wave 16 of the
+// step's tokens: it runs them from a zero start keeping the 16 decays of each
+// entry, the waves exchange ends and decays through LDS, and every wave runs its
+// tokens again from its true start without any exponential. A token's B and C
+// lie across the 16 lanes of a row and reach its channels by DPP broadcast; its
+// dt' and dt' x go through the wave's own LDS; the sum over dstate is two
+// swap-and-adds that also hand lane (r, c) the outputs of tokens 4r .. 4r + 3,
+// whose x, dt and z it loaded. dstate above 16 repeats the two runs per 16.
+template <typename IOT, typename DTT, int BC>
+__global__ __launch_bounds__(64 * kSweepWaves, 4) void ssu_scan_sweep_kernel(
+    const ScanParams p, int per_group, int blocks, int tiles)
+{
+    extern __shared__ float lds[];
+    // [waves][16][kVuPitch] dt', dt' x; [2][waves][64][8] ends and decays; [2][tiles][64][4] states
+    const int lane = threadIdx.x & 63, r = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float *vu = lds + wave * (16 * kVuPitch);
+    float4 *ends = reinterpret_cast<float4 *>(lds + kSweepWaves * 16 * kVuPitch);
+    float4 *starts = ends + 2 * kSweepWaves * 64 * 2;
+
+    // eight neighbouring blocks, which share cache lines of x, dt, z and out, on
+    // one XCD (workgroups go to the eight XCDs in turn)
+    int id = blockIdx.x;
+    if (id < (int)(gridDim.x & ~63u))
+        id = (id & ~63) + (id & 7) * 8 + ((id >> 3) & 7);
+    const int b = id / blocks, blk = id - b * blocks;
+    const int g = blk / per_group;
+    const int width = p.dim / p.ngroups;
+    // lanes past the group's last channel repeat it: they store the same values
+    const int d = g * width + min((blk - g * per_group) * 16 + c, width - 1);
+    int row;
+    const int len = row_tokens(p, b, &row);
+
+    constexpr int SZ = sizeof(IOT) == 4 ? 4 : 2, DZ = sizeof(DTT) == 4 ? 4 : 2;
+    using E = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+    using DE = typename std::conditional<DZ == 4, uint32_t, uint16_t>::type;
+    char *out = static_cast<char *>(p.out) + b * p.out_bs * SZ;
+    const uint32_t dx = d * SZ, dd = d * DZ;
+    if (p.out)
+        for (int t = len + wave * 4 + r; t < p.seq_len; t += kSweepWaves * 4)
+            put<IOT>(out + t * p.out_ts * SZ + dx, 0.0f);
+    if (len == 0)
+        return;
+
+    const bool gated = p.z != nullptr;  // absent operands are loaded from a present one and not used
+    const char *xp = static_cast<const char *>(p.x) + b * p.x_bs * SZ;
+    const char *zp = gated ? static_cast<const char *>(p.z) + b * p.z_bs * SZ : xp;
+    const int64_t zts = gated ? p.z_ts : p.x_ts;
+    const char *dp = static_cast<const char *>(p.dt) + b * p.dt_bs * DZ;
+    const int bz = p.bc_dtype == kF32 ? 4 : 2;
+    const char *bp = static_cast<const char *>(p.B) + (b * p.b_bs + (int64_t)g * p.dstate) * bz;
+    const char *cp = p.out ? static_cast<const char *>(p.C) + (b * p.c_bs + (int64_t)g * p.dstate) * bz : bp;
+    const int64_t bts = p.b_ts * bz, cts = (p.out ? p.c_ts : p.b_ts) * bz;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f;
+    const float skip = p.D ? p.D[d] : 0.0f;
+    const int64_t so = (int64_t)row * p.row_stride + (int64_t)d * p.dstate;
+
+    // the states at the first step's start
+    for (int k = wave; k < tiles; k += kSweepWaves) {
+        float h[4] = {};
+        const int n0 = k * kStates + r * 4;
+        if (n0 < p.dstate) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = ld_io(p.state, so + n0 + j, p.state_dtype);
+        }
+        starts[k * 64 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+    }
+    int starts_now = 0;  // which of the two copies the step reads; the other gets the next's
+
+    // a lane's byte offsets of its four tokens from the wave's first (host: 16
+    // token strides < 2^32 bytes)
+    const uint32_t xts = (uint32_t)p.x_ts * SZ, gts = (uint32_t)zts * SZ, dts = (uint32_t)p.dt_ts * DZ,
+                   ots = (uint32_t)p.out_ts * SZ;
+    E x[4], z[4];
+    DE dt[4];
+    auto load = [&](int t0) {  // this wave's tokens of the step at t0; past the row: its last
+        const int w0 = min(t0 + wave * kSub, len - 1), most = len - 1 - w0;
+        const char *xw = xp + w0 * p.x_ts * SZ, *zw = zp + w0 * zts * SZ, *dw = dp + w0 * p.dt_ts * DZ;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t t = min(r * 4 + q, most);
+            x[q] = *reinterpret_cast<const E *>(xw + (t * xts + dx));
+            z[q] = *reinterpret_cast<const E *>(zw + (t * gts + dx));
+            dt[q] = *reinterpret_cast<const DE *>(dw + (t * dts + dd));
+        }
+    };
+    load(0);
+    int buf = 0;
+    for (int t0 = 0; t0 < len; t0 += kSweep) {
+        const int w0 = t0 + wave * kSub;  // the wave's first token
+        float xs[4], gate[4], y4[4] = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v = cvt_raw1<DTT>(dt[q]) + bias;
+            if (p.dt_softplus)
+                v = softplus_f32(v);
+            const bool in = w0 + r * 4 + q < len;  // others are neutral: dt' = 0
+            v = in ? v : 0.0f;
+            const float xv = cvt_raw1<IOT>(x[q]);
+            *reinterpret_cast<float2 *>(vu + c * kVuPitch + (r * 4 + q) * 2) =
+                make_float2(v, in ? v * xv : 0.0f);
+            xs[q] = skip * xv;
+            gate[q] = cvt_raw1<IOT>(z[q]);
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (t0 + kSweep < len)
+            load(t0 + kSweep);
+        for (int k = 0; k < tiles; ++k) {
+            const int n0 = k * kStates + r * 4, nn = min(n0, p.dstate - 4);
+            const bool own = n0 < p.dstate;
+            const float4 aw = *reinterpret_cast<const float4 *>(p.A + (int64_t)d * p.dstate + nn);
+            const int tok = min(w0 + c, len - 1);  // B and C: lane c has token c of the wave's
+            float bv[4], cv[4];
+            ld_bc4<BC>(bp + tok * bts, nn * bz, p.bc_dtype, bv);
+            ld_bc4<BC>(cp + tok * cts, nn * bz, p.bc_dtype, cv);
+            const float a[4] = {aw.x * kLog2e, aw.y * kLog2e, aw.z * kLog2e, aw.w * kLog2e};
+            const bool real = own && w0 + c < len;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bv[j] = real ? bv[j] : 0.0f;
+                cv[j] = real ? cv[j] : 0.0f;
+            }
+            // from a zero start
+            float dec[kSub][4], h[4] = {}, sum = 0.0f;
+            each_of(
+                [&](auto tt) {
+                    constexpr int t = decltype(tt)::value;
+                    const float2 w = *reinterpret_cast<const float2 *>(vu + c * kVuPitch + t * 2);
+                    sum += w.x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dec[t][j] = __builtin_amdgcn_exp2f(a[j] * w.x);
+                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * w.y);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // keeps the tokens in order, and the registers few
+                },
+                std::make_integer_sequence<int, kSub>());
+            float4 *mine = ends + ((buf * kSweepWaves + wave) * 64 + lane) * 2;
+            mine[0] = make_float4(h[0], h[1], h[2], h[3]);
+            mine[1] = make_float4(__builtin_amdgcn_exp2f(a[0] * sum), __builtin_amdgcn_exp2f(a[1] * sum),
+                                  __builtin_amdgcn_exp2f(a[2] * sum), __builtin_amdgcn_exp2f(a[3] * sum));
+            __syncthreads();
+            // the wave's start
+            const float4 s0 = starts[(starts_now * tiles + k) * 64 + lane];
+            h[0] = s0.x, h[1] = s0.y, h[2] = s0.z, h[3] = s0.w;
+            for (int m = 0; m < wave; ++m) {
+                const float4 e = ends[((buf * kSweepWaves + m) * 64 + lane) * 2];
+                const float4 f = ends[((buf * kSweepWaves + m) * 64 + lane) * 2 + 1];
+                h[0] = fmaf(h[0], f.x, e.x);
+                h[1] = fmaf(h[1], f.y, e.y);
+                h[2] = fmaf(h[2], f.z, e.z);
+                h[3] = fmaf(h[3], f.w, e.w);
+            }
+            buf ^= 1;
+            float y[kSub];
+            each_of(
+                [&](auto tt) {
+                    constexpr int t = decltype(tt)::value;
+                    const float u = vu[c * kVuPitch + t * 2 + 1];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * u);
+                        y[t] = j == 0 ? row_lane<t>(cv[j]) * h[j] : fmaf(row_lane<t>(cv[j]), h[j], y[t]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                },
+                std::make_integer_sequence<int, kSub>());
+            // sums over the four rows: halves, then rows, leaving tokens 4r .. 4r + 3
+            float y8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[i]),
+                                                                __float_as_uint(y[i + 8]), false, false);
+                y8[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(y8[i]),
+                                                                __float_as_uint(y8[i + 4]), false, false);
+                y4[i] += __uint_as_float(w[0]) + __uint_as_float(w[1]);
+            }
+            if (wave == kSweepWaves - 1)
+                starts[((starts_now ^ 1) * tiles + k) * 64 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+        }
+        if (p.out) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v = y4[q] + xs[q];
+                if (gated)
+                    v *= silu_hw(gate[q]);
+                if (w0 + r * 4 + q < len)
+                    put<IOT>(out + w0 * p.out_ts * SZ + ((r * 4 + q) * ots + dx), v);
+            }
+        }
+        starts_now ^= 1;
+    }
+    __syncthreads();
+    if (p.update) {
+        for (int k = wave; k < tiles; k += kSweepWaves) {
+            const int n0 = k * kStates + r * 4;
+            const float4 s0 = starts[(starts_now * tiles + k) * 64 + lane];
+            const float h[4] = {s0.x, s0.y, s0.z, s0.w};
+            if (n0 < p.dstate) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_io(p.state, so + n0 + j, h[j], p.state_dtype);
+            }
+        }
+    }
+}
+
 // Which evaluation a call takes, and its cut. Chunks are as long as leaves about
 // three waves for each of the GPU's 1,024 SIMDs: every chunk costs its end, its
 // fold and 4 KiB of traffic, and too few leave SIMDs idle (1 x 2048 x 5120: 113 us
@@ -870,7 +1119,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
 // with lengths from an eighth up: 135 us at 3,072, 93 at 6,144, 86 at 8,192, 87 at
 // 10,000).
 struct Plan {
-    bool rows;
+    bool rows, sweep;
     ChunkShape s;
     int64_t bc_floats, start_floats, sum_floats;
 };
@@ -881,6 +1130,12 @@ Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int6
     Plan q = {};
     q.rows = seq_len <= 16;
     if (q.rows)
+        return q;
+#ifndef SWEEP_MIN
+#define SWEEP_MIN 192
+#endif
+    q.sweep = batch * ngroups * ((dim / ngroups + 15) / 16) >= SWEEP_MIN;
+    if (q.sweep)
         return q;
     q.s.tiles = (int32_t)((dstate + kStates - 1) / kStates);
     q.s.per_group = (int32_t)((dim / ngroups + 63) / 64);
@@ -900,6 +1155,21 @@ Plan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int6
     q.start_floats = batch * (chunks + 1) * q.s.blocks * q.s.tiles * (kStates * 64);
     q.sum_floats = batch * (chunks + 1) * q.s.blocks * 64;
     return q;
+}
+
+// Dynamic LDS above the default 64 KiB is allowed once per kernel and device.
+hipError_t raise_lds(const void *kernel, int bytes, std::atomic<uint64_t> *raised)
+{
+    if (bytes <= 65536)
+        return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess || (dev < 64 && ((raised->load(std::memory_order_relaxed) >> dev) & 1)))
+        return e;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 98304);
+    if (e == hipSuccess && dev < 64)
+        raised->fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
 }
 
 template <typename IOT, typename DTT>
@@ -932,34 +1202,54 @@ hipError_t launch_chunks(const ScanParams &p, const Plan &q, hipStream_t stream)
                            dim3(64 * s.team), lds, stream, p, s, s.bc, p.out);
         return hipGetLastError();
     }
-    // up to 96 KiB (16 waves): past the default limit, raised once per device
-    if (lds > 65536) {
-        const void *fn = reinterpret_cast<const void *>(ssu_scan_tokens_kernel<IOT, DTT, false>);
-        static std::atomic<uint64_t> raised{0};
-        int dev = 0;
-        e = hipGetDevice(&dev);
-        if (e != hipSuccess)
-            return e;
-        if (dev >= 64 || !((raised.load(std::memory_order_relaxed) >> dev) & 1)) {
-            e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 98304);
-            if (e != hipSuccess)
-                return e;
-            if (dev < 64)
-                raised.fetch_or(1ull << dev, std::memory_order_relaxed);
-        }
-    }
+    static std::atomic<uint64_t> raised{0};
+    e = raise_lds(reinterpret_cast<const void *>(ssu_scan_tokens_kernel<IOT, DTT, false>), lds, &raised);
+    if (e != hipSuccess)
+        return e;
     hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOT, DTT, false>), dim3((unsigned)cells),
                        dim3(64 * s.tiles * s.team), lds, stream, p, s, s.bc, p.out);
     return hipGetLastError();
 }
 
+template <typename IOT, typename DTT, int BC>
+hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
+{
+    const int per_group = (p.dim / p.ngroups + 15) / 16, blocks = per_group * p.ngroups;
+    const int tiles = (p.dstate + kStates - 1) / kStates;
+    if ((int64_t)p.batch * blocks > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    const int lds = 4 * (kSweepWaves * 16 * kVuPitch + 2 * kSweepWaves * 64 * 8 + 2 * tiles * 64 * 4);
+    const auto kernel = ssu_scan_sweep_kernel<IOT, DTT, BC>;
+    static std::atomic<uint64_t> raised{0};
+    const hipError_t e = raise_lds(reinterpret_cast<const void *>(kernel), lds, &raised);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.batch * blocks)), dim3(64 * kSweepWaves), lds, stream,
+                       p, per_group, blocks, tiles);
+    return hipGetLastError();
+}
+
+template <typename IOT, typename DTT>
+hipError_t launch_prompt(const ScanParams &p, const Plan &q, hipStream_t stream)
+{
+    if (!q.sweep)
+        return launch_chunks<IOT, DTT>(p, q, stream);
+    const int es = p.bc_dtype == kF32 ? 4 : 2;
+    auto vec = [&](const void *m, int64_t bs, int64_t ts) {
+        return (uintptr_t)m % (4 * es) == 0 && bs % 4 == 0 && ts % 4 == 0;
+    };
+    if (!vec(p.B, p.b_bs, p.b_ts) || (p.out && !vec(p.C, p.c_bs, p.c_ts)))
+        return launch_sweep<IOT, DTT, 0>(p, stream);
+    return es == 4 ? launch_sweep<IOT, DTT, 4>(p, stream) : launch_sweep<IOT, DTT, 2>(p, stream);
+}
+
 template <typename IOT>
-hipError_t launch_chunks_dt(const ScanParams &p, const Plan &q, hipStream_t stream)
+hipError_t launch_prompt_dt(const ScanParams &p, const Plan &q, hipStream_t stream)
 {
     switch (p.dt_dtype) {
-    case kF32: return launch_chunks<IOT, float>(p, q, stream);
-    case kF16: return launch_chunks<IOT, _Float16>(p, q, stream);
-    default: return launch_chunks<IOT, bf16_t>(p, q, stream);
+    case kF32: return launch_prompt<IOT, float>(p, q, stream);
+    case kF16: return launch_prompt<IOT, _Float16>(p, q, stream);
+    default: return launch_prompt<IOT, bf16_t>(p, q, stream);
     }
 }
 
@@ -982,9 +1272,9 @@ hipError_t launch_scan(const ScanParams &p, hipStream_t stream)
         q.s.start = q.s.bc + q.bc_floats;
         q.s.sum = q.s.start + q.start_floats;
         switch (p.io_dtype) {
-        case kF32: return launch_chunks_dt<float>(p, q, stream);
-        case kF16: return launch_chunks_dt<_Float16>(p, q, stream);
-        default: return launch_chunks_dt<bf16_t>(p, q, stream);
+        case kF32: return launch_prompt_dt<float>(p, q, stream);
+        case kF16: return launch_prompt_dt<_Float16>(p, q, stream);
+        default: return launch_prompt_dt<bf16_t>(p, q, stream);
         }
     }
     switch (p.state_dtype) {
