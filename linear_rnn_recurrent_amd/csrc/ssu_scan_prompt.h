@@ -1,0 +1,810 @@
+// Per-channel selective scan of prompts: the kernels of ssu_scan.hip's other two
+// evaluations, which that file describes. Instantiated once per type of x, z and
+// out by ssu_scan_prompt_{f32,f16,bf16}.hip.
+#pragma once
+
+#include "ssu_scan_impl.h"
+
+namespace ssu {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Chunks
+// ---------------------------------------------------------------------------
+// The block of channels, the batch row and the team of chunks of a workgroup.
+struct Place {
+    int b, team, blk, g, d, dl;  // .., group, channel (clamped), whether its lane is live
+};
+
+__device__ __forceinline__ Place place(const ScanParams &p, const ChunkShape &s, int teams)
+{
+    Place q;
+    int i = blockIdx.x;
+    q.blk = i % s.blocks;
+    i /= s.blocks;
+    q.team = i % teams;
+    q.b = i / teams;
+    q.g = q.blk / s.per_group;
+    const int width = p.dim / p.ngroups;
+    const int local = (q.blk - q.g * s.per_group) * 64 + (int)(threadIdx.x & 63);
+    q.dl = local < width;
+    q.d = q.g * width + min(local, width - 1);
+    return q;
+}
+
+// B and C in fp32 (C's half is not written without outputs).
+__global__ __launch_bounds__(256) void ssu_scan_pack_kernel(const ScanParams p, const ChunkShape s,
+                                                            int64_t total)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (blockIdx.x == 0 && threadIdx.x < 2 * kStates)
+        s.bc[s.zeros + threadIdx.x] = 0.0f;
+    if (i >= total)
+        return;
+    const int n16 = s.tiles * kStates;
+    const int n = (int)(i % n16);
+    int64_t r = i / n16;
+    const int g = (int)(r % p.ngroups);
+    r /= p.ngroups;
+    const int t = (int)(r % p.seq_len);
+    const int b = (int)(r / p.seq_len);
+    int row;
+    if (t >= row_tokens(p, b, &row))
+        return;
+    float *o = s.bc + (i / kStates) * (2 * kStates) + (n & (kStates - 1));
+    const bool in = n < p.dstate;
+    const int64_t e = (int64_t)g * p.dstate + n;
+    o[0] = in ? ld_io(p.B, b * p.b_bs + t * p.b_ts + e, p.bc_dtype) : 0.0f;
+    if (p.out)
+        o[kStates] = in ? ld_io(p.C, b * p.c_bs + t * p.c_ts + e, p.bc_dtype) : 0.0f;
+}
+
+// A[d, 16 tile ..] log2(e); entries past dstate are 0.
+__device__ __forceinline__ void load_a(const ScanParams &p, int d, int tile, float (&a)[kStates])
+{
+#pragma unroll
+    for (int j = 0; j < kStates; j += 4) {
+        float4 w = make_float4(0, 0, 0, 0);
+        if (tile * kStates + j < p.dstate)
+            w = *reinterpret_cast<const float4 *>(p.A + (int64_t)d * p.dstate + tile * kStates + j);
+        a[j] = w.x * kLog2e;
+        a[j + 1] = w.y * kLog2e;
+        a[j + 2] = w.z * kLog2e;
+        a[j + 3] = w.w * kLog2e;
+    }
+}
+
+// One activation [.., seq_len, dim] read a batch of tokens at a time: a scalar
+// base that moves by batches, and a byte offset per token of the batch and lane,
+// so that a load costs no address arithmetic. (Host: 4 token strides < 2^31 bytes.)
+template <typename T>
+struct Stream {
+    static constexpr int SZ = sizeof(T) == 4 ? 4 : 2;
+    using E = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+    const char *base;
+    int64_t step;
+    uint32_t off[kBatch];
+
+    __device__ __forceinline__ Stream(const void *p, int64_t first, int64_t ts, int d)
+        : base(static_cast<const char *>(p) + first * SZ), step(ts * (kBatch * SZ))
+    {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            off[i] = (uint32_t)(i * ts * SZ) + (uint32_t)d * SZ;
+    }
+    // `n` tokens are left: the ones past them read the last of them
+    __device__ __forceinline__ void load(int n, uint32_t (&w)[kBatch])
+    {
+        if (n < kBatch) {
+#pragma unroll
+            for (int i = 1; i < kBatch; ++i)
+                off[i] = i < n ? off[i] : off[i - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            w[i] = *reinterpret_cast<const E *>(base + off[i]);
+        base += step;
+    }
+};
+
+// dt' and dt' x of a batch; tokens from `n` on are neutral (dt' = 0 leaves the
+// state as it is), so that every batch runs the same straight code.
+template <typename IOT, typename DTT>
+__device__ __forceinline__ void step_sizes(const uint32_t (&x)[kBatch], const uint32_t (&dt)[kBatch],
+                                           float bias, bool softplus, int n, float (&v)[kBatch],
+                                           float (&u)[kBatch])
+{
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        v[i] = cvt_raw1<DTT>(dt[i]) + bias;
+    if (softplus) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            v[i] = softplus_f32(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        v[i] = i < n ? v[i] : 0.0f;
+        u[i] = i < n ? v[i] * cvt_raw1<IOT>(x[i]) : 0.0f;
+    }
+}
+
+// Every chunk's end from a zero start (all but a row's last chunk, or all of
+// them where only the state is wanted), and the copy of the pool's state.
+template <typename IOT, typename DTT>
+__global__ __launch_bounds__(256, 4) void ssu_scan_ends_kernel(const ScanParams p,
+                                                               const ChunkShape s,
+                                                               const float *__restrict__ packed)
+{
+    const Place q = place(p, s, (s.chunks + s.team - 1) / s.team);
+    const int c = q.team * s.team + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = blockIdx.y;
+    const int lane = threadIdx.x & 63;
+    int row;
+    const int len = row_tokens(p, q.b, &row);
+    const int t0 = c * s.chunk, t1 = min(t0 + s.chunk, len);
+    const int64_t at = ((int64_t)q.b * (s.chunks + 1) + c) * s.blocks + q.blk;
+    float *e = s.start + (at * s.tiles + tile) * (kStates * 64) + lane;
+    if (t0 >= len)
+        return;
+    if (c == 0) {
+        const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + tile * kStates;
+#pragma unroll
+        for (int j = 0; j < kStates; ++j)
+            e[j * 64] = tile * kStates + (j & ~3) < p.dstate ? ld_io(p.state, so + j, p.state_dtype)
+                                                              : 0.0f;
+    }
+    if (p.out && t1 == len)
+        return;
+    e += (int64_t)s.blocks * s.tiles * (kStates * 64);
+    const int64_t bc_step = (int64_t)p.ngroups * s.tiles * 2 * kStates;
+    int64_t bc = ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) * (2 * kStates);
+    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.0f;
+    Stream<IOT> xs(p.x, q.b * p.x_bs + t0 * p.x_ts, p.x_ts, q.d);
+    Stream<DTT> ds(p.dt, q.b * p.dt_bs + t0 * p.dt_ts, p.dt_ts, q.d);
+    float a[kStates], h[kStates] = {}, sum = 0.0f;
+    uint32_t x[kBatch], dt[kBatch];
+    xs.load(t1 - t0, x);
+    ds.load(t1 - t0, dt);
+    load_a(p, q.d, tile, a);
+    float bs[kStates];  // the next token's B
+#pragma unroll
+    for (int j = 0; j < kStates; ++j)
+        bs[j] = packed[bc + j];
+    for (int t = t0; t < t1; t += kBatch) {
+        float v[kBatch], u[kBatch];
+        step_sizes<IOT, DTT>(x, dt, bias, p.dt_softplus, t1 - t, v, u);
+        if (t + kBatch < t1) {
+            xs.load(t1 - t - kBatch, x);
+            ds.load(t1 - t - kBatch, dt);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
+            float bn[kStates];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                bn[j] = packed[bc + j];
+            sum += v[i];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j) {
+                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
+                bs[j] = bn[j];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kStates; ++j)
+        e[j * 64] = h[j];
+    if (tile == 0)
+        s.sum[(at + s.blocks) * 64 + lane] = sum;
+}
+
+// Runs the starts of chunks first, first + 1, .. of NS state entries (from j0
+// of a tile) through the ends in order: use(c, h) sees the start of chunk c for
+// c = from .. to.
+template <int NS, typename Use>
+__device__ __forceinline__ void fold_ends(const ScanParams &p, const ChunkShape &s, const Place &q,
+                                          int tile, int j0, int from, int to, Use use)
+{
+    const int64_t step = (int64_t)s.blocks * s.tiles * (kStates * 64), sum_step = s.blocks * 64;
+    const int64_t first = (int64_t)q.b * (s.chunks + 1) * s.blocks + q.blk;
+    const float *e = s.start + (first * s.tiles + tile) * (kStates * 64) + j0 * 64 + (threadIdx.x & 63);
+    const float *sum = s.sum + first * 64 + (threadIdx.x & 63);
+    float a[NS], h[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        const int n = tile * kStates + j0 + j;
+        a[j] = n < p.dstate ? p.A[(int64_t)q.d * p.dstate + n] * kLog2e : 0.0f;
+        h[j] = e[j * 64];
+    }
+    constexpr int F = 32 / NS;  // ends in flight
+    for (int c = 0; c < to; c += F) {
+        float end[F][NS], total[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int k = min(c + i, to - 1) + 1;
+            total[i] = sum[k * sum_step];
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                end[i][j] = e[k * step + j * 64];
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            if (c + i < to) {
+                if (c + i >= from)
+                    use(c + i, h);
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * total[i]), end[i][j]);
+            }
+        }
+    }
+    use(to, h);
+}
+
+// The last state where no outputs are wanted; a wave has one state entry of a
+// tile.
+__global__ __launch_bounds__(1024) void ssu_scan_last_kernel(const ScanParams p, const ChunkShape s)
+{
+    const Place q = place(p, s, 1);
+    const int tile = blockIdx.y;
+    int row;
+    const int len = row_tokens(p, q.b, &row);
+    if (len == 0)
+        return;
+    const int j0 = threadIdx.x >> 6, n0 = tile * kStates + j0;
+    const int chunks = (len + s.chunk - 1) / s.chunk;
+    fold_ends<1>(p, s, q, tile, j0, chunks, chunks, [&](int, const float (&h)[1]) {
+        if (p.update && n0 < p.dstate && q.dl)
+            st_io(p.state, (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + n0, h[0],
+                  p.state_dtype);
+    });
+}
+
+// The tokens of a team of chunks: tiles waves a chunk, one per 16 state
+// entries. The team's waves first share the fold of the ends before it (each
+// folds its part of every tile's entries; the starts meet in LDS). With more
+// than one tile a batch's partial outputs are summed through LDS (two buffers,
+// so one barrier a batch) and its tokens finished by the chunk's waves in turn.
+template <typename IOT, typename DTT, bool ONE>
+__global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
+    const ScanParams p, const ChunkShape s, const float *__restrict__ packed,
+    void *__restrict__ out)
+{
+    // [team][tiles][16][64] starts, then unless ONE [2][team][tiles][kBatch][64]
+    extern __shared__ float lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = ONE ? 0 : wave % s.tiles;
+    const int mate = ONE ? wave : wave / s.tiles;
+    const Place q = place(p, s, (s.chunks + s.team - 1) / s.team);
+    const int c0 = q.team * s.team, c = c0 + mate;
+    int row;
+    const int len = row_tokens(p, q.b, &row);
+    const int t0 = c * s.chunk, t_end = min(t0 + s.chunk, p.seq_len), t1 = min(t_end, len);
+    // lanes past the last channel repeat it: they store the same values
+    constexpr int SZ = Stream<IOT>::SZ;
+    char *o = static_cast<char *>(out) + (q.b * p.out_bs + t0 * p.out_ts) * SZ;
+    uint32_t off[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        off[i] = (uint32_t)(i * p.out_ts * SZ) + (uint32_t)q.d * SZ;
+    for (int t = max(t0, len) + tile; t < t_end; t += ONE ? 1 : s.tiles)
+        put<IOT>(o + (t - t0) * p.out_ts * SZ + off[0], 0.0f);
+    if (c0 * s.chunk >= len)  // the whole team
+        return;
+
+    const bool live = t0 < len;
+    const int64_t bc_step = (int64_t)p.ngroups * s.tiles * 2 * kStates;
+    int64_t bc = ((((int64_t)q.b * p.seq_len + t0) * p.ngroups + q.g) * s.tiles + tile) * (2 * kStates);
+    const float bias = p.dt_bias ? p.dt_bias[q.d] : 0.0f;
+    const float skip = p.D ? p.D[q.d] : 0.0f;
+    const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + tile * kStates;
+    const bool gated = p.z != nullptr;  // without a gate x is loaded in z's place and not used
+    Stream<IOT> xs(p.x, q.b * p.x_bs + t0 * p.x_ts, p.x_ts, q.d);
+    Stream<IOT> zs(gated ? p.z : p.x, gated ? q.b * p.z_bs + t0 * p.z_ts : q.b * p.x_bs + t0 * p.x_ts,
+                   gated ? p.z_ts : p.x_ts, q.d);
+    Stream<DTT> ds(p.dt, q.b * p.dt_bs + t0 * p.dt_ts, p.dt_ts, q.d);
+    uint32_t x[kBatch], dt[kBatch], z[kBatch];
+    auto load = [&](int n) {
+        xs.load(n, x);
+        ds.load(n, dt);
+        zs.load(n, z);
+    };
+    if (live)
+        load(t1 - t0);
+    float a[kStates], h[kStates] = {};
+    load_a(p, q.d, tile, a);
+    if (s.chunks > 1) {
+        // the team's last chunk with tokens
+        const int to = min(c0 + s.team, (len + s.chunk - 1) / s.chunk) - 1;
+        auto share = [&](auto ns) {
+            constexpr int NS = decltype(ns)::value;
+            const int j0 = mate * NS;
+            fold_ends<NS>(p, s, q, tile, j0, c0, to, [&](int k, const float (&st)[NS]) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    lds[(((k - c0) * s.tiles + tile) * kStates + j0 + j) * 64 + lane] = st[j];
+            });
+        };
+        if (s.team == 4)
+            share(std::integral_constant<int, 4>());
+        else if (s.team == 2)
+            share(std::integral_constant<int, 8>());
+        else
+            share(std::integral_constant<int, 16>());
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kStates; ++j)
+            h[j] = lds[((mate * s.tiles + tile) * kStates + j) * 64 + lane];
+    } else {
+#pragma unroll
+        for (int j = 0; j < kStates; ++j)
+            if (tile * kStates + (j & ~3) < p.dstate)
+                h[j] = ld_io(p.state, so + j, p.state_dtype);
+    }
+    if (ONE && !live)
+        return;
+    // the batches of the team's first chunk, the longest (every wave meets the
+    // barriers)
+    const int batches = (min(s.chunk, len - (ONE ? t0 : c0 * s.chunk)) + kBatch - 1) / kBatch;
+    float *part = lds + (s.chunks > 1 ? s.team * s.tiles * kStates * 64 : 0);
+    if (!live)
+        bc = s.zeros;
+    float bs[kStates];  // the next token's B
+#pragma unroll
+    for (int j = 0; j < kStates; ++j)
+        bs[j] = packed[bc + j];
+    int buf = 0;
+    for (int t = t0; t < t0 + batches * kBatch; t += kBatch) {
+        if (!ONE && t >= t1) {
+            __syncthreads();
+            continue;
+        }
+        float v[kBatch], u[kBatch], sk[kBatch], gate[kBatch], y[kBatch];
+        step_sizes<IOT, DTT>(x, dt, bias, p.dt_softplus, t1 - t, v, u);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            sk[i] = skip * cvt_raw1<IOT>(x[i]);
+            gate[i] = cvt_raw1<IOT>(z[i]);
+        }
+        if (t + kBatch < t1)
+            load(t1 - t - kBatch);
+        // token i's C and token i + 1's B (scalar loads) are on their way while
+        // token i's states are computed; the barriers keep that order
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float cs[kStates], bn[kStates];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                cs[j] = packed[bc + kStates + j];
+            bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                bn[j] = packed[bc + j];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            float y2[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < kStates; ++j) {
+                y2[j & 1] = fmaf(h[j], cs[j], y2[j & 1]);
+                bs[j] = bn[j];
+            }
+            y[i] = y2[0] + y2[1];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (!ONE) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                part[(((buf * s.team + mate) * s.tiles + tile) * kBatch + i) * 64 + lane] = y[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                y[i] = 0.0f;
+                if (i % s.tiles == tile)
+                    for (int k = 0; k < s.tiles; ++k)
+                        y[i] += part[(((buf * s.team + mate) * s.tiles + k) * kBatch + i) * 64 + lane];
+            }
+            buf ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            y[i] += sk[i];
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                y[i] *= silu_hw(gate[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (t + i < t1 && (ONE || i % s.tiles == tile))
+                put<IOT>(o + off[i], y[i]);
+        o += p.out_ts * (kBatch * SZ);
+    }
+    if (p.update && live && t1 == len) {
+#pragma unroll
+        for (int j = 0; j < kStates; ++j)
+            if (tile * kStates + (j & ~3) < p.dstate)
+                st_io(p.state, so + j, h[j], p.state_dtype);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sweep
+// ---------------------------------------------------------------------------
+constexpr int kSub = 16;                // tokens of a wave's part of a step
+constexpr int kVuPitch = 2 * kSub + 4;  // floats: the 16 channels' rows 4 banks apart
+
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// Lane I of each row of 16, in all of the row's lanes.
+template <int I>
+__device__ __forceinline__ float row_lane(float v)
+{
+    const int u = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, 0x150 + I, 0xF, 0xF, true));
+}
+
+// The row with the n-th most tokens (at most 64 rows; ties in order).
+__device__ __forceinline__ int nth_longest(const ScanParams &p, int n)
+{
+    const int i = threadIdx.x & 63;
+    int row, mine = -1, rank = 0;
+    if (i < p.batch)
+        mine = row_tokens(p, i, &row);
+    for (int j = 0; j < p.batch; ++j) {
+        const int other = __builtin_amdgcn_readlane(mine, j);
+        rank += other > mine || (other == mine && j < i);
+    }
+    return __ffsll((unsigned long long)__ballot(i < p.batch && rank == n)) - 1;
+}
+
+// Four adjacent B or C entries of one token as floats.
+template <int BC>
+__device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, float (&v)[4])
+{
+    if constexpr (BC == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = cvt1<0>(raw1<0>(base + off, j, dt), dt);
+    } else {
+        cvt4<BC>(raw4<BC>(base + off, 0, dt), dt, v);
+    }
+}
+
+// A workgroup of WAVES waves sweeps 16 channels through a row's tokens, 16 a wave
+// and step. Lane (r, c)
+// of a wave has four state entries (4r ..) of channel c and the wave 16 of the
+// step's tokens: it runs them from a zero start keeping the 16 decays of each
+// entry, the waves exchange ends and decays through LDS, and every wave runs its
+// tokens again from its true start without any exponential. A token's B and C
+// lie across the 16 lanes of a row and reach its channels by DPP broadcast; its
+// dt' and dt' x go through the wave's own LDS; the sum over dstate is two
+// swap-and-adds that also hand lane (r, c) the outputs of tokens 4r .. 4r + 3,
+// whose x, dt and z it loaded. dstate above 16 repeats the two runs per 16.
+template <typename IOT, typename DTT, int BC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
+    const ScanParams p, int per_group, int blocks, int tiles)
+{
+    extern __shared__ float lds[];
+    // [waves][16][kVuPitch] dt', dt' x; [2][waves][64][8] ends and decays; [2][tiles][64][4] states
+    const int lane = threadIdx.x & 63, r = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float *vu = lds + wave * (16 * kVuPitch);
+    float4 *ends = reinterpret_cast<float4 *>(lds + WAVES * 16 * kVuPitch);
+    float4 *starts = ends + 2 * WAVES * 64 * 2;
+
+    // eight neighbouring blocks, which share cache lines of x, dt, z and out, on
+    // one XCD (workgroups go to the eight XCDs in turn)
+    int id = blockIdx.x;
+    if (id < (int)(gridDim.x & ~63u))
+        id = (id & ~63) + (id & 7) * 8 + ((id >> 3) & 7);
+    const int turn = id / blocks, blk = id - turn * blocks;
+    // rows of uneven lengths start longest first
+    const int b = p.ctx && p.batch <= 64 ? nth_longest(p, turn) : turn;
+    const int g = blk / per_group;
+    const int width = p.dim / p.ngroups;
+    // lanes past the group's last channel repeat it: they store the same values
+    const int d = g * width + min((blk - g * per_group) * 16 + c, width - 1);
+    int row;
+    const int len = row_tokens(p, b, &row);
+
+    constexpr int SZ = sizeof(IOT) == 4 ? 4 : 2, DZ = sizeof(DTT) == 4 ? 4 : 2;
+    using E = typename std::conditional<SZ == 4, uint32_t, uint16_t>::type;
+    using DE = typename std::conditional<DZ == 4, uint32_t, uint16_t>::type;
+    char *out = static_cast<char *>(p.out) + b * p.out_bs * SZ;
+    const uint32_t dx = d * SZ, dd = d * DZ;
+    if (p.out)
+        for (int t = len + wave * 4 + r; t < p.seq_len; t += WAVES * 4)
+            put<IOT>(out + t * p.out_ts * SZ + dx, 0.0f);
+    if (len == 0)
+        return;
+
+    const bool gated = p.z != nullptr;  // absent operands are loaded from a present one and not used
+    const char *xp = static_cast<const char *>(p.x) + b * p.x_bs * SZ;
+    const char *zp = gated ? static_cast<const char *>(p.z) + b * p.z_bs * SZ : xp;
+    const int64_t zts = gated ? p.z_ts : p.x_ts;
+    const char *dp = static_cast<const char *>(p.dt) + b * p.dt_bs * DZ;
+    const int bz = p.bc_dtype == kF32 ? 4 : 2;
+    const char *bp = static_cast<const char *>(p.B) + (b * p.b_bs + (int64_t)g * p.dstate) * bz;
+    const char *cp = p.out ? static_cast<const char *>(p.C) + (b * p.c_bs + (int64_t)g * p.dstate) * bz : bp;
+    const int64_t bts = p.b_ts * bz, cts = (p.out ? p.c_ts : p.b_ts) * bz;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.0f;
+    const float skip = p.D ? p.D[d] : 0.0f;
+    const int64_t so = (int64_t)row * p.row_stride + (int64_t)d * p.dstate;
+
+    // the states at the first step's start
+    for (int k = wave; k < tiles; k += WAVES) {
+        float h[4] = {};
+        const int n0 = k * kStates + r * 4;
+        if (n0 < p.dstate) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = ld_io(p.state, so + n0 + j, p.state_dtype);
+        }
+        starts[k * 64 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+    }
+    int starts_now = 0;  // which of the two copies the step reads; the other gets the next's
+
+    // a lane's byte offsets of its four tokens from the wave's first (host: 16
+    // token strides < 2^32 bytes)
+    const uint32_t xts = (uint32_t)p.x_ts * SZ, gts = (uint32_t)zts * SZ, dts = (uint32_t)p.dt_ts * DZ,
+                   ots = (uint32_t)p.out_ts * SZ;
+    E x[4], z[4];
+    DE dt[4];
+    auto load = [&](int t0) {  // this wave's tokens of the step at t0; past the row: its last
+        const int w0 = min(t0 + wave * kSub, len - 1), most = len - 1 - w0;
+        const char *xw = xp + w0 * p.x_ts * SZ, *zw = zp + w0 * zts * SZ, *dw = dp + w0 * p.dt_ts * DZ;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t t = min(r * 4 + q, most);
+            x[q] = *reinterpret_cast<const E *>(xw + (t * xts + dx));
+            z[q] = *reinterpret_cast<const E *>(zw + (t * gts + dx));
+            dt[q] = *reinterpret_cast<const DE *>(dw + (t * dts + dd));
+        }
+    };
+    load(0);
+    int buf = 0;
+    for (int t0 = 0; t0 < len; t0 += (kSub * WAVES)) {
+        const int w0 = t0 + wave * kSub;  // the wave's first token
+        float xs[4], gate[4], y4[4] = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v = cvt_raw1<DTT>(dt[q]) + bias;
+            if (p.dt_softplus)
+                v = softplus_f32(v);
+            const bool in = w0 + r * 4 + q < len;  // others are neutral: dt' = 0
+            v = in ? v : 0.0f;
+            const float xv = cvt_raw1<IOT>(x[q]);
+            *reinterpret_cast<float2 *>(vu + c * kVuPitch + (r * 4 + q) * 2) =
+                make_float2(v, in ? v * xv : 0.0f);
+            xs[q] = skip * xv;
+            gate[q] = cvt_raw1<IOT>(z[q]);
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (t0 + (kSub * WAVES) < len)
+            load(t0 + (kSub * WAVES));
+        for (int k = 0; k < tiles; ++k) {
+            const int n0 = k * kStates + r * 4, nn = min(n0, p.dstate - 4);
+            const bool own = n0 < p.dstate;
+            const float4 aw = *reinterpret_cast<const float4 *>(p.A + (int64_t)d * p.dstate + nn);
+            const int tok = min(w0 + c, len - 1);  // B and C: lane c has token c of the wave's
+            float bv[4], cv[4];
+            ld_bc4<BC>(bp + tok * bts, nn * bz, p.bc_dtype, bv);
+            ld_bc4<BC>(cp + tok * cts, nn * bz, p.bc_dtype, cv);
+            const float a[4] = {aw.x * kLog2e, aw.y * kLog2e, aw.z * kLog2e, aw.w * kLog2e};
+            const bool real = own && w0 + c < len;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bv[j] = real ? bv[j] : 0.0f;
+                cv[j] = real ? cv[j] : 0.0f;
+            }
+            // from a zero start
+            float dec[kSub][4], h[4] = {}, sum = 0.0f;
+            each_of(
+                [&](auto tt) {
+                    constexpr int t = decltype(tt)::value;
+                    const float2 w = *reinterpret_cast<const float2 *>(vu + c * kVuPitch + t * 2);
+                    sum += w.x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dec[t][j] = __builtin_amdgcn_exp2f(a[j] * w.x);
+                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * w.y);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // keeps the tokens in order, and the registers few
+                },
+                std::make_integer_sequence<int, kSub>());
+            float4 *mine = ends + ((buf * WAVES + wave) * 64 + lane) * 2;
+            mine[0] = make_float4(h[0], h[1], h[2], h[3]);
+            mine[1] = make_float4(__builtin_amdgcn_exp2f(a[0] * sum), __builtin_amdgcn_exp2f(a[1] * sum),
+                                  __builtin_amdgcn_exp2f(a[2] * sum), __builtin_amdgcn_exp2f(a[3] * sum));
+            __syncthreads();
+            // the wave's start
+            const float4 s0 = starts[(starts_now * tiles + k) * 64 + lane];
+            h[0] = s0.x, h[1] = s0.y, h[2] = s0.z, h[3] = s0.w;
+            for (int m = 0; m < wave; ++m) {
+                const float4 e = ends[((buf * WAVES + m) * 64 + lane) * 2];
+                const float4 f = ends[((buf * WAVES + m) * 64 + lane) * 2 + 1];
+                h[0] = fmaf(h[0], f.x, e.x);
+                h[1] = fmaf(h[1], f.y, e.y);
+                h[2] = fmaf(h[2], f.z, e.z);
+                h[3] = fmaf(h[3], f.w, e.w);
+            }
+            buf ^= 1;
+            float y[kSub];
+            each_of(
+                [&](auto tt) {
+                    constexpr int t = decltype(tt)::value;
+                    const float u = vu[c * kVuPitch + t * 2 + 1];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * u);
+                        y[t] = j == 0 ? row_lane<t>(cv[j]) * h[j] : fmaf(row_lane<t>(cv[j]), h[j], y[t]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                },
+                std::make_integer_sequence<int, kSub>());
+            // sums over the four rows: halves, then rows, leaving tokens 4r .. 4r + 3
+            float y8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[i]),
+                                                                __float_as_uint(y[i + 8]), false, false);
+                y8[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(y8[i]),
+                                                                __float_as_uint(y8[i + 4]), false, false);
+                y4[i] += __uint_as_float(w[0]) + __uint_as_float(w[1]);
+            }
+            if (wave == WAVES - 1)
+                starts[((starts_now ^ 1) * tiles + k) * 64 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+        }
+        if (p.out) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v = y4[q] + xs[q];
+                if (gated)
+                    v *= silu_hw(gate[q]);
+                if (w0 + r * 4 + q < len)
+                    put<IOT>(out + w0 * p.out_ts * SZ + ((r * 4 + q) * ots + dx), v);
+            }
+        }
+        starts_now ^= 1;
+    }
+    __syncthreads();
+    if (p.update) {
+        for (int k = wave; k < tiles; k += WAVES) {
+            const int n0 = k * kStates + r * 4;
+            const float4 s0 = starts[(starts_now * tiles + k) * 64 + lane];
+            const float h[4] = {s0.x, s0.y, s0.z, s0.w};
+            if (n0 < p.dstate) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_io(p.state, so + n0 + j, h[j], p.state_dtype);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// Dynamic LDS above the default 64 KiB is allowed once per kernel and device.
+hipError_t raise_lds(const void *kernel, int bytes, std::atomic<uint64_t> *raised)
+{
+    if (bytes <= 65536)
+        return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess || (dev < 64 && ((raised->load(std::memory_order_relaxed) >> dev) & 1)))
+        return e;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 98304);
+    if (e == hipSuccess && dev < 64)
+        raised->fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
+template <typename IOT, typename DTT>
+hipError_t launch_chunks(const ScanParams &p, const ScanPlan &q, hipStream_t stream)
+{
+    const ChunkShape &s = q.s;
+    const int64_t cells = (int64_t)p.batch * s.blocks * ((s.chunks + s.team - 1) / s.team);
+    const int64_t packed = q.bc_floats / 2 - kStates;
+    if (cells > 0x7fffffff || (packed + 255) / 256 > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(ssu_scan_pack_kernel, dim3((unsigned)((packed + 255) / 256)), dim3(256), 0,
+                       stream, p, s, packed);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && (s.chunks > 1 || !p.out)) {
+        hipLaunchKernelGGL((ssu_scan_ends_kernel<IOT, DTT>), dim3((unsigned)cells, s.tiles),
+                           dim3(64 * s.team), 0, stream, p, s, s.bc);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess)
+        return e;
+    if (!p.out) {
+        hipLaunchKernelGGL(ssu_scan_last_kernel, dim3((unsigned)(p.batch * s.blocks), s.tiles),
+                           dim3(1024), 0, stream, p, s);
+        return hipGetLastError();
+    }
+    const int lds = 4 * 64 * s.team * s.tiles *
+                    ((s.chunks > 1 ? kStates : 0) + (s.tiles > 1 ? 2 * kBatch : 0));
+    if (s.tiles == 1) {
+        hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOT, DTT, true>), dim3((unsigned)cells),
+                           dim3(64 * s.team), lds, stream, p, s, s.bc, p.out);
+        return hipGetLastError();
+    }
+    static std::atomic<uint64_t> raised{0};
+    e = raise_lds(reinterpret_cast<const void *>(ssu_scan_tokens_kernel<IOT, DTT, false>), lds, &raised);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((ssu_scan_tokens_kernel<IOT, DTT, false>), dim3((unsigned)cells),
+                       dim3(64 * s.tiles * s.team), lds, stream, p, s, s.bc, p.out);
+    return hipGetLastError();
+}
+
+template <typename IOT, typename DTT, int BC, int WAVES>
+hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
+{
+    const int per_group = (p.dim / p.ngroups + 15) / 16, blocks = per_group * p.ngroups;
+    const int tiles = (p.dstate + kStates - 1) / kStates;
+    if ((int64_t)p.batch * blocks > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    const int lds = 4 * (WAVES * 16 * kVuPitch + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4);
+    const auto kernel = ssu_scan_sweep_kernel<IOT, DTT, BC, WAVES>;
+    static std::atomic<uint64_t> raised{0};
+    const hipError_t e = raise_lds(reinterpret_cast<const void *>(kernel), lds, &raised);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.batch * blocks)), dim3(64 * WAVES), lds, stream,
+                       p, per_group, blocks, tiles);
+    return hipGetLastError();
+}
+
+template <typename IOT, typename DTT, int BC>
+hipError_t launch_sweep_waves(const ScanParams &p, int waves, hipStream_t stream)
+{
+    switch (waves) {
+    case 4: return launch_sweep<IOT, DTT, BC, 4>(p, stream);
+    case 8: return launch_sweep<IOT, DTT, BC, 8>(p, stream);
+    default: return launch_sweep<IOT, DTT, BC, 16>(p, stream);
+    }
+}
+
+template <typename IOT, typename DTT>
+hipError_t launch_prompt(const ScanParams &p, const ScanPlan &q, hipStream_t stream)
+{
+    if (!q.sweep)
+        return launch_chunks<IOT, DTT>(p, q, stream);
+    const int es = p.bc_dtype == kF32 ? 4 : 2;
+    auto vec = [&](const void *m, int64_t bs, int64_t ts) {
+        return (uintptr_t)m % (4 * es) == 0 && bs % 4 == 0 && ts % 4 == 0;
+    };
+    if (!vec(p.B, p.b_bs, p.b_ts) || (p.out && !vec(p.C, p.c_bs, p.c_ts)))
+        return launch_sweep_waves<IOT, DTT, 0>(p, q.sweep, stream);
+    return es == 4 ? launch_sweep_waves<IOT, DTT, 4>(p, q.sweep, stream)
+                   : launch_sweep_waves<IOT, DTT, 2>(p, q.sweep, stream);
+}
+
+template <typename IOT>
+hipError_t launch_prompt_dt(const ScanParams &p, const ScanPlan &q, hipStream_t stream)
+{
+    switch (p.dt_dtype) {
+    case kF32: return launch_prompt<IOT, float>(p, q, stream);
+    case kF16: return launch_prompt<IOT, _Float16>(p, q, stream);
+    default: return launch_prompt<IOT, bf16_t>(p, q, stream);
+    }
+}
+
+}  // namespace
+}  // namespace ssu

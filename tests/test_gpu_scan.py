@@ -153,6 +153,69 @@ def test_many_workgroups(batch, seq_len, dim, dstate):
     run_both(scan_inputs(10, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate))
 
 
+# The library picks one of three evaluations by sizes. These reach, in order: rows
+# of many and of few tokens; sweeping workgroups of 4, 8 and 16 waves, with one
+# and several tiles of 16 states; chunks with one and several tiles, in teams of
+# 4, 2 and 1.
+EVALUATIONS = [(64, 20, 640, 16), (2, 16, 70, 40), (64, 60, 48, 16), (6, 70, 500, 16), (3, 120, 90, 16),
+               (4, 200, 33, 16), (70, 33, 40, 8), (20, 40, 130, 20), (2, 129, 64, 48), (1, 250, 48, 100),
+               (1, 1900, 40, 16), (2, 2000, 90, 12), (1, 1850, 3, 16), (1, 600, 70, 64), (2, 300, 48, 128),
+               (1, 290, 33, 256), (1, 280, 20, 200)]
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", EVALUATIONS)
+@pytest.mark.parametrize("kind", ["f32", "mixed", "commit", "window"])
+def test_every_evaluation(batch, seq_len, dim, dstate, kind):
+    """Uneven lengths (0, 1, all, too many among them), padding rows, strided
+    views at odd offsets, padded pool rows; outputs and states; nothing read past
+    a row's end."""
+    g = np.random.default_rng(seq_len)
+    ctx = g.integers(0, seq_len + 1, batch)
+    ctx[0] = seq_len if batch < 3 else seq_len + 7
+    if batch > 2:
+        ctx[1], ctx[2] = 0, 1
+    idx = g.permutation(batch + 2)[:batch]
+    if batch > 3:
+        idx[3] = -4
+    T = scan_inputs(seq_len + dim, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate,
+                    io="f32" if kind == "f32" else "bf16", dt="f32" if kind == "f32" else "bf16",
+                    st="f16" if kind == "mixed" else "f32", ctx=ctx.tolist(), idx=idx.tolist(),
+                    wide=3 if kind == "mixed" else 4, row_pad=16, gate=kind != "f32")
+    for b in range(batch):
+        n = 0 if idx[b] < 0 else min(int(ctx[b]), seq_len)
+        for k in ("x", "z", "dt", "B", "C"):
+            if T[k] is not None:
+                T[k][b, n:] = float("nan")
+    run_both(T, update=kind != "window", with_out=kind != "commit")
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,groups,dstate", [(8, 64, 320, 4, 16), (1, 1900, 45, 3, 16),
+                                                             (2, 300, 50, 2, 128), (40, 20, 60, 5, 16),
+                                                             (1, 200, 96, 6, 32)])
+def test_groups_in_every_evaluation(batch, seq_len, dim, groups, dstate):
+    run_both(scan_inputs(5, batch=batch, seq_len=seq_len, dim=dim, groups=groups, dstate=dstate, io="f16"))
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [(1, 1900, 40, 16), (6, 70, 500, 16), (2, 300, 48, 128)])
+def test_infinite_state_entries_stay_where_they_are(batch, seq_len, dim, dstate):
+    """An infinite entry of one channel's state touches that channel alone, and
+    tokens past a row's end leave every entry, finite or not."""
+    T = scan_inputs(6, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate, io="f32", gate=False,
+                    ctx=[seq_len - 5] * batch)
+    row = int(T["idx"][0])
+    clean = {**T, "state": T["state"].clone()}
+    want = run_both(clean)
+    T["A"][7, 2] = 0.0  # a decay of exactly 1
+    T["state"][row, 7, 2] = float("inf")
+    out = torch.empty_like(T["x"])
+    call(T, out)
+    torch.cuda.synchronize()
+    assert torch.isinf(T["state"][row, 7, 2])
+    keep = [c for c in range(dim) if c != 7]
+    assert_bitwise(out[0][:, keep].contiguous(), want[0][:, keep].contiguous(), "other channels")
+    assert not torch.isnan(T["state"][row][keep]).any()
+
+
 @pytest.mark.parametrize("dstate", [4, 16, 24, 64, 256])
 @pytest.mark.parametrize("io,dt,st", [("bf16", "bf16", "f32"), ("f32", "f32", "f16"),
                                       ("f16", "f32", "bf16")])
