@@ -709,6 +709,9 @@ def _fail(msg):
     raise ValueError(msg)
 
 
+_DENSE = (0, 0)
+
+
 def _outer(stride, shape, name, step):
     """(batch stride, token stride) of an activation [batch, (tokens,) *row] for the
     C call, 0 where the axis has one entry; rows must be dense, the outer axes may
@@ -731,46 +734,48 @@ def _outer(stride, shape, name, step):
     return bs, ts
 
 
-def _view(t, name, dtype, shape, device, step):
-    """_outer of an activation after its checks."""
-    if t.device != device or t.dtype is not dtype or t.shape != shape:
-        _fail(f"{name}: expected a {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
-              f"{tuple(t.shape)} on {t.device}")
-    return _outer(t.stride(), shape, name, step)
+def _bad(t, name, kind, dtype, shape, dev):
+    _fail(f"{name}: expected a {kind}{dtype} tensor {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+          f"{tuple(t.shape)} on {t.device}")
 
 
-def _vector(t, name, dtype, shape, device):
-    """Address of a dense tensor (0 if absent) after its checks."""
+def _view(t, name, dtype, shape, dev, step):
+    """_outer of an activation after its checks ((0, 0) where it is contiguous)."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _bad(t, name, "", dtype, shape, dev)
+    return _DENSE if t.is_contiguous() else _outer(t.stride(), shape, name, step)
+
+
+def _vector(t, name, dtype, shape, dev):
+    """Address of a dense tensor after its checks (0 where there is none)."""
     if t is None:
         return 0
-    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _fail(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
-              f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _bad(t, name, "contiguous ", dtype, shape, dev)
     return t.data_ptr()
 
 
 def _first(t, name, dims, what):
-    """Device of a call's first tensor after its checks."""
+    """Device index of a call's first tensor after its checks."""
     if not t.is_cuda:
         _fail(f"{name} must be a GPU tensor")
-    if t.dtype not in _DT or t.dtype is torch.uint8 or t.dim() != dims:
+    if t.dtype not in _FLOAT or t.dim() != dims:
         _fail(f"{name} must be {what}, fp32, fp16 or bf16")
-    return t.device
+    return t.get_device()
 
 
-def _raw_stream(device, stream):
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _launch(device, fn, *args):
-    """fn(*args) with `device` current; a failure raises."""
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args)
+def _launch(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current; a failure raises."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args)
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
     if rc != SSU_OK:
         _check(rc)
 
@@ -778,40 +783,39 @@ def _launch(device, fn, *args):
 def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
                state_indices, stream, step):
     lib = _LIB or load_library()
-    device = _first(x, "x", 2 if step else 3, "[batch, channels]" if step else
-                    "[batch, seq_len, channels]")
+    dev = _first(x, "x", 2 if step else 3, "[batch, channels]" if step else
+                 "[batch, seq_len, channels]")
     shape, dtype = x.shape, x.dtype
     batch, channels = shape[0], shape[-1]
-    xs = _outer(x.stride(), shape, "x", step)
-    os_ = (0, 0) if out is None else _view(out, "out", dtype, shape, device, step)
+    xs = _DENSE if x.is_contiguous() else _outer(x.stride(), shape, "x", step)
+    os_ = _DENSE if out is None else _view(out, "out", dtype, shape, dev, step)
     if weight.dim() != 2 or weight.shape[0] != channels or weight.dtype not in _FLOAT:
         _fail("weight must be [channels, width], fp32, fp16 or bf16")
     wdt = weight.dtype
     width = weight.shape[1]
-    wp = _vector(weight, "weight", wdt, weight.shape, device)
-    bp = _vector(bias, "bias", wdt, (channels,), device)
+    wp = _vector(weight, "weight", wdt, weight.shape, dev)
+    bp = _vector(bias, "bias", wdt, (channels,), dev)
     if conv_state is not None:
         sdt, rows, ss, sp = (conv_state.dtype, conv_state.shape[0], conv_state.stride(),
                              conv_state.data_ptr())
-        if (conv_state.device != device or conv_state.dim() != 3 or sdt not in _FLOAT
+        if (conv_state.get_device() != dev or conv_state.dim() != 3 or sdt not in _FLOAT
                 or conv_state.shape[1] != channels or conv_state.shape[2] != width - 1):
-            _fail(f"conv_state must be a [rows, {channels}, {width - 1}] view on {device}")
+            _fail(f"conv_state must be a [rows, {channels}, {width - 1}] view on cuda:{dev}")
     else:
         if width != 1:
             _fail("conv_state is required")
         rows, sdt, ss, sp = batch, dtype, (0, 0, 0), 0
-    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), device)
+    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), dev)
     d = ssu_conv_dims(batch, channels, width, rows, _DT[dtype], _DT[wdt], _DT[sdt], 0, *xs, *os_,
                       *ss)
-    st = _raw_stream(device, stream)
     op = 0 if out is None else out.data_ptr()
     if step:
-        _launch(device, lib.ssu_conv_decode, d, x.data_ptr(), wp, bp, sp, op, 1 if silu else 0, ip,
-                st)
+        _launch(dev, stream, lib.ssu_conv_decode, d, x.data_ptr(), wp, bp, sp, op,
+                1 if silu else 0, ip)
     else:
-        cp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), device)
-        _launch(device, lib.ssu_conv_prefill, d, shape[1], x.data_ptr(), wp, bp, sp, op,
-                1 if silu else 0, 1 if update_state else 0, cp, ip, st)
+        cp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), dev)
+        _launch(dev, stream, lib.ssu_conv_prefill, d, shape[1], x.data_ptr(), wp, bp, sp, op,
+                1 if silu else 0, 1 if update_state else 0, cp, ip)
     return out
 
 
@@ -840,7 +844,7 @@ def ssu_conv_decode(x, weight, bias, conv_state, out, *, silu=True, state_indice
 def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
                context_lengths, state_indices, workspace, stream, step):
     lib = _LIB or load_library()
-    device = _first(x, "x", 2 if step else 3, "[batch, dim]" if step else "[batch, seq_len, dim]")
+    dev = _first(x, "x", 2 if step else 3, "[batch, dim]" if step else "[batch, seq_len, dim]")
     shape, dtype = x.shape, x.dtype
     batch, dim = shape[0], shape[-1]
     bshape, bdt, ddt, sdt = B.shape, B.dtype, dt.dtype, state.dtype
@@ -850,51 +854,50 @@ def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_st
         _fail("B must be [batch, ngroups, dstate]" if step else
               "B must be [batch, seq_len, ngroups, dstate]")
     ngroups, dstate = bshape[-2], bshape[-1]
-    xs = _outer(x.stride(), shape, "x", step)
-    ds = _view(dt, "dt", ddt, shape, device, step)
-    bs = _view(B, "B", bdt, bshape, device, step)
-    cs = zs = os_ = (0, 0)
+    xs = _DENSE if x.is_contiguous() else _outer(x.stride(), shape, "x", step)
+    ds = _view(dt, "dt", ddt, shape, dev, step)
+    bs = _view(B, "B", bdt, bshape, dev, step)
+    cs = zs = os_ = _DENSE
     cp = zp = op = 0
     if C is not None:
-        cs, cp = _view(C, "C", bdt, bshape, device, step), C.data_ptr()
+        cs, cp = _view(C, "C", bdt, bshape, dev, step), C.data_ptr()
     if z is not None:
-        zs, zp = _view(z, "z", dtype, shape, device, step), z.data_ptr()
+        zs, zp = _view(z, "z", dtype, shape, dev, step), z.data_ptr()
     if out is not None:
         if C is None:
             _fail("C is required")
-        os_, op = _view(out, "out", dtype, shape, device, step), out.data_ptr()
+        os_, op = _view(out, "out", dtype, shape, dev, step), out.data_ptr()
     f32 = torch.float32
-    ap = _vector(A, "A", f32, (dim, dstate), device)
-    hp = _vector(dt_bias, "dt_bias", f32, (dim,), device)
-    kp = _vector(D, "D", f32, (dim,), device)
+    ap = _vector(A, "A", f32, (dim, dstate), dev)
+    hp = _vector(dt_bias, "dt_bias", f32, (dim,), dev)
+    kp = _vector(D, "D", f32, (dim,), dev)
     sshape, st = state.shape, state.stride()
-    if (state.device != device or len(sshape) != 3 or sshape[1] != dim or sshape[2] != dstate):
-        _fail(f"state must be [rows, {dim}, {dstate}] on {device}, got {tuple(sshape)} on "
+    if (state.get_device() != dev or len(sshape) != 3 or sshape[1] != dim or sshape[2] != dstate):
+        _fail(f"state must be [rows, {dim}, {dstate}] on cuda:{dev}, got {tuple(sshape)} on "
               f"{state.device}")
     rows = sshape[0]
     if (st[2] != 1 and dstate > 1) or (st[1] != dstate and dim > 1):
         _fail("state rows must be dense ([dim, dstate] contiguous)")
     if rows > 1 and st[0] < dim * dstate:
         _fail("state row stride too small")
-    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), device)
+    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), dev)
     d = ssu_scan_dims(batch, dim, dstate, ngroups, rows, _DT[sdt], _DT[dtype], _DT[ddt], _DT[bdt],
                       0, st[0] if rows > 1 else 0, *xs, *zs, *os_, *ds, *bs, *cs)
-    sm = _raw_stream(device, stream)
     soft = 1 if dt_softplus else 0
     if step:
-        _launch(device, lib.ssu_scan_decode, d, x.data_ptr(), ap, B.data_ptr(), cp, dt.data_ptr(),
-                hp, kp, zp, state.data_ptr(), op, soft, ip, sm)
+        _launch(dev, stream, lib.ssu_scan_decode, d, x.data_ptr(), ap, B.data_ptr(), cp,
+                dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, ip)
         return out
-    lp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), device)
+    lp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), dev)
     need = lib.ssu_scan_workspace_bytes(d, shape[1])
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
     else:
         _dense(workspace, "workspace", (torch.uint8,))
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _launch(device, lib.ssu_scan_prefill, d, shape[1], x.data_ptr(), ap, B.data_ptr(), cp,
+    _launch(dev, stream, lib.ssu_scan_prefill, d, shape[1], x.data_ptr(), ap, B.data_ptr(), cp,
             dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, 1 if update_state else 0, lp, ip,
-            wp, wn, sm)
+            wp, wn)
     return out
 
 
@@ -953,37 +956,37 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
         _fail("tokens must be a GPU tensor")
     if tokens.dim() != 2:
         _fail("tokens must be [batch, num_tokens]")
-    device, i32, shape, dtype = tokens.device, torch.int32, tokens.shape, target_probs.dtype
+    dev, i32, shape, dtype = tokens.get_device(), torch.int32, tokens.shape, target_probs.dtype
     batch, n = shape
     if dtype not in _FLOAT or target_probs.dim() != 3:
         _fail("target_probs must be [batch, num_tokens, vocab], fp32, fp16 or bf16")
     vocab = target_probs.shape[2]
-    ts = _view(target_probs, "target_probs", dtype, (batch, n, vocab), device, False)
-    ds, qp = (0, 0), 0
+    ts = _view(target_probs, "target_probs", dtype, (batch, n, vocab), dev, False)
+    ds, qp = _DENSE, 0
     if draft_probs is not None:
-        ds = _view(draft_probs, "draft_probs", dtype, (batch, n - 1, vocab), device, False)
+        ds = _view(draft_probs, "draft_probs", dtype, (batch, n - 1, vocab), dev, False)
         qp = draft_probs.data_ptr()
         if n == 1:
             qp = 0  # no row
-    tp = _vector(tokens, "tokens", i32, shape, device)
-    up = _vector(uniforms, "uniforms", torch.float32, shape, device)
-    pp = _vector(parent_ids, "parent_ids", i32, shape, device)
-    cp = _vector(context_lengths, "context_lengths", i32, (batch,), device)
-    ip = _vector(state_indices, "state_indices", i32, (batch,), device)
-    ap = _vector(accepted_lengths, "accepted_lengths", i32, (batch,), device)
-    np_ = _vector(next_tokens, "next_tokens", i32, (batch,), device)
+    tp = _vector(tokens, "tokens", i32, shape, dev)
+    up = _vector(uniforms, "uniforms", torch.float32, shape, dev)
+    pp = _vector(parent_ids, "parent_ids", i32, shape, dev)
+    cp = _vector(context_lengths, "context_lengths", i32, (batch,), dev)
+    ip = _vector(state_indices, "state_indices", i32, (batch,), dev)
+    ap = _vector(accepted_lengths, "accepted_lengths", i32, (batch,), dev)
+    np_ = _vector(next_tokens, "next_tokens", i32, (batch,), dev)
     most = kp = 0
     if accepted_node_ids is not None:
         most = accepted_node_ids.shape[-1]
-        kp = _vector(accepted_node_ids, "accepted_node_ids", i32, (batch, most), device)
+        kp = _vector(accepted_node_ids, "accepted_node_ids", i32, (batch, most), dev)
     d = ssu_verify_dims(batch, n, vocab, most, _DT[dtype], 0, *ts, *ds)
     if workspace is None:
         workspace = torch.empty(max(int(lib.ssu_verify_workspace_bytes(d)), 16), dtype=torch.uint8,
-                                device=device)
+                                device=tokens.device)
     else:
         _dense(workspace, "workspace", (torch.uint8,))
-    _launch(device, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip, ap, kp,
-            np_, workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream))
+    _launch(dev, stream, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip,
+            ap, kp, np_, workspace.data_ptr(), workspace.numel())
     return accepted_lengths, next_tokens
 
 
