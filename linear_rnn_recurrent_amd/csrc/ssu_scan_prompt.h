@@ -699,7 +699,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-// Dynamic LDS above the default 64 KiB is allowed once per kernel and device.
+// Dynamic LDS above the default 64 KiB (up to a CU's 160) is allowed once per
+// kernel and device.
 hipError_t raise_lds(const void *kernel, int bytes, std::atomic<uint64_t> *raised)
 {
     if (bytes <= 65536)
@@ -708,7 +709,7 @@ hipError_t raise_lds(const void *kernel, int bytes, std::atomic<uint64_t> *raise
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess || (dev < 64 && ((raised->load(std::memory_order_relaxed) >> dev) & 1)))
         return e;
-    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 98304);
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
     if (e == hipSuccess && dev < 64)
         raised->fetch_or(1ull << dev, std::memory_order_relaxed);
     return e;

@@ -780,6 +780,21 @@ def _launch(dev, stream, fn, *args):
         _check(rc)
 
 
+def _scratch(workspace, need, device, stream):
+    """The caller's workspace, or one of `need` bytes for this call on `stream`; returns
+    (address, bytes)."""
+    if workspace is None:
+        if need <= 0:
+            return 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:  # the allocator frees it for the current stream alone
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device)
+                                    if isinstance(stream, int) else stream)
+    else:
+        _dense(workspace, "workspace", (torch.uint8,))
+    return workspace.data_ptr(), workspace.numel()
+
+
 def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
                state_indices, stream, step):
     lib = _LIB or load_library()
@@ -889,12 +904,7 @@ def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_st
                 dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, ip)
         return out
     lp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), dev)
-    need = lib.ssu_scan_workspace_bytes(d, shape[1])
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
-    else:
-        _dense(workspace, "workspace", (torch.uint8,))
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    wp, wn = _scratch(workspace, lib.ssu_scan_workspace_bytes(d, shape[1]), x.device, stream)
     _launch(dev, stream, lib.ssu_scan_prefill, d, shape[1], x.data_ptr(), ap, B.data_ptr(), cp,
             dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, 1 if update_state else 0, lp, ip,
             wp, wn)
@@ -980,13 +990,9 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
         most = accepted_node_ids.shape[-1]
         kp = _vector(accepted_node_ids, "accepted_node_ids", i32, (batch, most), dev)
     d = ssu_verify_dims(batch, n, vocab, most, _DT[dtype], 0, *ts, *ds)
-    if workspace is None:
-        workspace = torch.empty(max(int(lib.ssu_verify_workspace_bytes(d)), 16), dtype=torch.uint8,
-                                device=tokens.device)
-    else:
-        _dense(workspace, "workspace", (torch.uint8,))
+    wp, wn = _scratch(workspace, max(lib.ssu_verify_workspace_bytes(d), 16), tokens.device, stream)
     _launch(dev, stream, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip,
-            ap, kp, np_, workspace.data_ptr(), workspace.numel())
+            ap, kp, np_, wp, wn)
     return accepted_lengths, next_tokens
 
 

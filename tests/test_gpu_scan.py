@@ -307,3 +307,50 @@ def test_graph_and_other_stream():
     call(T, out, stream=side)
     side.synchronize()
     assert_bitwise(out, ref, "out on another stream")
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [(1, 1900, 40, 16), (2, 300, 48, 128), (3, 40, 2000, 16),
+                                                      (1, 600, 70, 64), (2, 129, 64, 48)])
+def test_prompts_of_every_evaluation_in_a_graph(batch, seq_len, dim, dstate):
+    """Several launches and a workspace of the call's own among them; the commit
+    (no outputs) too."""
+    T = scan_inputs(18, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate)
+    T["ctx"] = torch.full((batch,), seq_len - 3, dtype=torch.int32, device="cuda")
+    start = T["state"].clone()
+    ref, out = torch.empty_like(T["x"]), torch.empty_like(T["x"])
+    ref_state = start.clone()
+    call(T, ref, state=ref_state)
+    call(T, None, state=ref_state)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(T, out)
+        call(T, None)
+    for rep in range(3):
+        T["state"].copy_(start)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert_bitwise(out, ref, f"out, replay {rep}")
+        assert_bitwise(T["state"], ref_state, f"state, replay {rep}")
+        del junk
+
+
+def test_two_streams_at_once_with_workspaces_of_their_own():
+    A = [scan_inputs(19 + i, batch=1, seq_len=1900, dim=200, dstate=16) for i in range(2)]
+    want, outs = [], [torch.empty_like(a["x"]) for a in A]
+    for a in A:
+        o = torch.empty_like(a["x"])
+        call(a, o, state=a["state"].clone())
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in A]
+    for _ in range(3):
+        states = [a["state"].clone() for a in A]
+        torch.cuda.synchronize()
+        for a, o, st, s in zip(A, outs, states, streams):
+            call(a, o, state=st, stream=s)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert_bitwise(o, w, "out")

@@ -147,6 +147,38 @@ def test_residual_without_mass_and_rows_without_mass():
     assert want[1][0] >= 0 and want[1][1:].tolist() == [-1, -1, -1]
 
 
+def test_large_vocabularies_take_two_launches():
+    """Over 65536 entries: the sums in a launch of their own; residuals without
+    mass, rows without mass, bounded paths and padding there too."""
+    for probs, wide in (("f32", 0), ("bf16", 3)):
+        T = verify_inputs(33, batch=6, tokens=4, vocab=70001, probs=probs, wide=wide,
+                          ctx=[4, 0, 4, 4, 4, 1], idx=[0, 1, -1, 2, 3, 4])
+        T["draft"][3] = T["target"][3, :-1] * 2
+        T["uniforms"][3, 1:] = 0.75
+        T["target"][4] = 0.0
+        run_both(T)
+        run_both(T, most=2)
+    T = verify_inputs(34, batch=3, tokens=20, vocab=66000, tree=True)
+    T["parents"][1, 1:] = 0
+    run_both(T)
+    run_both(T, most=2)
+    run_both(verify_inputs(35, batch=2, tokens=100, vocab=65537, draft=False, sharp=9.0))
+
+
+def test_large_vocabulary_in_a_graph():
+    T = verify_inputs(36, batch=4, tokens=5, vocab=90000)
+    want = run_both(T)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        acc, nxt, ids = call(T)
+    for rep in range(3):
+        acc.fill_(9), nxt.fill_(9), ids.fill_(9)
+        g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((acc, nxt, ids), want):
+            np.testing.assert_array_equal(f64(got), ref)
+
+
 def test_numbers_at_the_ends():
     """u = 0 draws the first entry with mass, u just below 1 the last with any."""
     T = verify_inputs(24, batch=4, tokens=1, vocab=9000, draft=False)
