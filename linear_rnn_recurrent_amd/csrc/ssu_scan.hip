@@ -13,7 +13,7 @@
 //
 // Sweep (ssu_scan_prompt.h; prompts with channels enough to fill the GPU): a
 // workgroup takes 16 channels through the tokens, its waves side by side along
-// them. Every wave runs its 16 tokens of a step from a zero start, keeping the
+// them. Every wave runs its 8 or 16 tokens of a step from a zero start, keeping the
 // decays in registers; the ends meet in LDS; then the tokens run again from
 // their true start. Per token, channel and state entry that is a product, an
 // exponential at half rate, two products with B and two multiply-adds for the
@@ -45,36 +45,60 @@ hipError_t launch_scan_prompt_bf16(const ScanParams &p, const ScanPlan &q, hipSt
 
 namespace {
 
-// Estimated microseconds of the three evaluations, fitted to measurements (bf16,
-// 1 to 64 rows, 5 to 2048 tokens, 160 to 5120 channels, dstate 16 to 256; most
-// within 15%, some within 30%): `mega` counts 1e6 state entries and tokens.
-double rows_us(int64_t seq_len, double mega)
+// Estimated microseconds of the three evaluations, fitted to measurements of each
+// at 37 sizes (bf16, 1 to 64 rows, 17 to 8192 tokens, 160 to 8192 channels, dstate
+// 16 to 256: nearly all within 25%; where B and C are not aligned to four entries
+// rows take twice as long and sweeps a quarter longer). `mega` counts 1e6 state
+// entries and tokens, `tiles` the sixteens of dstate. Rows of uneven lengths, an
+// eighth of seq_len up, take a share of it: the sweep's, longest first and in short
+// steps, least; of the chunks' many end up empty or cut.
+double rows_us(bool ragged, int64_t seq_len, double mega)
 {
-    return 2.0 + fmax(0.27 * seq_len, 0.58 * mega);  // a token's latency, or the vector ALU
+    // a token's latency, or the vector ALU
+    return (5.0 + fmax(0.285 * seq_len, 0.57 * mega)) * (ragged ? 0.85 : 1.0);
 }
 
-// Sweeping workgroups of `waves` waves, 16 waves a CU: a step takes 4 us on a CU
-// with 4 waves and 8 us with 16.
-double sweep_us(int waves, int64_t blocks, int64_t tiles, int64_t seq_len)
+// Sweeping workgroups of `waves` waves; a CU holds 16 waves, or as many workgroups
+// as its LDS does.
+double sweep_us(int waves, bool ragged, int64_t blocks, int64_t tiles, int64_t seq_len)
 {
-    const int64_t steps = (seq_len + 16 * waves - 1) / (16 * waves) * tiles;
-    const int64_t slots = 256 * (16 / waves), rest = blocks % slots;
-    auto step = [](int64_t w) { return 2.6 + 0.34 * w; };
-    const double rounds = (blocks / slots) * step(16) + (rest ? step(waves * ((rest + 255) / 256)) : 0.0);
-    return 3.0 + steps * rounds * (waves == 16 ? 1.08 : waves == 8 ? 1.0 : 0.92);
+    const int64_t sub = sweep_tokens(waves), steps = (seq_len + sub * waves - 1) / (sub * waves);
+    const int64_t lds = 4 * (waves * 16 * (2 * sub + 4) + waves * 1024 + tiles * 512);
+    const int64_t fit = 163840 / lds, per_cu = fit < 16 / waves ? (fit < 1 ? 1 : fit) : 16 / waves;
+    const int64_t slots = 256 * per_cu, rest = blocks % slots;
+    auto step = [](int64_t w) { return 3.15 + 0.27 * w; };  // w waves on a CU
+    const double rounds = (blocks / slots) * step(per_cu * waves) +
+                          (rest ? step(waves * ((rest + 255) / 256)) : 0.0);
+    const double body = steps * (0.3 + 0.7 * tiles);
+    if (waves == 4)
+        return 3.0 + rounds * (0.1 + body) * (ragged ? 0.32 : 0.51);
+    if (waves == 8)
+        return 3.0 + rounds * (0.08 + body) * (ragged ? 0.75 : 1.0);
+    return 3.0 + rounds * (0.19 + body) * (ragged ? 0.89 : 1.11);
 }
 
-double chunks_us(int64_t tiles, double mega)
+double chunks_us(bool cut, bool ragged, int64_t tiles, int64_t seq_len, double mega)
 {
-    return tiles > 1 ? 60.0 + 0.33 * mega : fmax(45.0, fmax(30.0 + 0.45 * mega, 0.62 * mega));
+    const double us = cut ? 41.0 + (tiles > 1 ? 0.555 : 0.4) * mega
+                          : 16.5 + fmax(0.35 * seq_len, 0.31 * mega);
+    return us * (ragged ? 0.8 : 1.0);
 }
 
 // Which evaluation a call takes, and its cut: the one with the least estimate.
 // Measured (us, rows | sweep of 4, 8, 16 waves | chunks):
-//   64 x 32 x 2560      47 | 75, 139, 369 | 47     8 x 64 x 2560  26 | 17, 24, - | -
-//   16 x 256 x 1024     76 | 35, 36, 45   | 57     1 x 512 x 1536  - | 36, 25, 21 | 46
-//   4 x 512 x 2560       - | 52, 50, 58   | 65     1 x 2048 x 1536 - | 129, 83, 66 | 61
-//   1 x 2048 x 5120      - | 158, 126, 139 | 102   2 x 509 x 1536, dstate 64: 96, 65, 57 | 80
+//   64 x 32 x 2560                 48 | 45, 141, 368   | 47
+//   8 x 64 x 2560                  26 | 14, 24, 50     | 48
+//   16 x 256 x 1024                76 | 36, 36, 46     | 57
+//   4 x 512 x 2560                144 | 54, 51, 58     | 65
+//   1 x 512 x 1536                128 | 38, 25, 21     | 47
+//   1 x 2048 x 1536               554 | 140, 84, 66    | 62
+//   1 x 2048 x 5120               592 | 178, 127, 140  | 110
+//   64 x 64 x 5120                173 | 154, 308, 772  | 129
+//   2 x 509 x 1536, dstate 64     148 | 112, 67, 59    | 82
+//   4 x 512 x 2560, dstate 64     245 | 173, 147, 162  | 245
+//   8 x 777 x 2560, uneven        182 | 59, 71, 93     | 86
+//   64 x 500 x 1024, uneven       266 | 149, 202, 303  | 237
+//   1 x 4096 x 1024, dstate 128  1714 | 1583, 927, 763 | 365
 // Chunks are as long as leaves about three waves for each of the GPU's 1,024
 // SIMDs: every chunk costs its end, its fold and 4 KiB of traffic, and too few
 // leave SIMDs idle (1 x 2048 x 5120: 113 us at 2,560 waves, 102 at 3,072, 104 at
@@ -88,22 +112,19 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     const int64_t tiles = (dstate + kStates - 1) / kStates;
     const int64_t blocks = batch * ngroups * ((dim / ngroups + 15) / 16);
     const double mega = 1e-6 * (double)batch * (double)dim * (double)(tiles * kStates) * (double)seq_len;
-    double best = rows_us(seq_len, mega);
+    int64_t held = 4;  // states that a channel's lanes hold: a power of two
+    while (held < dstate)
+        held *= 2;
+    double best = rows_us(ragged, seq_len, mega * held / (tiles * kStates));
     q.rows = true;
-    for (int waves = 4; waves <= 16; waves *= 2) {
-        // rows of uneven lengths suit the sweep, longest first, more than chunks
-        // that rows end inside (8 x 777 x 2560: 62 | 86 us)
-        const double us = sweep_us(waves, blocks, tiles, seq_len) * (ragged ? 0.7 : 1.0);
-        if (seq_len > 1 && us < best) {
+    for (int waves = 4; waves <= 16 && seq_len > 1; waves *= 2) {
+        const double us = sweep_us(waves, ragged, blocks, tiles, seq_len);
+        if (us < best) {
             best = us;
             q.rows = false;
             q.sweep = waves;
         }
     }
-    if (seq_len <= 16 || best <= chunks_us(tiles, mega))
-        return q;
-    q.rows = false;
-    q.sweep = 0;
     q.s.tiles = (int32_t)tiles;
     q.s.per_group = (int32_t)((dim / ngroups + 63) / 64);
     q.s.blocks = (int32_t)(q.s.per_group * ngroups);
@@ -114,6 +135,10 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     if (len < 32)
         len = 32;
     chunks = (seq_len + len - 1) / len;
+    if (seq_len <= 16 || best <= chunks_us(chunks > 1, ragged, tiles, seq_len, mega))
+        return q;
+    q.rows = false;
+    q.sweep = 0;
     q.s.chunk = (int32_t)(len > seq_len ? seq_len : len);
     q.s.chunks = (int32_t)chunks;
     const int most = q.s.tiles <= 4 ? 4 : q.s.tiles <= 8 ? 2 : 1;

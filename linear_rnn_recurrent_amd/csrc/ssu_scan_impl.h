@@ -119,6 +119,9 @@ struct ChunkShape {
 };
 
 // How a call is evaluated (scan_plan).
+// Tokens of a sweeping wave and step
+constexpr int sweep_tokens(int waves) { return waves == 4 ? 8 : 16; }
+
 struct ScanPlan {
     bool rows;
     int32_t sweep;  // waves of a sweeping workgroup: 4, 8 or 16; 0: chunks

@@ -436,8 +436,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
 // ---------------------------------------------------------------------------
 // Sweep
 // ---------------------------------------------------------------------------
-constexpr int kSub = 16;                // tokens of a wave's part of a step
-constexpr int kVuPitch = 2 * kSub + 4;  // floats: the 16 channels' rows 4 banks apart
+constexpr int vu_pitch(int sub) { return 2 * sub + 4; }  // floats: the channels on different banks
 
 template <typename F, int... I>
 __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
@@ -480,21 +479,31 @@ __device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, f
     }
 }
 
-// A workgroup of WAVES waves sweeps 16 channels through a row's tokens, 16 a wave
-// and step. Lane (r, c)
-// of a wave has four state entries (4r ..) of channel c and the wave 16 of the
-// step's tokens: it runs them from a zero start keeping the 16 decays of each
-// entry, the waves exchange ends and decays through LDS, and every wave runs its
-// tokens again from its true start without any exponential. A token's B and C
+// A workgroup of WAVES waves sweeps 16 channels through a row's tokens, kSub
+// tokens a wave and step. Lane (r, c) of a wave has four state entries (4r ..) of
+// channel c: it runs the wave's tokens from a zero start keeping the kSub decays of
+// each entry, the waves exchange ends and decays through LDS, and every wave runs
+// its tokens again from its true start without any exponential. A token's B and C
 // lie across the 16 lanes of a row and reach its channels by DPP broadcast; its
 // dt' and dt' x go through the wave's own LDS; the sum over dstate is two
-// swap-and-adds that also hand lane (r, c) the outputs of tokens 4r .. 4r + 3,
+// swap-and-adds that also hand lane (r, c) the outputs of kSub / 4 tokens, those
 // whose x, dt and z it loaded. dstate above 16 repeats the two runs per 16.
+//
+// kSub: 16 spreads a step's exchange over more tokens, 8 wastes less at the rows'
+// ends and holds half the decays. 4 waves are what short and uneven rows take, with
+// 8 (us with 8 | 16: 8 x 777 x 2560 uneven 59 | 64, 32 x 128 x 2560 74 | 83,
+// 4 x 512 x 2560 54 | 52); 8 and 16 waves take longer rows, with 16 (8 waves: 53 |
+// 50, 16 waves: 1 x 2048 x 1536 72 | 66). The vector ALU is busy 69% of the time
+// (8 x 777 x 2560); the rest is the exchange's barriers and the rows' ends. Four
+// waves a SIMD leave the 128 registers that kSub 16 needs: at five it spills (115 us
+// for 64).
 template <typename IOT, typename DTT, int BC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     const ScanParams p, int per_group, int blocks, int tiles)
 {
     extern __shared__ float lds[];
+    constexpr int kSub = sweep_tokens(WAVES);
+    constexpr int kOwn = kSub / 4, kVuPitch = vu_pitch(kSub);  // a lane loads and finishes kOwn tokens
     // [waves][16][kVuPitch] dt', dt' x; [2][waves][64][8] ends and decays; [2][tiles][64][4] states
     const int lane = threadIdx.x & 63, r = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -554,18 +563,18 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     }
     int starts_now = 0;  // which of the two copies the step reads; the other gets the next's
 
-    // a lane's byte offsets of its four tokens from the wave's first (host: 16
+    // a lane's byte offsets of its tokens from the wave's first (host: 16
     // token strides < 2^32 bytes)
     const uint32_t xts = (uint32_t)p.x_ts * SZ, gts = (uint32_t)zts * SZ, dts = (uint32_t)p.dt_ts * DZ,
                    ots = (uint32_t)p.out_ts * SZ;
-    E x[4], z[4];
-    DE dt[4];
+    E x[kOwn], z[kOwn];
+    DE dt[kOwn];
     auto load = [&](int t0) {  // this wave's tokens of the step at t0; past the row: its last
         const int w0 = min(t0 + wave * kSub, len - 1), most = len - 1 - w0;
         const char *xw = xp + w0 * p.x_ts * SZ, *zw = zp + w0 * zts * SZ, *dw = dp + w0 * p.dt_ts * DZ;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t t = min(r * 4 + q, most);
+        for (int q = 0; q < kOwn; ++q) {
+            const uint32_t t = min(r * kOwn + q, most);
             x[q] = *reinterpret_cast<const E *>(xw + (t * xts + dx));
             z[q] = *reinterpret_cast<const E *>(zw + (t * gts + dx));
             dt[q] = *reinterpret_cast<const DE *>(dw + (t * dts + dd));
@@ -573,35 +582,35 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     };
     load(0);
     int buf = 0;
-    for (int t0 = 0; t0 < len; t0 += (kSub * WAVES)) {
+    for (int t0 = 0; t0 < len; t0 += kSub * WAVES) {
         const int w0 = t0 + wave * kSub;  // the wave's first token
-        float xs[4], gate[4], y4[4] = {};
+        float xs[kOwn], gate[kOwn], y4[kOwn] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kOwn; ++q) {
             float v = cvt_raw1<DTT>(dt[q]) + bias;
             if (p.dt_softplus)
                 v = softplus_f32(v);
-            const bool in = w0 + r * 4 + q < len;  // others are neutral: dt' = 0
+            const bool in = w0 + r * kOwn + q < len;  // others are neutral: dt' = 0
             v = in ? v : 0.0f;
             const float xv = cvt_raw1<IOT>(x[q]);
-            *reinterpret_cast<float2 *>(vu + c * kVuPitch + (r * 4 + q) * 2) =
+            *reinterpret_cast<float2 *>(vu + c * kVuPitch + (r * kOwn + q) * 2) =
                 make_float2(v, in ? v * xv : 0.0f);
             xs[q] = skip * xv;
             gate[q] = cvt_raw1<IOT>(z[q]);
         }
         __builtin_amdgcn_wave_barrier();
-        if (t0 + (kSub * WAVES) < len)
-            load(t0 + (kSub * WAVES));
+        if (t0 + kSub * WAVES < len)
+            load(t0 + kSub * WAVES);
         for (int k = 0; k < tiles; ++k) {
             const int n0 = k * kStates + r * 4, nn = min(n0, p.dstate - 4);
             const bool own = n0 < p.dstate;
             const float4 aw = *reinterpret_cast<const float4 *>(p.A + (int64_t)d * p.dstate + nn);
-            const int tok = min(w0 + c, len - 1);  // B and C: lane c has token c of the wave's
+            const int tok = min(w0 + c % kSub, len - 1);  // B and C: lane c has token c of the wave's
             float bv[4], cv[4];
             ld_bc4<BC>(bp + tok * bts, nn * bz, p.bc_dtype, bv);
             ld_bc4<BC>(cp + tok * cts, nn * bz, p.bc_dtype, cv);
             const float a[4] = {aw.x * kLog2e, aw.y * kLog2e, aw.z * kLog2e, aw.w * kLog2e};
-            const bool real = own && w0 + c < len;
+            const bool real = own && w0 + c % kSub < len;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 bv[j] = real ? bv[j] : 0.0f;
@@ -652,18 +661,18 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
                     __builtin_amdgcn_sched_barrier(0);
                 },
                 std::make_integer_sequence<int, kSub>());
-            // sums over the four rows: halves, then rows, leaving tokens 4r .. 4r + 3
-            float y8[8];
+            // sums over the four rows: halves, then rows, leaving the lane's own tokens
+            float y8[2 * kOwn];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 2 * kOwn; ++i) {
                 const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[i]),
-                                                                __float_as_uint(y[i + 8]), false, false);
+                                                                __float_as_uint(y[i + 2 * kOwn]), false, false);
                 y8[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kOwn; ++i) {
                 const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(y8[i]),
-                                                                __float_as_uint(y8[i + 4]), false, false);
+                                                                __float_as_uint(y8[i + kOwn]), false, false);
                 y4[i] += __uint_as_float(w[0]) + __uint_as_float(w[1]);
             }
             if (wave == WAVES - 1)
@@ -671,12 +680,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
         }
         if (p.out) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kOwn; ++q) {
                 float v = y4[q] + xs[q];
                 if (gated)
                     v *= silu_hw(gate[q]);
-                if (w0 + r * 4 + q < len)
-                    put<IOT>(out + w0 * p.out_ts * SZ + ((r * 4 + q) * ots + dx), v);
+                if (w0 + r * kOwn + q < len)
+                    put<IOT>(out + w0 * p.out_ts * SZ + ((r * kOwn + q) * ots + dx), v);
             }
         }
         starts_now ^= 1;
@@ -761,7 +770,7 @@ hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
     const int tiles = (p.dstate + kStates - 1) / kStates;
     if ((int64_t)p.batch * blocks > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    const int lds = 4 * (WAVES * 16 * kVuPitch + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4);
+    const int lds = 4 * (WAVES * 16 * vu_pitch(sweep_tokens(WAVES)) + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4);
     const auto kernel = ssu_scan_sweep_kernel<IOT, DTT, BC, WAVES>;
     static std::atomic<uint64_t> raised{0};
     const hipError_t e = raise_lds(reinterpret_cast<const void *>(kernel), lds, &raised);
@@ -773,9 +782,9 @@ hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
 }
 
 template <typename IOT, typename DTT, int BC>
-hipError_t launch_sweep_waves(const ScanParams &p, int waves, hipStream_t stream)
+hipError_t launch_sweep_waves(const ScanParams &p, const ScanPlan &q, hipStream_t stream)
 {
-    switch (waves) {
+    switch (q.sweep) {
     case 4: return launch_sweep<IOT, DTT, BC, 4>(p, stream);
     case 8: return launch_sweep<IOT, DTT, BC, 8>(p, stream);
     default: return launch_sweep<IOT, DTT, BC, 16>(p, stream);
@@ -792,9 +801,9 @@ hipError_t launch_prompt(const ScanParams &p, const ScanPlan &q, hipStream_t str
         return (uintptr_t)m % (4 * es) == 0 && bs % 4 == 0 && ts % 4 == 0;
     };
     if (!vec(p.B, p.b_bs, p.b_ts) || (p.out && !vec(p.C, p.c_bs, p.c_ts)))
-        return launch_sweep_waves<IOT, DTT, 0>(p, q.sweep, stream);
-    return es == 4 ? launch_sweep_waves<IOT, DTT, 4>(p, q.sweep, stream)
-                   : launch_sweep_waves<IOT, DTT, 2>(p, q.sweep, stream);
+        return launch_sweep_waves<IOT, DTT, 0>(p, q, stream);
+    return es == 4 ? launch_sweep_waves<IOT, DTT, 4>(p, q, stream)
+                   : launch_sweep_waves<IOT, DTT, 2>(p, q, stream);
 }
 
 template <typename IOT>

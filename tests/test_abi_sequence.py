@@ -149,11 +149,12 @@ def test_scan_workspace(lib):
     d = scan_dims(dim=96, ngroups=2, dstate=40)  # long rows of few channels: chunks
     need = lib.ssu_scan_workspace_bytes(d, 1000)
     assert need == S.scan_workspace_bytes(2, 1000, 96, 40, 2) > 4 * 2 * 1000 * 2 * 48 * 2
-    assert lib.ssu_scan_workspace_bytes(scan_dims(batch=64, dim=4096), 200) == 0  # a sweep
+    assert lib.ssu_scan_workspace_bytes(scan_dims(batch=8, dim=2560), 64) == 0  # a sweep
     # the sizes at which the GPU tests mean to reach the chunked evaluation do
     for batch, seq_len, dim, dstate in [(1, 1900, 40, 16), (2, 2000, 90, 12), (1, 1850, 3, 16),
                                         (1, 600, 70, 64), (2, 300, 48, 128), (1, 290, 33, 256),
-                                        (1, 280, 20, 200), (1, 2048, 5120, 16)]:
+                                        (1, 280, 20, 200), (1, 2048, 5120, 16), (32, 20, 4000, 16),
+                                        (32, 17, 600, 100)]:
         assert S.scan_workspace_bytes(batch, seq_len, dim, dstate) > 0
     assert scan(lib, d, seq_len=1000, ws_bytes=need - 1) == 1 and "workspace_bytes" in err(lib)
     assert scan(lib, d, seq_len=1000, ws=None) == 1 and "'workspace'" in err(lib)
