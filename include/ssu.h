@@ -361,8 +361,9 @@ typedef struct ssu_conv_dims {
  * context_lengths = k). out may be NULL when the state is updated (only the
  * state is wanted then). Padding rows: out[b] = +0.0, no pool access.
  * Layouts: x, out [batch, seq_len, channels]; weight [channels, W] and bias
- * [channels] dense. out must not overlap x (x == out is refused). Optional:
- * bias, out, context_lengths, state_indices; conv_state when W == 1. */
+ * [channels] dense. seq_len up to 2^30 (else SSU_ENOTSUP). out must not overlap
+ * x (x == out is refused). Optional: bias, out, context_lengths, state_indices;
+ * conv_state when W == 1. */
 ssu_status ssu_conv_prefill(const ssu_conv_dims *dims, int32_t seq_len, const void *x,
                             const void *weight, const void *bias, void *conv_state, void *out,
                             int32_t silu, int32_t update_state, const int32_t *context_lengths,
@@ -411,7 +412,7 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
                            int32_t dt_softplus, const int32_t *state_indices,
                            hipStream_t stream);
 
-/* ssu_scan_prefill -- seq_len tokens in one launch: row b runs its first
+/* ssu_scan_prefill -- seq_len tokens in one call: row b runs its first
  * L_b = clamp(context_lengths[b], 0, seq_len) tokens through the step of
  * ssu_scan_decode in order; out[b,t] = +0.0 for t >= L_b, where no input is
  * read. x, z, out, dt [batch, seq_len, dim]; B, C [batch, seq_len, ngroups,
@@ -422,7 +423,8 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
  * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
  * call and rounded once, at its end. Long calls run the tokens in chunks side by
  * side: they agree with the token-by-token recurrence to fp32 rounding, not
- * bitwise. dim and the activations' token strides up to 2^25 (else SSU_ENOTSUP).
+ * bitwise. dim and the activations' token strides up to 2^25, seq_len up to 2^30
+ * (else SSU_ENOTSUP). An infinite entry of A acts as the largest finite one.
  * workspace: caller-owned device scratch of at least
  * ssu_scan_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
  * that is 0); contents on entry ignored, on return unspecified; calls sharing a
@@ -471,8 +473,8 @@ typedef struct ssu_verify_dims {
  *   uniforms[b,c] * (1 - removed) < p[x],
  * otherwise removed += p[x] and p[x] = 0 (a token that a sibling tried before
  * has p[x] = 0). When no child is left, or max_accept_len nodes are accepted,
- * the next token is drawn from p as it is then. Either way the drawn tokens follow the
- * target's distribution.
+ * the next token is drawn from p as it is then. Either way the drawn tokens
+ * follow the target's distribution.
  * Drawing from weights w: the lowest v with sum_{i<=v} w_i > uniforms[b,0] *
  * sum_i w_i; weights without mass are replaced by the target row itself, and
  * with no mass there either the token is -1. Negative and NaN weights count
@@ -487,8 +489,8 @@ typedef struct ssu_verify_dims {
  * context_lengths, state_indices, accepted_node_ids.
  * workspace: caller-owned device scratch of at least
  * ssu_verify_workspace_bytes(dims) bytes, 16-byte aligned (partial sums of a
- * large vocabulary, from the first of two launches to the second); contents on entry ignored, on
- * return unspecified; calls sharing a workspace must be ordered (one stream). */
+ * large vocabulary, from the first of two launches to the second); contents on
+ * entry ignored, on return unspecified; calls sharing a workspace must be ordered (one stream). */
 ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
                             const void *target_probs, const void *draft_probs,
                             const float *uniforms, const int32_t *parent_ids,

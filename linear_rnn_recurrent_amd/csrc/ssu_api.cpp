@@ -547,7 +547,8 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
         p.st_row < (d.channels - 1) * p.st_chan + (taps - 1) * p.st_tap + 1)
         return fail(SSU_EINVAL, "%s: conv_state row stride %lld too small", fn,
                     (long long)p.st_row);
-    if ((int64_t)d.batch * ((d.channels + 255) / 256) * ((seq_len + 15) / 16) > 0x7fffffff)
+    if (seq_len > (1 << 30) ||
+        (int64_t)d.batch * ((d.channels + 255) / 256) * ((seq_len + 15) / 16) > 0x7fffffff)
         return fail(SSU_ENOTSUP, "%s: problem too large", fn);
     if (d.batch == 0 || seq_len == 0)
         return ok();
@@ -635,8 +636,8 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
         if (st != SSU_OK)
             return st;
     }
-    if ((int64_t)d.batch * d.dim > 0x7fffffff)
-        return fail(SSU_ENOTSUP, "%s: batch * dim too large", fn);
+    if (seq_len > (1 << 30) || (int64_t)d.batch * d.dim > 0x7fffffff)
+        return fail(SSU_ENOTSUP, "%s: seq_len or batch * dim too large", fn);
     if (p.x_ts > (1 << 25) || p.z_ts > (1 << 25) || p.out_ts > (1 << 25) || p.dt_ts > (1 << 25) ||
         d.dim > (1 << 25))
         return fail(SSU_ENOTSUP, "%s: dim and token strides above 2^25", fn);

@@ -34,6 +34,14 @@ __device__ __forceinline__ float silu_hw(float v)
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
+// A's entry for exp2; an infinite one as the largest finite, which decays as fast
+// and leaves the state where dt' is 0 (tokens behind a row's end).
+__device__ __forceinline__ float log2_rate(float a)
+{
+    const float r = a * kLog2e;
+    return __builtin_isinf(r) ? copysignf(3.402823466e38f, r) : r;
+}
+
 __device__ __forceinline__ int row_tokens(const ScanParams &p, int b, int *row)
 {
     *row = p.idx ? p.idx[b] : b;
@@ -118,10 +126,10 @@ struct ChunkShape {
     float *bc, *start, *sum;
 };
 
-// How a call is evaluated (scan_plan).
 // Tokens of a sweeping wave and step
 constexpr int sweep_tokens(int waves) { return waves == 4 ? 8 : 16; }
 
+// How a call is evaluated (scan_plan).
 struct ScanPlan {
     bool rows;
     int32_t sweep;  // waves of a sweeping workgroup: 4, 8 or 16; 0: chunks

@@ -67,10 +67,10 @@ __device__ __forceinline__ void load_a(const ScanParams &p, int d, int tile, flo
         float4 w = make_float4(0, 0, 0, 0);
         if (tile * kStates + j < p.dstate)
             w = *reinterpret_cast<const float4 *>(p.A + (int64_t)d * p.dstate + tile * kStates + j);
-        a[j] = w.x * kLog2e;
-        a[j + 1] = w.y * kLog2e;
-        a[j + 2] = w.z * kLog2e;
-        a[j + 3] = w.w * kLog2e;
+        a[j] = log2_rate(w.x);
+        a[j + 1] = log2_rate(w.y);
+        a[j + 2] = log2_rate(w.z);
+        a[j + 3] = log2_rate(w.w);
     }
 }
 
@@ -216,7 +216,7 @@ __device__ __forceinline__ void fold_ends(const ScanParams &p, const ChunkShape 
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int n = tile * kStates + j0 + j;
-        a[j] = n < p.dstate ? p.A[(int64_t)q.d * p.dstate + n] * kLog2e : 0.0f;
+        a[j] = n < p.dstate ? log2_rate(p.A[(int64_t)q.d * p.dstate + n]) : 0.0f;
         h[j] = e[j * 64];
     }
     constexpr int F = 32 / NS;  // ends in flight
@@ -609,7 +609,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
             float bv[4], cv[4];
             ld_bc4<BC>(bp + tok * bts, nn * bz, p.bc_dtype, bv);
             ld_bc4<BC>(cp + tok * cts, nn * bz, p.bc_dtype, cv);
-            const float a[4] = {aw.x * kLog2e, aw.y * kLog2e, aw.z * kLog2e, aw.w * kLog2e};
+            const float a[4] = {log2_rate(aw.x), log2_rate(aw.y), log2_rate(aw.z), log2_rate(aw.w)};
             const bool real = own && w0 + c % kSub < len;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

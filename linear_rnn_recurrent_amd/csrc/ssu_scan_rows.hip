@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void ssu_scan_rows_kernel(const ScanParams p, 
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const float xv = cvt1<IO>(x[i], p.io_dtype), u = v[i] * xv;
-        const float a[4] = {aw[i].x * kLog2e, aw[i].y * kLog2e, aw[i].z * kLog2e, aw[i].w * kLog2e};
+        const float a[4] = {log2_rate(aw[i].x), log2_rate(aw[i].y), log2_rate(aw[i].z), log2_rate(aw[i].w)};
         float bv[4], cv[4], acc = 0.0f;
         cvt4<BC>(rb[i], p.bc_dtype, bv);
         cvt4<BC>(rc[i], p.bc_dtype, cv);
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void ssu_scan_window_kernel(const ScanParams p
     float bias = bsrc[d], skip = dsrc[d], h[4];
     bias = p.dt_bias ? bias : 0.0f;
     skip = p.D ? skip : 0.0f;
-    const float a[4] = {aw.x * kLog2e, aw.y * kLog2e, aw.z * kLog2e, aw.w * kLog2e};
+    const float a[4] = {log2_rate(aw.x), log2_rate(aw.y), log2_rate(aw.z), log2_rate(aw.w)};
     cvt_raw4<ST>(hraw, h);
     for (int t0 = 0; t0 < len; t0 += K) {
         float v = cvt1<DT>(dt, p.dt_dtype) + bias;

@@ -762,6 +762,8 @@ def _first(t, name, dims, what):
         _fail(f"{name} must be a GPU tensor")
     if t.dtype not in _FLOAT or t.dim() != dims:
         _fail(f"{name} must be {what}, fp32, fp16 or bf16")
+    if max(t.shape) > 1 << 30:
+        _fail(f"{name} has an axis above 2^30")
     return t.get_device()
 
 
@@ -782,17 +784,18 @@ def _launch(dev, stream, fn, *args):
 
 def _scratch(workspace, need, device, stream):
     """The caller's workspace, or one of `need` bytes for this call on `stream`; returns
-    (address, bytes)."""
+    (tensor, address, bytes). The tensor has to live until the call is launched: freed
+    before, its memory could go to a call on another stream at once."""
     if workspace is None:
         if need <= 0:
-            return 0, 0
+            return None, 0, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:  # the allocator frees it for the current stream alone
             workspace.record_stream(torch.cuda.ExternalStream(stream, device)
                                     if isinstance(stream, int) else stream)
     else:
         _dense(workspace, "workspace", (torch.uint8,))
-    return workspace.data_ptr(), workspace.numel()
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
@@ -816,6 +819,8 @@ def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_len
         if (conv_state.get_device() != dev or conv_state.dim() != 3 or sdt not in _FLOAT
                 or conv_state.shape[1] != channels or conv_state.shape[2] != width - 1):
             _fail(f"conv_state must be a [rows, {channels}, {width - 1}] view on cuda:{dev}")
+        if rows > 1 << 30:
+            _fail("conv_state has more than 2^30 rows")
     else:
         if width != 1:
             _fail("conv_state is required")
@@ -895,6 +900,8 @@ def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_st
         _fail("state rows must be dense ([dim, dstate] contiguous)")
     if rows > 1 and st[0] < dim * dstate:
         _fail("state row stride too small")
+    if rows > 1 << 30:
+        _fail("state has more than 2^30 rows")
     ip = _vector(state_indices, "state_indices", torch.int32, (batch,), dev)
     d = ssu_scan_dims(batch, dim, dstate, ngroups, rows, _DT[sdt], _DT[dtype], _DT[ddt], _DT[bdt],
                       0, st[0] if rows > 1 else 0, *xs, *zs, *os_, *ds, *bs, *cs)
@@ -904,7 +911,7 @@ def _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_st
                 dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, ip)
         return out
     lp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), dev)
-    wp, wn = _scratch(workspace, lib.ssu_scan_workspace_bytes(d, shape[1]), x.device, stream)
+    workspace, wp, wn = _scratch(workspace, lib.ssu_scan_workspace_bytes(d, shape[1]), x.device, stream)
     _launch(dev, stream, lib.ssu_scan_prefill, d, shape[1], x.data_ptr(), ap, B.data_ptr(), cp,
             dt.data_ptr(), hp, kp, zp, state.data_ptr(), op, soft, 1 if update_state else 0, lp, ip,
             wp, wn)
@@ -971,6 +978,8 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
     if dtype not in _FLOAT or target_probs.dim() != 3:
         _fail("target_probs must be [batch, num_tokens, vocab], fp32, fp16 or bf16")
     vocab = target_probs.shape[2]
+    if vocab > 1 << 24 or batch > 65535:
+        _fail(f"vocab {vocab} above 2^24, or batch {batch} above 65535")
     ts = _view(target_probs, "target_probs", dtype, (batch, n, vocab), dev, False)
     ds, qp = _DENSE, 0
     if draft_probs is not None:
@@ -990,7 +999,8 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
         most = accepted_node_ids.shape[-1]
         kp = _vector(accepted_node_ids, "accepted_node_ids", i32, (batch, most), dev)
     d = ssu_verify_dims(batch, n, vocab, most, _DT[dtype], 0, *ts, *ds)
-    wp, wn = _scratch(workspace, max(lib.ssu_verify_workspace_bytes(d), 16), tokens.device, stream)
+    workspace, wp, wn = _scratch(workspace, max(lib.ssu_verify_workspace_bytes(d), 16), tokens.device,
+                                 stream)
     _launch(dev, stream, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip,
             ap, kp, np_, wp, wn)
     return accepted_lengths, next_tokens

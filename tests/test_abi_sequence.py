@@ -89,6 +89,7 @@ def test_conv_pointers(lib):
     assert conv(lib, conv_dims(), idx=FAKE + 2) == 1 and "'state_indices'" in err(lib)
     assert conv(lib, conv_dims(), ctx=FAKE + 2) == 1 and "'context_lengths'" in err(lib)
     assert conv(lib, conv_dims(), seq_len=-1) == 1 and "seq_len" in err(lib)
+    assert conv(lib, conv_dims(), seq_len=(1 << 30) + 1) == 2 and "too large" in err(lib)
     assert conv(lib, conv_dims(batch=5), idx=FAKE, x=None) == 1 and "'x'" in err(lib)
     for rc in (conv(lib, conv_dims(batch=0), x=None), conv(lib, conv_dims(), seq_len=0, x=None)):
         assert rc == 0 and err(lib) == ""
@@ -141,6 +142,7 @@ def test_scan_pointers(lib):
     assert scan(lib, scan_dims(), state=FAKE + 8) == 1 and "'state'" in err(lib)
     assert scan(lib, scan_dims(), dt=FAKE + 2) == 1 and "'dt'" in err(lib)
     assert scan(lib, scan_dims(), seq_len=-1) == 1
+    assert scan(lib, scan_dims(), seq_len=(1 << 30) + 1) == 2 and "seq_len" in err(lib)
     for rc in (scan(lib, scan_dims(batch=0), x=None), scan(lib, scan_dims(), seq_len=0, x=None)):
         assert rc == 0 and err(lib) == ""
 

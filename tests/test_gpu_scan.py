@@ -355,3 +355,16 @@ def test_two_streams_at_once_with_workspaces_of_their_own():
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert_bitwise(o, w, "out")
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [(2, 1, 40, 16), (64, 17, 600, 16), (6, 70, 500, 16),
+                                                      (4, 200, 33, 16), (1, 200, 48, 40), (1, 1900, 40, 16),
+                                                      (2, 300, 48, 128)])
+def test_infinite_decay_leaves_the_last_token_alone(batch, seq_len, dim, dstate):
+    """Entries of A at -inf (or at -inf once scaled to powers of two) forget all but
+    a token's own term, and tokens past a row's end do not touch them."""
+    T = scan_inputs(8, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate, io="f32",
+                    ctx=[max(seq_len - 5 - b % 3, 1) for b in range(batch)])
+    T["A"][:, 1] = -float("inf")
+    T["A"][5, 3] = -3e38
+    run_both(T)
