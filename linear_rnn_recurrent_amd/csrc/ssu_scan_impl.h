@@ -99,6 +99,14 @@ __device__ __forceinline__ void cvt4(const Raw4x &r, int dt, float (&v)[4])
             v[j] = cvt1<SZ>(r.w[j], dt);
     }
 }
+// Four adjacent state entries, aligned to four, as floats.
+__device__ __forceinline__ void ld_state4(const ScanParams &p, int64_t i, float (&v)[4])
+{
+    if (p.state_dtype == kF32)
+        cvt4<4>(raw4<4>(p.state, i, kF32), kF32, v);
+    else
+        cvt4<2>(raw4<2>(p.state, i, p.state_dtype), p.state_dtype, v);
+}
 template <int SZ>
 __device__ __forceinline__ void st1(void *p, int64_t i, float v, int dt)
 {

@@ -129,6 +129,39 @@ __device__ __forceinline__ void step_sizes(const uint32_t (&x)[kBatch], const ui
     }
 }
 
+// The pool's entries of a lane (0 past dstate), all on their way at once.
+__device__ __forceinline__ void load_states(const ScanParams &p, int64_t so, int tile, float (&h)[kStates])
+{
+    auto load = [&](auto f32) {
+        constexpr int SZ = decltype(f32)::value ? 4 : 2;
+        Raw4x w[kStates / 4];
+#pragma unroll
+        for (int j = 0; j < kStates; j += 4)
+            w[j / 4] = raw4<SZ>(p.state, so + (tile * kStates + j < p.dstate ? j : 0), p.state_dtype);
+#pragma unroll
+        for (int j = 0; j < kStates; j += 4) {
+            float v[4];
+            cvt4<SZ>(w[j / 4], p.state_dtype, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[j + k] = tile * kStates + j < p.dstate ? v[k] : 0.0f;
+        }
+    };
+    if (p.state_dtype == kF32)
+        load(std::true_type());
+    else
+        load(std::false_type());
+}
+
+// Waits for v, values of scalar loads. Those return in any order, so that any
+// wait is for all of them: loads are issued after the wait for the ones before.
+__device__ __forceinline__ void arrived(const float (&v)[kStates])
+{
+    asm volatile("" ::"s"(v[0]), "s"(v[1]), "s"(v[2]), "s"(v[3]), "s"(v[4]), "s"(v[5]), "s"(v[6]),
+                 "s"(v[7]), "s"(v[8]), "s"(v[9]), "s"(v[10]), "s"(v[11]), "s"(v[12]), "s"(v[13]),
+                 "s"(v[14]), "s"(v[15]));
+}
+
 // Every chunk's end from a zero start (all but a row's last chunk, or all of
 // them where only the state is wanted), and the copy of the pool's state.
 template <typename IOT, typename DTT>
@@ -149,10 +182,11 @@ __global__ __launch_bounds__(256, 4) void ssu_scan_ends_kernel(const ScanParams 
         return;
     if (c == 0) {
         const int64_t so = (int64_t)row * p.row_stride + (int64_t)q.d * p.dstate + tile * kStates;
+        float h[kStates];
+        load_states(p, so, tile, h);
 #pragma unroll
         for (int j = 0; j < kStates; ++j)
-            e[j * 64] = tile * kStates + (j & ~3) < p.dstate ? ld_io(p.state, so + j, p.state_dtype)
-                                                              : 0.0f;
+            e[j * 64] = h[j];
     }
     if (p.out && t1 == len)
         return;
@@ -181,6 +215,8 @@ __global__ __launch_bounds__(256, 4) void ssu_scan_ends_kernel(const ScanParams 
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
+            arrived(bs);
+            __builtin_amdgcn_sched_barrier(0);
             float bn[kStates];
 #pragma unroll
             for (int j = 0; j < kStates; ++j)
@@ -340,10 +376,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
         for (int j = 0; j < kStates; ++j)
             h[j] = lds[((mate * s.tiles + tile) * kStates + j) * 64 + lane];
     } else {
-#pragma unroll
-        for (int j = 0; j < kStates; ++j)
-            if (tile * kStates + (j & ~3) < p.dstate)
-                h[j] = ld_io(p.state, so + j, p.state_dtype);
+        load_states(p, so, tile, h);
     }
     if (ONE && !live)
         return;
@@ -353,10 +386,10 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
     float *part = lds + (s.chunks > 1 ? s.team * s.tiles * kStates * 64 : 0);
     if (!live)
         bc = s.zeros;
-    float bs[kStates];  // the next token's B
+    float bs[kStates], cs[kStates];  // the next token's B and C
 #pragma unroll
     for (int j = 0; j < kStates; ++j)
-        bs[j] = packed[bc + j];
+        bs[j] = packed[bc + j], cs[j] = packed[bc + kStates + j];
     int buf = 0;
     for (int t = t0; t < t0 + batches * kBatch; t += kBatch) {
         if (!ONE && t >= t1) {
@@ -372,27 +405,24 @@ __global__ __launch_bounds__(ONE ? 256 : 1024, 4) void ssu_scan_tokens_kernel(
         }
         if (t + kBatch < t1)
             load(t1 - t - kBatch);
-        // token i's C and token i + 1's B (scalar loads) are on their way while
-        // token i's states are computed; the barriers keep that order
+        // token i + 1's B and C are on their way while token i is computed
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            float cs[kStates], bn[kStates];
-#pragma unroll
-            for (int j = 0; j < kStates; ++j)
-                cs[j] = packed[bc + kStates + j];
             bc = t + i + 1 < t1 ? bc + bc_step : s.zeros;
-#pragma unroll
-            for (int j = 0; j < kStates; ++j)
-                bn[j] = packed[bc + j];
-#pragma unroll
-            for (int j = 0; j < kStates; ++j)
-                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
+            arrived(bs);
+            arrived(cs);
             __builtin_amdgcn_sched_barrier(0);
+            float bn[kStates], cn[kStates];
+#pragma unroll
+            for (int j = 0; j < kStates; ++j)
+                bn[j] = packed[bc + j], cn[j] = packed[bc + kStates + j];
             float y2[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < kStates; ++j) {
+                h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * v[i]), u[i] * bs[j]);
                 y2[j & 1] = fmaf(h[j], cs[j], y2[j & 1]);
                 bs[j] = bn[j];
+                cs[j] = cn[j];
             }
             y[i] = y2[0] + y2[1];
             __builtin_amdgcn_sched_barrier(0);
@@ -554,11 +584,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     for (int k = wave; k < tiles; k += WAVES) {
         float h[4] = {};
         const int n0 = k * kStates + r * 4;
-        if (n0 < p.dstate) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                h[j] = ld_io(p.state, so + n0 + j, p.state_dtype);
-        }
+        if (n0 < p.dstate)
+            ld_state4(p, so + n0, h);
         starts[k * 64 + lane] = make_float4(h[0], h[1], h[2], h[3]);
     }
     int starts_now = 0;  // which of the two copies the step reads; the other gets the next's
