@@ -17,7 +17,8 @@
 // decays in registers; the ends meet in LDS; then the tokens run again from
 // their true start. Per token, channel and state entry that is a product, an
 // exponential at half rate, two products with B and two multiply-adds for the
-// state, one for the output: 8 issue slots of the vector ALU, which bounds it.
+// state, one for the output: 8 issue slots of the vector ALU, which bounds it (12
+// counted, with softplus, gate and exchange: busy 72% of 60 us at 8 x 777 x 2560).
 //
 // Chunks (ssu_scan_prompt.h; long prompts of few channels): a lane is a channel
 // and holds 16 state entries, which makes B and C the same for the whole wave
@@ -28,7 +29,8 @@
 //           (the chunk's decay is exp(A sum dt'))
 //   tokens  every chunk's start from the pool's state and the ends before it, in
 //           order, then its tokens: the outputs, the last state
-// The chunks' decays are computed twice (11 slots). dstate above 16 takes
+// The chunks' decays are computed twice (11 slots; 1 x 2048 x 5120: pack 5 us, ends
+// 42 of which the vector ALU 29, tokens 64 of which 42). dstate above 16 takes
 // ceil(dstate / 16) waves, whose partial outputs meet in LDS. (A single chunk
 // needs no ends; without outputs a small kernel folds the ends into the last
 // state and the tokens are not run.)

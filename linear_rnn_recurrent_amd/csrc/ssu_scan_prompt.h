@@ -523,8 +523,8 @@ __device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, f
 // ends and holds half the decays. 4 waves are what short and uneven rows take, with
 // 8 (us with 8 | 16: 8 x 777 x 2560 uneven 59 | 64, 32 x 128 x 2560 74 | 83,
 // 4 x 512 x 2560 54 | 52); 8 and 16 waves take longer rows, with 16 (8 waves: 53 |
-// 50, 16 waves: 1 x 2048 x 1536 72 | 66). The vector ALU is busy 69% of the time
-// (8 x 777 x 2560); the rest is the exchange's barriers and the rows' ends. Four
+// 50, 16 waves: 1 x 2048 x 1536 72 | 66). The rest
+// beside the vector ALU is the exchange's barriers and the rows' ends. Four
 // waves a SIMD leave the 128 registers that kSub 16 needs: at five it spills (115 us
 // for 64).
 template <typename IOT, typename DTT, int BC, int WAVES>
