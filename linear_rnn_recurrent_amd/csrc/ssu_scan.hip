@@ -65,7 +65,7 @@ double rows_us(bool ragged, int64_t seq_len, double mega)
 double sweep_us(int waves, bool ragged, int64_t blocks, int64_t tiles, int64_t seq_len)
 {
     const int64_t sub = sweep_tokens(waves), steps = (seq_len + sub * waves - 1) / (sub * waves);
-    const int64_t lds = 4 * (waves * 16 * (2 * sub + 4) + waves * 1024 + tiles * 512);
+    const int64_t lds = 4 * (waves * (16 * (2 * sub + 4) + 1024 + sub * 16) + tiles * 512);
     const int64_t fit = 163840 / lds, per_cu = fit < 16 / waves ? (fit < 1 ? 1 : fit) : 16 / waves;
     const int64_t slots = 256 * per_cu, rest = blocks % slots;
     auto step = [](int64_t w) { return 3.15 + 0.27 * w; };  // w waves on a CU
@@ -73,10 +73,10 @@ double sweep_us(int waves, bool ragged, int64_t blocks, int64_t tiles, int64_t s
                           (rest ? step(waves * ((rest + 255) / 256)) : 0.0);
     const double body = steps * (0.3 + 0.7 * tiles);
     if (waves == 4)
-        return 3.0 + rounds * (0.1 + body) * (ragged ? 0.32 : 0.51);
+        return 3.0 + rounds * (0.1 + body) * (ragged ? 0.3 : 0.48);
     if (waves == 8)
-        return 3.0 + rounds * (0.08 + body) * (ragged ? 0.75 : 1.0);
-    return 3.0 + rounds * (0.19 + body) * (ragged ? 0.89 : 1.11);
+        return 3.0 + rounds * (0.08 + body) * (ragged ? 0.69 : 0.92);
+    return 3.0 + rounds * (0.19 + body) * (ragged ? 0.82 : 1.03);
 }
 
 double chunks_us(bool cut, bool ragged, int64_t tiles, int64_t seq_len, double mega)

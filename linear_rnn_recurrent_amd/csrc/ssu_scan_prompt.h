@@ -513,9 +513,10 @@ __device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, f
 // tokens a wave and step. Lane (r, c) of a wave has four state entries (4r ..) of
 // channel c: it runs the wave's tokens from a zero start keeping the kSub decays of
 // each entry, the waves exchange ends and decays through LDS, and every wave runs
-// its tokens again from its true start without any exponential. A token's B and C
-// lie across the 16 lanes of a row and reach its channels by DPP broadcast; its
-// dt' and dt' x go through the wave's own LDS; the sum over dstate is two
+// its tokens again from its true start without any exponential. A token's B lies
+// across the 16 lanes of a row and reaches its channels by the DPP of a product; C,
+// whose multiply-adds do not take one here, goes through the wave's own LDS (by DPP
+// as well: 52 us for 49 at 4 x 512 x 2560), and so do dt' and dt' x; the sum over dstate is two
 // swap-and-adds that also hand lane (r, c) the outputs of kSub / 4 tokens, those
 // whose x, dt and z it loaded. dstate above 16 repeats the two runs per 16.
 //
@@ -534,12 +535,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     extern __shared__ float lds[];
     constexpr int kSub = sweep_tokens(WAVES);
     constexpr int kOwn = kSub / 4, kVuPitch = vu_pitch(kSub);  // a lane loads and finishes kOwn tokens
-    // [waves][16][kVuPitch] dt', dt' x; [2][waves][64][8] ends and decays; [2][tiles][64][4] states
+    // [waves][16][kVuPitch] dt', dt' x; [2][waves][64][8] ends and decays; [2][tiles][64][4] states;
+    // [waves][kSub][4][4] C
     const int lane = threadIdx.x & 63, r = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float *vu = lds + wave * (16 * kVuPitch);
     float4 *ends = reinterpret_cast<float4 *>(lds + WAVES * 16 * kVuPitch);
     float4 *starts = ends + 2 * WAVES * 64 * 2;
+    float4 *cl = starts + 2 * tiles * 64 + wave * (kSub * 4);  // [token][r] C
 
     // eight neighbouring blocks, which share cache lines of x, dt, z and out, on
     // one XCD (workgroups go to the eight XCDs in turn)
@@ -643,21 +646,24 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
                 bv[j] = real ? bv[j] : 0.0f;
                 cv[j] = real ? cv[j] : 0.0f;
             }
+            cl[(c % kSub) * 4 + r] = make_float4(cv[0], cv[1], cv[2], cv[3]);
             // from a zero start
             float dec[kSub][4], h[4] = {}, sum = 0.0f;
             each_of(
                 [&](auto tt) {
-                    constexpr int t = decltype(tt)::value;
-                    const float2 w = *reinterpret_cast<const float2 *>(vu + c * kVuPitch + t * 2);
-                    sum += w.x;
+                    constexpr int t = decltype(tt)::value * 2;
+                    const float4 w = *reinterpret_cast<const float4 *>(vu + c * kVuPitch + t * 2);
+                    sum += w.x + w.z;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         dec[t][j] = __builtin_amdgcn_exp2f(a[j] * w.x);
+                        dec[t + 1][j] = __builtin_amdgcn_exp2f(a[j] * w.z);
                         h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * w.y);
+                        h[j] = fmaf(h[j], dec[t + 1][j], row_lane<t + 1>(bv[j]) * w.w);
                     }
                     __builtin_amdgcn_sched_barrier(0);  // keeps the tokens in order, and the registers few
                 },
-                std::make_integer_sequence<int, kSub>());
+                std::make_integer_sequence<int, kSub / 2>());
             float4 *mine = ends + ((buf * WAVES + wave) * 64 + lane) * 2;
             mine[0] = make_float4(h[0], h[1], h[2], h[3]);
             mine[1] = make_float4(__builtin_amdgcn_exp2f(a[0] * sum), __builtin_amdgcn_exp2f(a[1] * sum),
@@ -678,16 +684,20 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
             float y[kSub];
             each_of(
                 [&](auto tt) {
-                    constexpr int t = decltype(tt)::value;
-                    const float u = vu[c * kVuPitch + t * 2 + 1];
+                    constexpr int t = decltype(tt)::value * 2;
+                    const float4 w = *reinterpret_cast<const float4 *>(vu + c * kVuPitch + t * 2);
+                    const float4 c0 = cl[t * 4 + r], c1 = cl[t * 4 + 4 + r];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * u);
-                        y[t] = j == 0 ? row_lane<t>(cv[j]) * h[j] : fmaf(row_lane<t>(cv[j]), h[j], y[t]);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = fmaf(h[j], dec[t][j], row_lane<t>(bv[j]) * w.y);
+                    y[t] = fmaf(h[3], c0.w, fmaf(h[2], c0.z, fmaf(h[1], c0.y, h[0] * c0.x)));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        h[j] = fmaf(h[j], dec[t + 1][j], row_lane<t + 1>(bv[j]) * w.w);
+                    y[t + 1] = fmaf(h[3], c1.w, fmaf(h[2], c1.z, fmaf(h[1], c1.y, h[0] * c1.x)));
                     __builtin_amdgcn_sched_barrier(0);
                 },
-                std::make_integer_sequence<int, kSub>());
+                std::make_integer_sequence<int, kSub / 2>());
             // sums over the four rows: halves, then rows, leaving the lane's own tokens
             float y8[2 * kOwn];
 #pragma unroll
@@ -797,7 +807,8 @@ hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
     const int tiles = (p.dstate + kStates - 1) / kStates;
     if ((int64_t)p.batch * blocks > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    const int lds = 4 * (WAVES * 16 * vu_pitch(sweep_tokens(WAVES)) + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4);
+    const int lds = 4 * (WAVES * 16 * vu_pitch(sweep_tokens(WAVES)) + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4 +
+                         WAVES * sweep_tokens(WAVES) * 16);
     const auto kernel = ssu_scan_sweep_kernel<IOT, DTT, BC, WAVES>;
     static std::atomic<uint64_t> raised{0};
     const hipError_t e = raise_lds(reinterpret_cast<const void *>(kernel), lds, &raised);
