@@ -155,8 +155,8 @@ def test_scan_workspace(lib):
     # the sizes at which the GPU tests mean to reach the chunked evaluation do
     for batch, seq_len, dim, dstate in [(1, 1900, 40, 16), (2, 2000, 90, 12), (1, 1850, 3, 16),
                                         (1, 600, 70, 64), (2, 300, 48, 128), (1, 290, 33, 256),
-                                        (1, 280, 20, 200), (1, 2048, 5120, 16), (32, 20, 4000, 16),
-                                        (32, 17, 600, 100)]:
+                                        (1, 280, 20, 200), (1, 2048, 5120, 16), (64, 20, 4000, 16),
+                                        (64, 17, 600, 100)]:
         assert S.scan_workspace_bytes(batch, seq_len, dim, dstate) > 0
     assert scan(lib, d, seq_len=1000, ws_bytes=need - 1) == 1 and "workspace_bytes" in err(lib)
     assert scan(lib, d, seq_len=1000, ws=None) == 1 and "'workspace'" in err(lib)

@@ -160,8 +160,8 @@ def test_many_workgroups(batch, seq_len, dim, dstate):
 EVALUATIONS = [(64, 20, 640, 16), (64, 17, 600, 16), (2, 16, 70, 40), (64, 60, 48, 16), (6, 70, 500, 16), (3, 120, 90, 16),
                (4, 200, 33, 16), (70, 33, 40, 8), (20, 40, 130, 20), (2, 129, 64, 48), (1, 250, 48, 100),
                (1, 1900, 40, 16), (2, 2000, 90, 12), (1, 1850, 3, 16), (1, 600, 70, 64), (2, 300, 48, 128),
-               (1, 290, 33, 256), (1, 280, 20, 200), (1, 70, 48, 40), (1, 200, 48, 40), (32, 20, 4000, 16),
-               (32, 17, 600, 100)]
+               (1, 290, 33, 256), (1, 280, 20, 200), (1, 70, 48, 40), (1, 200, 48, 40), (64, 20, 4000, 16),
+               (64, 17, 600, 100), (32, 17, 600, 100)]
 
 
 @pytest.mark.parametrize("batch,seq_len,dim,dstate", EVALUATIONS)
