@@ -17,8 +17,8 @@
 // decays in registers; the ends meet in LDS; then the tokens run again from
 // their true start. Per token, channel and state entry that is a product, an
 // exponential at half rate, two products with B and two multiply-adds for the
-// state, one for the output: 8 issue slots of the vector ALU, which bounds it (12
-// counted, with softplus, gate and exchange: busy 72% of 60 us at 8 x 777 x 2560).
+// state, one for the output: 8 issue slots of the vector ALU, which bounds it (11
+// counted, with softplus, gate and exchange: busy 72% of 57 us at 8 x 777 x 2560).
 //
 // Chunks (ssu_scan_prompt.h; long prompts of few channels): a lane is a channel
 // and holds 16 state entries, which makes B and C the same for the whole wave
@@ -88,19 +88,19 @@ double chunks_us(bool cut, bool ragged, int64_t tiles, int64_t seq_len, double m
 
 // Which evaluation a call takes, and its cut: the one with the least estimate.
 // Measured (us, rows | sweep of 4, 8, 16 waves | chunks):
-//   64 x 32 x 2560                 48 | 45, 141, 368   | 47
-//   8 x 64 x 2560                  26 | 14, 24, 50     | 48
-//   16 x 256 x 1024                76 | 36, 36, 46     | 57
-//   4 x 512 x 2560                144 | 54, 51, 58     | 65
-//   1 x 512 x 1536                128 | 38, 25, 21     | 47
-//   1 x 2048 x 1536               554 | 140, 84, 66    | 62
-//   1 x 2048 x 5120               592 | 178, 127, 140  | 110
-//   64 x 64 x 5120                173 | 154, 308, 772  | 129
-//   2 x 509 x 1536, dstate 64     148 | 112, 67, 59    | 82
-//   4 x 512 x 2560, dstate 64     245 | 173, 147, 162  | 245
-//   8 x 777 x 2560, uneven        182 | 59, 71, 93     | 86
-//   64 x 500 x 1024, uneven       266 | 149, 202, 303  | 237
-//   1 x 4096 x 1024, dstate 128  1714 | 1583, 927, 763 | 365
+//   64 x 32 x 2560                 48 | 43, 128, 339   | 44
+//   8 x 64 x 2560                  26 | 14, 23, 47     | 45
+//   16 x 256 x 1024                76 | 35, 34, 42     | 52
+//   4 x 512 x 2560                145 | 52, 47, 55     | 66
+//   1 x 512 x 1536                128 | 35, 22, 20     | 42
+//   1 x 2048 x 1536               552 | 128, 75, 61    | 59
+//   1 x 2048 x 5120               579 | 172, 121, 130  | 108
+//   64 x 64 x 5120                169 | 149, 288, 717  | 112
+//   2 x 509 x 1536, dstate 64     146 | 101, 58, 55    | 82
+//   4 x 512 x 2560, dstate 64     246 | 159, 132, 152  | 241
+//   8 x 777 x 2560, uneven        179 | 57, 66, 87     | 86
+//   64 x 500 x 1024, uneven       268 | 145, 193, 283  | 234
+//   1 x 4096 x 1024, dstate 128  1725 | 1405, 783, 714 | 361
 // Chunks are as long as leaves about three waves for each of the GPU's 1,024
 // SIMDs: every chunk costs its end, its fold and 4 KiB of traffic, and too few
 // leave SIMDs idle (1 x 2048 x 5120: 113 us at 2,560 waves, 102 at 3,072, 104 at

@@ -516,18 +516,18 @@ __device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, f
 // its tokens again from its true start without any exponential. A token's B lies
 // across the 16 lanes of a row and reaches its channels by the DPP of a product; C,
 // whose multiply-adds do not take one here, goes through the wave's own LDS (by DPP
-// as well: 52 us for 49 at 4 x 512 x 2560), and so do dt' and dt' x; the sum over dstate is two
-// swap-and-adds that also hand lane (r, c) the outputs of kSub / 4 tokens, those
-// whose x, dt and z it loaded. dstate above 16 repeats the two runs per 16.
+// as well: 52 us for 49 at 4 x 512 x 2560), and so do dt' and dt' x, two tokens a
+// read (one: 49 us for 46). The sum over dstate is two swap-and-adds that also hand
+// lane (r, c) the outputs of kSub / 4 tokens, those whose x, dt and z it loaded.
+// dstate above 16 repeats the two runs per 16.
 //
 // kSub: 16 spreads a step's exchange over more tokens, 8 wastes less at the rows'
 // ends and holds half the decays. 4 waves are what short and uneven rows take, with
 // 8 (us with 8 | 16: 8 x 777 x 2560 uneven 59 | 64, 32 x 128 x 2560 74 | 83,
 // 4 x 512 x 2560 54 | 52); 8 and 16 waves take longer rows, with 16 (8 waves: 53 |
-// 50, 16 waves: 1 x 2048 x 1536 72 | 66). The rest
-// beside the vector ALU is the exchange's barriers and the rows' ends. Four
-// waves a SIMD leave the 128 registers that kSub 16 needs: at five it spills (115 us
-// for 64).
+// 50, 16 waves: 1 x 2048 x 1536 72 | 66; all before C went through LDS). The rest
+// beside the vector ALU is the exchange's barriers and the rows' ends. Four waves a
+// SIMD leave the 128 registers that kSub 16 needs: at five it spills (115 us for 64).
 template <typename IOT, typename DTT, int BC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     const ScanParams p, int per_group, int blocks, int tiles)

@@ -12,8 +12,8 @@
 // The row is read once, so HBM bounds large vocabularies; a small one is a
 // chain of dependent accesses (lengths, tokens, gathered entries, the row, a
 // segment again).
-// Measured: 64 x 131072 fp32 with draft probabilities 14.3 us for the sums (4.7
-// TB/s) and 4.1 for the draw; 16 trees of 64 nodes x 32000 bf16 10.4. One launch |
+// Measured: 64 x 131072 fp32 with draft probabilities 14.3-14.9 us for the sums (4.5
+// TB/s) and 4.1-4.7 for the draw; 16 trees of 64 nodes x 32000 bf16 10.4. One launch |
 // two, fp32: 64 x 32000 11.2 | 13.9 us, 1 x 32000 9.0 | 9.0, 1 x 2000 8.1 | 9.6.
 #include "ssu_device.h"
 #include "ssu_internal.h"
