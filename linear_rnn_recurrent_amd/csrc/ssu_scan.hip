@@ -103,10 +103,10 @@ double chunks_us(bool cut, bool ragged, int64_t tiles, int64_t seq_len, double m
 //   1 x 4096 x 1024, dstate 128  1725 | 1405, 783, 714 | 361
 // Chunks are as long as leaves about three waves for each of the GPU's 1,024
 // SIMDs: every chunk costs its end, its fold and 4 KiB of traffic, and too few
-// leave SIMDs idle (1 x 2048 x 5120: 113 us at 2,560 waves, 102 at 3,072, 104 at
-// 4,096, 109 at 8,192). With context_lengths rows end early and unevenly, and
-// shorter chunks fill the gaps (8 x 777 x 2560 with lengths from an eighth up:
-// 135 us at 3,072, 93 at 6,144, 86 at 8,192, 87 at 10,000).
+// leave SIMDs idle (1 x 2048 x 5120: 113 us at 2.5 waves a SIMD, 102 at three, 104
+// at four, 109 at eight). With context_lengths rows end early and unevenly, and
+// shorter chunks fill the gaps (8 x 777 x 2560 with lengths from an eighth up: 135
+// us at three, 93 at six, 86 at eight, 87 at ten).
 ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, int64_t seq_len,
                    bool ragged)
 {
@@ -130,7 +130,7 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     q.s.tiles = (int32_t)tiles;
     q.s.per_group = (int32_t)((dim / ngroups + 63) / 64);
     q.s.blocks = (int32_t)(q.s.per_group * ngroups);
-    const int64_t waves = batch * q.s.blocks * q.s.tiles, target = ragged ? 8192 : 3072;
+    const int64_t waves = batch * q.s.blocks * q.s.tiles, target = (ragged ? 8 : 3) * 1024;
     int64_t chunks = waves * 2 > target ? 1 : target / waves;
     int64_t len = (seq_len + chunks - 1) / chunks;
     len = (len + kBatch - 1) / kBatch * kBatch;
