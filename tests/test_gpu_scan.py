@@ -368,3 +368,16 @@ def test_infinite_decay_leaves_the_last_token_alone(batch, seq_len, dim, dstate)
     T["A"][:, 1] = -float("inf")
     T["A"][5, 3] = -3e38
     run_both(T)
+
+
+def test_stream_by_object_and_by_handle():
+    T = scan_inputs(4, batch=1, seq_len=1900, dim=40, dstate=16)
+    s, outs = torch.cuda.Stream(), []
+    for stream in (None, 0, s.cuda_stream, s):
+        out, state = torch.empty_like(T["x"]), T["state"].clone()
+        torch.cuda.synchronize()
+        call(T, out, state=state, stream=stream)
+        torch.cuda.synchronize()
+        outs.append(out)
+    for out in outs[1:]:
+        assert_bitwise(out, outs[0], "out")
