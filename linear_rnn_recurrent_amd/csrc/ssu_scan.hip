@@ -156,6 +156,8 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
 int64_t scan_workspace_floats(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups,
                               int64_t seq_len)
 {
+    if (batch <= 0 || seq_len <= 0)
+        return 0;  // nothing runs
     int64_t most = 0;  // with and without context_lengths
     for (int ragged = 0; ragged < 2; ++ragged) {
         const ScanPlan q = scan_plan(batch, dim, dstate, ngroups, seq_len, ragged != 0);
