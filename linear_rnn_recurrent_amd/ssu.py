@@ -784,15 +784,19 @@ def _launch(dev, stream, fn, *args):
 
 def _scratch(workspace, need, device, stream):
     """The caller's workspace, or one of `need` bytes for this call on `stream`; returns
-    (tensor, address, bytes). The tensor has to live until the call is launched: freed
-    before, its memory could go to a call on another stream at once."""
+    (tensor, address, bytes). A new one is allocated with the call's stream current, so
+    that the allocator orders it there on both sides: a block that was freed on another
+    stream may still be in use by what is queued on that one. The tensor has to live until
+    the call is launched: freed before, its memory could go to another call at once."""
     if workspace is None:
         if need <= 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:  # the allocator frees it for the current stream alone
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device)
-                                    if isinstance(stream, int) else stream)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)
+                                   if isinstance(stream, int) else stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         _dense(workspace, "workspace", (torch.uint8,))
     return workspace, workspace.data_ptr(), workspace.numel()

@@ -5,6 +5,7 @@ import torch
 
 import linear_rnn_recurrent_amd as L
 from gpu_helpers import assert_bitwise
+from sequence_helpers import scan_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,60 @@ def test_empty_calls_do_nothing(batch, seq_len):
     torch.cuda.synchronize()
     assert_bitwise(state, before[0], "state")
     assert_bitwise(conv, before[1], "conv_state")
+
+
+def _spy(monkeypatch, kept):
+    """Keeps (address, stream current at the allocation) of every torch.empty."""
+    empty = torch.empty
+
+    def spied(*a, **k):
+        t = empty(*a, **k)
+        kept.append((t.data_ptr(), torch.cuda.current_stream(t.device).cuda_stream))
+        return t
+
+    monkeypatch.setattr(torch, "empty", spied)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("op", ["scan", "verify"])
+def test_scratch_of_a_call_on_another_stream(monkeypatch, op, handle):
+    """A block freed on the current stream, where work on it may be pending, does not
+    become the scratch of a call on another stream; the results are those of the
+    current stream with no wait for the device between."""
+    side, kept = torch.cuda.Stream(), []
+    stream = side.cuda_stream if handle else side
+    if op == "scan":
+        T = scan_inputs(71, batch=1, seq_len=1900, dim=200, dstate=16)
+        need = L.scan_workspace_bytes(1, 1900, 200, 16)
+
+        def call(stream=None):
+            out, state = torch.zeros_like(T["x"]), T["state"].clone()
+            go = (lambda: L.ssu_scan_prefill(T["x"], T["A"], T["B"], T["C"], T["dt"], state, out,
+                                             dt_bias=T["dt_bias"], D=T["D"], z=T["z"],
+                                             state_indices=T["idx"], stream=stream))
+            return go, (out, state)
+    else:
+        T = verify_inputs(72, batch=3, tokens=4, vocab=70001)
+        need = L.verify_workspace_bytes(3, 70001)
+
+        def call(stream=None):
+            acc, nxt = (torch.full((3,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+            go = (lambda: L.ssu_draft_verify(T["tokens"], T["target"], T["uniforms"], acc, nxt,
+                                             draft_probs=T["draft"], stream=stream))
+            return go, (acc, nxt)
+    assert need > 0
+    go, want = call()
+    go()
+    for _ in range(3):
+        go, got = call(stream)
+        side.wait_stream(torch.cuda.current_stream())
+        block = torch.zeros(need, dtype=torch.uint8, device="cuda")  # in use on the current stream ..
+        address = block.data_ptr()
+        del block                                                    # .. and free to be handed out there
+        with monkeypatch.context() as m:
+            _spy(m, kept)
+            go()
+        assert [s for _, s in kept] == [side.cuda_stream] and kept.pop()[0] != address
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(got, want):
+            assert_bitwise(a, b, op)

@@ -7,6 +7,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from linear_rnn_recurrent_amd import ssu as S
 
@@ -32,3 +33,60 @@ def test_an_empty_scan_needs_no_workspace(lib, batch, seq_len, dim, dstate):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-500:]
     assert r.stdout.split() == ["0", "0"]
+
+
+class _Allocations:
+    """Records what is entered and allocated, in order."""
+
+    def __init__(self, monkeypatch):
+        self.log = log = []
+
+        class Under:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                log.append(("enter", self.stream))
+
+            def __exit__(self, *_):
+                log.append(("leave", self.stream))
+
+        class Block:
+            is_cuda, dtype = True, torch.uint8
+
+            def data_ptr(self):
+                return 4096
+
+            def numel(self):
+                return 100
+
+            def record_stream(self, stream):
+                log.append(("record", stream))
+
+        def empty(*_, **__):
+            log.append("empty")
+            return Block()
+
+        monkeypatch.setattr(torch.cuda, "stream", Under)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device))
+        monkeypatch.setattr(torch, "empty", empty)
+
+
+@pytest.mark.parametrize("stream,current", [(None, None), ("a stream", "a stream"),
+                                            (7040, ("external", 7040, "gpu")), (0, ("external", 0, "gpu"))])
+def test_scratch_belongs_to_the_stream_of_its_call(monkeypatch, stream, current):
+    """The allocator orders a block by the stream that is current at its allocation:
+    a block of another stream's may still be in use there by what was queued before
+    it was freed, and nothing makes the call's stream wait for that."""
+    seen = _Allocations(monkeypatch)
+    block, address, size = S._scratch(None, 100, "gpu", stream)
+    assert block is not None and (address, size) == (4096, 100)
+    if current is None:
+        assert seen.log == ["empty"]
+    else:
+        assert seen.log[:3] == [("enter", current), "empty", ("leave", current)]
+
+
+def test_no_scratch_where_none_is_needed(monkeypatch):
+    seen = _Allocations(monkeypatch)
+    assert S._scratch(None, 0, "gpu", "a stream") == (None, 0, 0) and seen.log == []
