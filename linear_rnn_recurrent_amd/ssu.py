@@ -7,6 +7,7 @@ kernels of libssu.so; there is no fallback. If the library has not been built
 the first call raises RuntimeError (build it with
 `python -m linear_rnn_recurrent_amd.build`).
 """
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -228,6 +229,40 @@ def _dense(t, name, dtypes=None, shape=None):
 _FLOAT = (torch.float32, torch.float16, torch.bfloat16)
 
 
+def _on(stream, device):
+    """A context in which new tensors belong to `stream` (None: to the current one). The
+    allocator orders a block by the stream that is current at its allocation; one that was
+    freed on another stream may still be in use by what is queued on that one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int)
+                             else stream)
+
+
+def _scratch(workspace, need, device, stream):
+    """The caller's workspace, or one of `need` bytes that belongs to the call's stream;
+    returns (tensor, address, bytes). The tensor has to live until the call is launched:
+    freed before, its memory could go to another call at once."""
+    if workspace is None:
+        if need <= 0:
+            return None, 0, 0
+        with _on(stream, device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dense(workspace, "workspace", (torch.uint8,))
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _result(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` writes and its caller may read on the current
+    stream: it belongs to the first, and its free waits for the second."""
+    with _on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _state_geometry(state, nheads, dim, dstate):
     """state: [rows, nheads, dim, dstate] with dense rows; stride(0) may be padded."""
     _dev(state, "state", _FLOAT)
@@ -430,17 +465,15 @@ def ssu_tree_verify(x, A, B, C, dt, state, out, parent_ids, *, depths=None, dt_b
     stash = (replay_dA, replay_u, replay_B, replay_dt)
     d, num_nodes = _tree_dims(x, A, B, C, dt, state, out, parent_ids, depths, dt_bias, D, z,
                               state_indices, stash)
-    if workspace is None:
-        need = max(int(lib.ssu_tree_workspace_bytes(ctypes.byref(d), num_nodes)), 16)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _dense(workspace, "workspace", (torch.uint8,))
+    need = max(int(lib.ssu_tree_workspace_bytes(ctypes.byref(d), num_nodes)), 16)
+    workspace, wp, wn = _scratch(workspace, need, x.device, stream)
     with torch.cuda.device(x.device):
         _check(lib.ssu_tree_verify(ctypes.byref(d), num_nodes, _ptr(x), _ptr(A), _ptr(B),
                                    _ptr(C), _ptr(dt), _ptr(dt_bias), _ptr(D), _ptr(z),
                                    _ptr(state), _ptr(out), 1 if dt_softplus else 0,
                                    _ptr(state_indices), _ptr(parent_ids), _ptr(depths),
-                                   *[_ptr(s) for s in stash], _ptr(workspace),
-                                   workspace.numel(), _stream(x.device, stream)))
+                                   *[_ptr(s) for s in stash], wp, wn,
+                                   _stream(x.device, stream)))
     return out
 
 
@@ -675,7 +708,7 @@ def ssu_gdn_decode(hidden_states, w_ba, mixed_qkv, conv_weight, conv_bias, conv_
     _need(ssm_state.shape[0] == conv_state.shape[0], "both pools have the same slots")
     _dense(state_indices, "state_indices", (torch.int32,), (B,))
     if out is None:
-        out = torch.empty((B, 1, hv, d), dtype=torch.bfloat16, device=hidden_states.device)
+        out = _result((B, 1, hv, d), torch.bfloat16, hidden_states.device, stream)
     _dense(out, "out", bf, (B, 1, hv, d))
     cs = conv_state.stride()
     dims = ssu_gdn_dims(B, hidden, hq, hv, d, width, ssm_state.shape[0],
@@ -683,16 +716,13 @@ def ssu_gdn_decode(hidden_states, w_ba, mixed_qkv, conv_weight, conv_bias, conv_
                         st[0] if ssm_state.shape[0] > 1 else hv * d * d, cs[0], cs[1], cs[2])
     sc = 0.0 if scale is None else float(scale)
     need = int(lib.ssu_gdn_workspace_bytes(ctypes.byref(dims)))
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=hidden_states.device)
-    _dense(workspace, "workspace", (torch.uint8,))
+    workspace, wp, wn = _scratch(workspace, max(need, 16), hidden_states.device, stream)
     with torch.cuda.device(hidden_states.device):
         _check(lib.ssu_gdn_decode(ctypes.byref(dims), _ptr(hidden_states), _ptr(w_ba),
                                   _ptr(mixed_qkv), _ptr(conv_weight), _ptr(conv_bias),
                                   _ptr(conv_state), _ptr(A_log), _ptr(dt_bias), sc,
                                   _ptr(ssm_state), _ptr(state_indices), _ptr(out),
-                                  _ptr(workspace), workspace.numel(),
-                                  _stream(hidden_states.device, stream)))
+                                  wp, wn, _stream(hidden_states.device, stream)))
     return out
 
 
@@ -780,26 +810,6 @@ def _launch(dev, stream, fn, *args):
             rc = fn(*args, stream)
     if rc != SSU_OK:
         _check(rc)
-
-
-def _scratch(workspace, need, device, stream):
-    """The caller's workspace, or one of `need` bytes for this call on `stream`; returns
-    (tensor, address, bytes). A new one is allocated with the call's stream current, so
-    that the allocator orders it there on both sides: a block that was freed on another
-    stream may still be in use by what is queued on that one. The tensor has to live until
-    the call is launched: freed before, its memory could go to another call at once."""
-    if workspace is None:
-        if need <= 0:
-            return None, 0, 0
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)
-                                   if isinstance(stream, int) else stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _dense(workspace, "workspace", (torch.uint8,))
-    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_lengths,
@@ -1181,7 +1191,7 @@ class SsuPool:
         """Copy one slot of every state into `dst` (list of GPU tensors, allocated
         here when None) and return it."""
         if dst is None:
-            dst = [torch.empty((1,) + shape, dtype=dtype, device=self.device)
+            dst = [_result((1,) + shape, dtype, self.device, stream)
                    for (_, _, shape, dtype) in self.specs]
         n = len(dst)
         ptrs = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in dst])

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import linear_rnn_recurrent_amd as L
-from gpu_helpers import assert_bitwise
+from gpu_helpers import assert_bitwise, gpu
+from linear_rnn_recurrent_amd import inputs
 from sequence_helpers import scan_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,46 @@ def test_scratch_of_a_call_on_another_stream(monkeypatch, op, handle):
         torch.cuda.current_stream().wait_stream(side)
         for a, b in zip(got, want):
             assert_bitwise(a, b, op)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_tensors_made_by_the_other_calls_on_another_stream(monkeypatch, handle):
+    """The workspace of a tree verify, workspace and output of a gated-delta-rule step
+    and the rows that a pool captures: allocated under the call's stream, with the
+    results of the current stream."""
+    side, kept = torch.cuda.Stream(), []
+    stream = side.cuda_stream if handle else side
+    w = inputs.tree_workload(batch=3, num_nodes=24, nheads=2, dim=32, dstate=32, ngroups=1,
+                             pool_rows=5, seed=31)
+    T = {k: gpu(v) for k, v in w.tensors.items()}
+    g = inputs.gdn_workload(batch=5, hidden=256, num_q_heads=2, num_v_heads=4, head_dim=64,
+                            conv_width=4, pool_rows=8, seed=32)
+    G = {k: gpu(v) for k, v in g.tensors.items()}
+    start = {k: G[k].clone() for k in ("conv_state", "ssm_state")}
+    pool = L.SsuPool([(0, 0, (3, 40), torch.float32), (1, 0, (7,), torch.bfloat16)], 3)
+
+    def calls(stream=None):
+        out = torch.zeros_like(T["x"])
+        conv, ssm = start["conv_state"].clone(), start["ssm_state"].clone()
+        if stream is not None:
+            side.wait_stream(torch.cuda.current_stream())
+        L.ssu_tree_verify(T["x"], T["A"], T["B"], T["C"], T["dt"], T["state"], out, T["parent_ids"],
+                          depths=T["depths"], dt_bias=T["dt_bias"], D=T["D"], z=T["z"],
+                          state_indices=T["state_indices"], stream=stream)
+        y = L.ssu_gdn_decode(G["hidden_states"], G["w_ba"], G["mixed_qkv"], G["conv_weight"],
+                             G["conv_bias"], conv, G["A_log"], G["dt_bias"], g.dims["scale"], ssm,
+                             G["state_indices"], num_q_heads=2, stream=stream)
+        rows = pool.capture(1, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(side)
+        return [out, y, conv, ssm, *rows]
+
+    want = calls()
+    for _ in range(3):
+        kept.clear()
+        with monkeypatch.context() as m:
+            _spy(m, kept)
+            got = calls(stream)
+        assert [s for _, s in kept] == [side.cuda_stream] * 5
+        for a, b in zip(got, want):
+            assert_bitwise(a, b, "result")

@@ -90,3 +90,13 @@ def test_scratch_belongs_to_the_stream_of_its_call(monkeypatch, stream, current)
 def test_no_scratch_where_none_is_needed(monkeypatch):
     seen = _Allocations(monkeypatch)
     assert S._scratch(None, 0, "gpu", "a stream") == (None, 0, 0) and seen.log == []
+
+
+def test_results_belong_to_the_stream_of_their_call_and_wait_for_their_reader(monkeypatch):
+    seen = _Allocations(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: ("current", device))
+    S._result((3, 4), torch.float32, "gpu", None)
+    assert seen.log == ["empty"]
+    S._result((3, 4), torch.float32, "gpu", "a stream")
+    assert seen.log[1:] == [("enter", "a stream"), "empty", ("leave", "a stream"),
+                            ("record", ("current", "gpu"))]
