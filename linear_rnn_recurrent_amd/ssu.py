@@ -835,6 +835,9 @@ def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_len
             _fail(f"conv_state must be a [rows, {channels}, {width - 1}] view on cuda:{dev}")
         if rows > 1 << 30:
             _fail("conv_state has more than 2^30 rows")
+        if width > 1 and ((ss[0] <= 0 and rows > 1) or (ss[1] <= 0 and channels > 1)
+                          or (ss[2] <= 0 and width > 2)):
+            _fail("conv_state must not be broadcast")
     else:
         if width != 1:
             _fail("conv_state is required")

@@ -100,3 +100,52 @@ def test_results_belong_to_the_stream_of_their_call_and_wait_for_their_reader(mo
     S._result((3, 4), torch.float32, "gpu", "a stream")
     assert seen.log[1:] == [("enter", "a stream"), "empty", ("leave", "a stream"),
                             ("record", ("current", "gpu"))]
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that the binding takes for one of cuda:0."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    """(entry point, arguments) of every call that the binding would make."""
+    calls = []
+    monkeypatch.setattr(S, "_launch", lambda dev, stream, fn, *args: calls.append((fn, args)))
+    return calls
+
+
+def conv_prefill(state, batch=2, seq_len=5, channels=8, width=4, x=None, out=None):
+    x = torch.zeros(batch, seq_len, channels) if x is None else x
+    out = torch.zeros(batch, seq_len, channels) if out is None else out
+    S.ssu_conv_prefill(on_gpu(x), on_gpu(torch.zeros(channels, width)), None,
+                       None if state is None else on_gpu(state), on_gpu(out))
+
+
+@pytest.mark.parametrize("make", [
+    lambda: torch.zeros(()).expand(6, 8, 3), lambda: torch.zeros(8, 3).expand(6, 8, 3),
+    lambda: torch.zeros(6, 1, 3).expand(6, 8, 3), lambda: torch.zeros(6, 8, 1).expand(6, 8, 3),
+    lambda: torch.zeros(1, 1, 3).expand(6, 8, 3)])
+def test_a_broadcast_conv_state_is_refused(lib, launched, make):
+    """Three strides of 0 are the library's word for a dense pool: passed on, the call
+    would read and write past the one entry that is there."""
+    with pytest.raises(ValueError, match="conv_state must not be broadcast"):
+        conv_prefill(make())
+    assert not launched
+
+
+@pytest.mark.parametrize("shape,channels,width", [((1, 1, 1), 1, 2), ((1, 8, 3), 8, 4), ((1, 1, 3), 1, 4),
+                                                  ((2, 8, 0), 8, 1)])
+def test_axes_of_one_entry_may_have_any_stride(lib, launched, shape, channels, width):
+    state = torch.zeros(shape)
+    state = state.as_strided(shape, [0 if n == 1 else s for n, s in zip(shape, state.stride())])
+    conv_prefill(state, batch=1, channels=channels, width=width)
+    dims = launched[0][1][0]
+    assert (dims.pool_rows, dims.channels, dims.width) == (shape[0], channels, width)
