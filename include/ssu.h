@@ -346,8 +346,10 @@ typedef struct ssu_conv_dims {
     int64_t x_batch_stride, x_token_stride;
     int64_t out_batch_stride, out_token_stride;
     int64_t state_row_stride;  /* element strides of conv_state's logical     */
-    int64_t state_chan_stride; /* [P, channels, W-1] view, any layout whose   */
-    int64_t state_tap_stride;  /* entries do not overlap; all three 0 = dense */
+    int64_t state_chan_stride; /* [P, channels, W-1] view: axes in any order, */
+    int64_t state_tap_stride;  /* each stride above the reach of the axes inside
+                                * its own (an axis of one entry may have any);
+                                * all three 0 = dense */
 } ssu_conv_dims;
 
 /* ssu_conv_prefill -- depthwise causal convolution of seq_len tokens. With

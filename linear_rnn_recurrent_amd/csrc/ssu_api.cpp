@@ -1,7 +1,9 @@
 // C ABI of libssu: host-side argument checks, dispatch to the kernel
 // launchers, and the recurrent-state pool. No entry point reads device memory
 // on the host, synchronises, or allocates, except ssu_pool_alloc/ssu_pool_free.
+#include <algorithm>
 #include <atomic>
+#include <iterator>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -537,16 +539,27 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
         p.st_chan = taps;
         p.st_tap = 1;
     }
-    // entries of one row are distinct for every layout with the channels of a
-    // tap, or the taps of a channel, apart from each other
-    if (taps > 0 && !((p.st_tap >= 1 || taps == 1) && (p.st_chan >= 1 || d.channels == 1) &&
-                      (p.st_chan > (taps - 1) * p.st_tap || p.st_tap > (d.channels - 1) * p.st_chan)))
-        return fail(SSU_EINVAL, "%s: conv_state strides (%lld, %lld) overlap", fn,
-                    (long long)p.st_chan, (long long)p.st_tap);
-    if (taps > 0 && d.pool_rows > 1 &&
-        p.st_row < (d.channels - 1) * p.st_chan + (taps - 1) * p.st_tap + 1)
-        return fail(SSU_EINVAL, "%s: conv_state row stride %lld too small", fn,
-                    (long long)p.st_row);
+    // entries are distinct where the axes nest: each has a stride above the reach of
+    // those inside it, in whatever order
+    if (taps > 0) {
+        struct Axis { int64_t n, stride; bool row; } axes[] = {
+            {taps, p.st_tap, false}, {d.channels, p.st_chan, false}, {d.pool_rows, p.st_row, true}};
+        std::stable_sort(std::begin(axes), std::end(axes),
+                         [](const Axis &x, const Axis &y) { return x.stride < y.stride; });
+        __int128 reach = 0;
+        bool row = false;
+        for (const Axis &x : axes) {
+            if (x.n <= 1)
+                continue;
+            row |= x.row;
+            if (x.stride <= reach)
+                return row ? fail(SSU_EINVAL, "%s: conv_state row stride %lld overlaps its rows' entries",
+                                  fn, (long long)p.st_row)
+                           : fail(SSU_EINVAL, "%s: conv_state strides (%lld, %lld) overlap", fn,
+                                  (long long)p.st_chan, (long long)p.st_tap);
+            reach += (__int128)(x.n - 1) * x.stride;
+        }
+    }
     if (seq_len > (1 << 30) ||
         (int64_t)d.batch * ((d.channels + 255) / 256) * ((seq_len + 15) / 16) > 0x7fffffff)
         return fail(SSU_ENOTSUP, "%s: problem too large", fn);

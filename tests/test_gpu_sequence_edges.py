@@ -6,7 +6,7 @@ import torch
 import linear_rnn_recurrent_amd as L
 from gpu_helpers import assert_bitwise, gpu
 from linear_rnn_recurrent_amd import inputs
-from sequence_helpers import scan_inputs, verify_inputs
+from sequence_helpers import conv_inputs, scan_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,26 @@ def test_tensors_made_by_the_other_calls_on_another_stream(monkeypatch, handle):
         assert [s for _, s in kept] == [side.cuda_stream] * 5
         for a, b in zip(got, want):
             assert_bitwise(a, b, "result")
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2), (0, 2, 1), (1, 0, 2), (1, 2, 0), (2, 0, 1), (2, 1, 0)])
+@pytest.mark.parametrize("io,channels,width", [("bf16", 72, 4), ("f32", 33, 3), ("f16", 16, 8)])
+def test_pools_with_their_axes_in_any_order(order, io, channels, width):
+    T = conv_inputs(81, batch=5, seq_len=9, channels=channels, width=width, io=io,
+                    ctx=[9, 0, 2, 7, 1], idx=[6, 1, -1, 0, 3], pool=8)
+    want = torch.empty_like(T["x"])
+    dense = T["conv_state"].clone()
+    pool = dense.permute(order).clone(memory_format=torch.contiguous_format)
+    pool = pool.permute([order.index(i) for i in range(3)])
+    assert pool.shape == dense.shape and torch.equal(pool, dense)
+    kw = dict(context_lengths=T["ctx"], state_indices=T["idx"])
+    L.ssu_conv_prefill(T["x"], T["weight"], T["bias"], dense, want, **kw)
+    out = torch.empty_like(T["x"])
+    L.ssu_conv_prefill(T["x"], T["weight"], T["bias"], pool, out, **kw)
+    assert_bitwise(out, want, "out")
+    assert_bitwise(pool, dense, "conv_state")
+    one, ref = torch.empty_like(T["x"][:, 0]), torch.empty_like(T["x"][:, 0])
+    L.ssu_conv_decode(T["x"][:, 1], T["weight"], T["bias"], dense, ref, state_indices=T["idx"])
+    L.ssu_conv_decode(T["x"][:, 1], T["weight"], T["bias"], pool, one, state_indices=T["idx"])
+    assert_bitwise(one, ref, "step")
+    assert_bitwise(pool, dense, "conv_state after a step")

@@ -149,3 +149,33 @@ def test_axes_of_one_entry_may_have_any_stride(lib, launched, shape, channels, w
     conv_prefill(state, batch=1, channels=channels, width=width)
     dims = launched[0][1][0]
     assert (dims.pool_rows, dims.channels, dims.width) == (shape[0], channels, width)
+
+
+def conv_dims(**kw):
+    d = dict(batch=0, channels=16, width=4, pool_rows=4, io_dtype=2, weight_dtype=2, state_dtype=2,
+             reserved=0, x_batch_stride=0, x_token_stride=0, out_batch_stride=0, out_token_stride=0,
+             state_row_stride=0, state_chan_stride=0, state_tap_stride=0)
+    d.update(kw)
+    return S.ssu_conv_dims(*d.values())
+
+
+def conv_status(lib, seq_len=8, **kw):
+    """With batch 0 a call returns after its checks of sizes and strides."""
+    return lib.ssu_conv_prefill(conv_dims(**kw), seq_len, *([None] * 5), 1, 1, None, None, None)
+
+
+@pytest.mark.parametrize("row,chan,tap", [
+    (48, 3, 1), (48, 1, 16), (3, 12, 1), (1, 12, 4), (1, 4, 64), (16, 1, 64), (50, 3, 1), (5, 23, 1)])
+def test_every_order_of_the_pools_axes_is_taken(lib, row, chan, tap):
+    assert conv_status(lib, state_row_stride=row, state_chan_stride=chan, state_tap_stride=tap) == 0
+
+
+@pytest.mark.parametrize("row,chan,tap", [(47, 3, 1), (2, 12, 1), (3, 11, 1), (1, 3, 48), (1, 4, 63), (15, 1, 64),
+                                          (16, 1, 63), (0, 3, 1), (3, 3, 1), (48, 3, 0), (1, 1, 1)])
+def test_overlapping_pools_are_refused(lib, row, chan, tap):
+    assert conv_status(lib, state_row_stride=row, state_chan_stride=chan, state_tap_stride=tap) == 1
+    assert "conv_state" in lib.ssu_last_error().decode()
+
+
+def test_huge_strides_do_not_wrap(lib):
+    assert conv_status(lib, state_row_stride=1 << 62, state_chan_stride=1 << 61, state_tap_stride=1) == 1
