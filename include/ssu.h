@@ -330,7 +330,9 @@ int64_t ssu_gdn_workspace_bytes(const ssu_gdn_dims *dims);
  * where ssu_decode and ssu_prefill have one per head. Activations may be
  * slices of wider tensors: their channel axis is contiguous, the batch and
  * token strides are given in elements (0 = dense; a token stride is at least
- * the row's length). All pointers need the alignment of their element unless
+ * the row's length). Either axis may lie outside the other, batch-major
+ * (batch stride >= the row's tokens) or sequence-major (token stride >= the
+ * batch's rows); other strides are refused, as they could overlap. All pointers need the alignment of their element unless
  * stated. Pool rows, negative state_indices and context_lengths are as in
  * ssu_decode and ssu_prefill.
  * ---------------------------------------------------------------------- */
@@ -452,8 +454,8 @@ typedef struct ssu_verify_dims {
     int32_t max_accept_len; /* row length of accepted_node_ids; ignored without it */
     int32_t prob_dtype; /* target_probs, draft_probs: SSU_F32, SSU_F16 or SSU_BF16 */
     int32_t reserved;   /* must be 0 */
-    int64_t target_batch_stride, target_row_stride; /* elements; 0 = dense; */
-    int64_t draft_batch_stride, draft_row_stride;   /* a row stride >= V    */
+    int64_t target_batch_stride, target_row_stride; /* elements, as the activations' */
+    int64_t draft_batch_stride, draft_row_stride;   /* above; a row stride >= V      */
 } ssu_verify_dims;
 
 /* ssu_draft_verify -- which drafted tokens of a verify window stand, and the

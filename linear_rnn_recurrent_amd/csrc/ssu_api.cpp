@@ -475,22 +475,23 @@ ssu_status ssu_gdn_decode(const ssu_gdn_dims *dims, const void *hidden_states, c
 
 namespace {
 
-// Batch and token strides of one activation: 0 selects dense, and a token's
-// row may not reach into the next one's (nor a batch row into the next).
+// Batch and token strides of one activation: 0 selects dense. Rows of different
+// tokens and batch entries may not overlap: either axis lies outside the other.
 ssu_status check_strides(const char *fn, const char *name, int64_t bs, int64_t ts, int64_t row,
-                         int64_t tokens, int64_t *out_bs, int64_t *out_ts)
+                         int64_t batch, int64_t tokens, int64_t *out_bs, int64_t *out_ts)
 {
     if (ts == 0)
         ts = row;
     if (ts < row)
         return fail(SSU_EINVAL, "%s: %s token stride %lld < %lld", fn, name, (long long)ts,
                     (long long)row);
-    const int64_t span = tokens > 0 ? (tokens - 1) * ts + row : 0;
+    const __int128 span = tokens > 0 ? (__int128)(tokens - 1) * ts + row : 0;
     if (bs == 0)
         bs = tokens * ts;
-    if (bs < span)
-        return fail(SSU_EINVAL, "%s: %s batch stride %lld < %lld", fn, name, (long long)bs,
-                    (long long)span);
+    const bool tokens_outside = bs >= row && ts >= (__int128)(batch - 1) * bs + row;
+    if (bs < span && !tokens_outside)
+        return fail(SSU_EINVAL, "%s: %s batch stride %lld overlaps the tokens (stride %lld, row %lld)",
+                    fn, name, (long long)bs, (long long)ts, (long long)row);
     *out_bs = bs;
     *out_ts = ts;
     return SSU_OK;
@@ -521,11 +522,11 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
                     d.pool_rows);
     ssu::ConvParams p = {};
     ssu_status st = check_strides(fn, "x", d.x_batch_stride, step ? 0 : d.x_token_stride,
-                                  d.channels, seq_len, &p.x_bs, &p.x_ts);
+                                  d.channels, d.batch, seq_len, &p.x_bs, &p.x_ts);
     if (st != SSU_OK)
         return st;
     st = check_strides(fn, "out", d.out_batch_stride, step ? 0 : d.out_token_stride, d.channels,
-                       seq_len, &p.out_bs, &p.out_ts);
+                       d.batch, seq_len, &p.out_bs, &p.out_ts);
     if (st != SSU_OK)
         return st;
     const int64_t taps = d.width - 1;
@@ -644,8 +645,8 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
         {"C", d.c_batch_stride, d.c_token_stride, gn, &p.c_bs, &p.c_ts},
     };
     for (const auto &v : views) {
-        const ssu_status st = check_strides(fn, v.name, v.bs, step ? 0 : v.ts, v.row, seq_len,
-                                            v.obs, v.ots);
+        const ssu_status st = check_strides(fn, v.name, v.bs, step ? 0 : v.ts, v.row, d.batch,
+                                            seq_len, v.obs, v.ots);
         if (st != SSU_OK)
             return st;
     }
@@ -797,11 +798,11 @@ ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
                     d.max_accept_len);
     ssu::VerifyParams p = {};
     ssu_status st = check_strides(fn, "target_probs", d.target_batch_stride, d.target_row_stride,
-                                  d.vocab, d.num_tokens, &p.t_bs, &p.t_rs);
+                                  d.vocab, d.batch, d.num_tokens, &p.t_bs, &p.t_rs);
     if (st != SSU_OK)
         return st;
     st = check_strides(fn, "draft_probs", d.draft_batch_stride, d.draft_row_stride, d.vocab,
-                       d.num_tokens - 1, &p.d_bs, &p.d_rs);
+                       d.batch, d.num_tokens - 1, &p.d_bs, &p.d_rs);
     if (st != SSU_OK)
         return st;
     if (d.batch == 0)

@@ -744,8 +744,8 @@ _DENSE = (0, 0)
 
 def _outer(stride, shape, name, step):
     """(batch stride, token stride) of an activation [batch, (tokens,) *row] for the
-    C call, 0 where the axis has one entry; rows must be dense, the outer axes may
-    have any stride but no broadcast."""
+    C call, 0 where the axis has one entry; rows must be dense and not broadcast, either
+    outer axis may lie outside the other (the C call refuses strides that could overlap)."""
     n = len(shape)
     row = 1 if step else 2
     if stride[-1] != 1 and shape[-1] > 1:
@@ -861,7 +861,7 @@ def ssu_conv_prefill(x, weight, bias, conv_state, out, *, silu=True, context_len
     """Causal convolution of seq_len tokens, the last width-1 inputs kept in a pool.
 
     x, out [batch, seq_len, channels] (slices of wider tensors are fine: channels dense,
-    other strides free); weight [channels, width]; bias [channels] or None; conv_state
+    the other two axes in either order); weight [channels, width]; bias [channels] or None; conv_state
     [rows, channels, width-1], any strides, updated in place unless update_state is False;
     context_lengths, state_indices [batch] int32. out may be None when only the state is
     wanted (commit of a window: context_lengths = accepted lengths).
@@ -941,7 +941,7 @@ def ssu_scan_prefill(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None
     """Per-channel selective scan of seq_len tokens.
 
     x, z, out, dt [batch, seq_len, dim]; B, C [batch, seq_len, ngroups, dstate] (slices of
-    wider tensors are fine: a token's entries dense, other strides free); A [dim, dstate],
+    wider tensors are fine: a token's entries dense, the other two axes in either order); A [dim, dstate],
     dt_bias, D [dim] fp32; state [rows, dim, dstate], updated in place unless update_state is
     False; context_lengths, state_indices [batch] int32. out (and C) may be None when only
     the state is wanted (commit of a window: context_lengths = accepted lengths). workspace: a

@@ -157,3 +157,58 @@ def test_pools_with_their_axes_in_any_order(order, io, channels, width):
     L.ssu_conv_decode(T["x"][:, 1], T["weight"], T["bias"], pool, one, state_indices=T["idx"])
     assert_bitwise(one, ref, "step")
     assert_bitwise(pool, dense, "conv_state after a step")
+
+
+def sequence_major(t):
+    """The same values with the token axis outside the batch axis."""
+    return None if t is None else t.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+# Rows, sweeps of 4, 8 and 16 waves, chunks with one and several tiles, one chunk to a row.
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [
+    (3, 1, 40, 16), (64, 17, 600, 16), (8, 64, 2560, 16), (3, 40, 2000, 16), (2, 300, 33, 16), (2, 2000, 90, 12),
+    (2, 300, 48, 128), (64, 20, 4000, 16)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_sequence_major_scan(batch, seq_len, dim, dstate, io):
+    T = scan_inputs(91, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate, io=io, dt=io,
+                    ctx=[seq_len - b % 3 for b in range(batch)])
+    M = {k: sequence_major(v) if k in ("x", "z", "dt", "B", "C") else v for k, v in T.items()}
+    got = []
+    for src, out in ((T, torch.full_like(T["x"], 7.0)), (M, sequence_major(torch.full_like(T["x"], 7.0)))):
+        state = T["state"].clone()
+        L.ssu_scan_prefill(src["x"], T["A"], src["B"], src["C"], src["dt"], state, out,
+                           dt_bias=T["dt_bias"], D=T["D"], z=src["z"], context_lengths=T["ctx"],
+                           state_indices=T["idx"])
+        got.append((out, state))
+    assert batch == 1 or seq_len == 1 or got[1][0].stride() == (dim, batch * dim, 1)
+    assert_bitwise(got[1][0], got[0][0], "out")
+    assert_bitwise(got[1][1], got[0][1], "state")
+
+
+@pytest.mark.parametrize("batch,seq_len,channels", [(4, 19, 128), (3, 2, 77), (8, 100, 1030)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_sequence_major_conv(batch, seq_len, channels, io):
+    T = conv_inputs(92, batch=batch, seq_len=seq_len, channels=channels, width=4, io=io,
+                    ctx=[max(seq_len - 4 * b, 0) for b in range(batch)])
+    got = []
+    for f in (lambda t: t, sequence_major):
+        pool, out = T["conv_state"].clone(), f(torch.full_like(T["x"], 7.0))
+        L.ssu_conv_prefill(f(T["x"]), T["weight"], T["bias"], pool, out, context_lengths=T["ctx"],
+                           state_indices=T["idx"])
+        got.append((out, pool))
+    assert_bitwise(got[1][0], got[0][0], "out")
+    assert_bitwise(got[1][1], got[0][1], "conv_state")
+
+
+@pytest.mark.parametrize("vocab", [2500, 70001])
+def test_sequence_major_verification(vocab):
+    T = verify_inputs(93, batch=5, tokens=6, vocab=vocab, sharp=6.0)
+    got = []
+    for f in (lambda t: t, sequence_major):
+        acc, nxt = (torch.full((5,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+        ids = torch.full((5, 6), -7, dtype=torch.int32, device="cuda")
+        L.ssu_draft_verify(T["tokens"], f(T["target"]), T["uniforms"], acc, nxt, draft_probs=f(T["draft"]),
+                           accepted_node_ids=ids)
+        got.append((acc, nxt, ids))
+    for a, b in zip(got[1], got[0]):
+        assert_bitwise(a, b, "result")

@@ -179,3 +179,37 @@ def test_overlapping_pools_are_refused(lib, row, chan, tap):
 
 def test_huge_strides_do_not_wrap(lib):
     assert conv_status(lib, state_row_stride=1 << 62, state_chan_stride=1 << 61, state_tap_stride=1) == 1
+
+
+def scan_dims(**kw):
+    d = dict(batch=0, dim=16, dstate=16, ngroups=1, pool_rows=4, state_dtype=0, io_dtype=2,
+             dt_dtype=0, bc_dtype=2, reserved=0, state_row_stride=0)
+    for k in ("x", "z", "out", "dt", "b", "c"):
+        d[k + "_batch_stride"] = d[k + "_token_stride"] = 0
+    d.update(kw)
+    return S.ssu_scan_dims(*d.values())
+
+
+# A null pointer is the first thing refused after the strides: status 1 with its name.
+@pytest.mark.parametrize("bs,ts,taken", [
+    (16, 48, True), (20, 60, True), (16, 1000, True), (128, 16, True), (16, 47, False), (15, 48, False),
+    (17, 49, False), (20, 55, False), (127, 16, False), (16, 16, False), (1 << 61, 1 << 62, False)])
+def test_sequence_major_activations_are_taken(lib, bs, ts, taken):
+    """3 batch entries of 8 tokens of 16 channels: rows that do not overlap are taken
+    in either order of the axes, others refused."""
+    def told(rc, needle):
+        assert rc == 1 and needle in lib.ssu_last_error().decode(), lib.ssu_last_error()
+
+    for name in ("x", "out"):
+        kw = {name + "_batch_stride": bs, name + "_token_stride": ts}
+        told(conv_status(lib, batch=3, **kw), "'x'" if taken else f"{name} batch stride")
+    for name, arg in (("x", "x"), ("z", "z"), ("out", "out"), ("dt", "dt"), ("b", "B"), ("c", "C")):
+        kw = {name + "_batch_stride": bs, name + "_token_stride": ts}
+        rc = lib.ssu_scan_prefill(scan_dims(batch=3, **kw), 8, *([None] * 10), 1, 1, None, None, None, 0, None)
+        told(rc, "'x'" if taken else f"{arg} batch stride")
+    for name, tokens in (("target", 8), ("draft", 9)):
+        kw = dict(batch=3, num_tokens=tokens, vocab=16, max_accept_len=1, prob_dtype=0, reserved=0,
+                  target_batch_stride=0, target_row_stride=0, draft_batch_stride=0, draft_row_stride=0)
+        kw[name + "_batch_stride"], kw[name + "_row_stride"] = bs, ts
+        rc = lib.ssu_draft_verify(S.ssu_verify_dims(*kw.values()), *([None] * 11), 0, None)
+        told(rc, "'tokens'" if taken else f"{name}_probs batch stride")
