@@ -497,6 +497,14 @@ ssu_status check_strides(const char *fn, const char *name, int64_t bs, int64_t t
     return SSU_OK;
 }
 
+// Of a launch that refuses what one launch cannot hold.
+ssu_status launch_status(hipError_t e, const char *fn)
+{
+    if (e == hipErrorInvalidConfiguration)
+        return fail(SSU_ENOTSUP, "%s: too large: 2^32 threads or more", fn);
+    return hip_status(e, fn);
+}
+
 ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len, const void *x,
                      const void *weight, const void *bias, void *conv_state, void *out,
                      int32_t silu, int32_t update_state, const int32_t *context_lengths,
@@ -561,9 +569,8 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
             reach += (__int128)(x.n - 1) * x.stride;
         }
     }
-    if (seq_len > (1 << 30) ||
-        (int64_t)d.batch * ((d.channels + 255) / 256) * ((seq_len + 15) / 16) > 0x7fffffff)
-        return fail(SSU_ENOTSUP, "%s: problem too large", fn);
+    if (seq_len > (1 << 30))
+        return fail(SSU_ENOTSUP, "%s: seq_len %d too large", fn, seq_len);
     if (d.batch == 0 || seq_len == 0)
         return ok();
     const size_t io = io_bytes(d.io_dtype);
@@ -595,7 +602,7 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
     p.state_dtype = d.state_dtype;
     p.silu = silu ? 1 : 0;
     p.update = update_state ? 1 : 0;
-    return hip_status(ssu::launch_conv(p, stream), fn);
+    return launch_status(ssu::launch_conv(p, stream), fn);
 }
 
 ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len, const void *x,
@@ -707,7 +714,7 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
     p.bc_dtype = d.bc_dtype;
     p.dt_softplus = dt_softplus ? 1 : 0;
     p.update = update_state ? 1 : 0;
-    return hip_status(ssu::launch_scan(p, stream), fn);
+    return launch_status(ssu::launch_scan(p, stream), fn);
 }
 
 }  // namespace

@@ -375,7 +375,7 @@ hipError_t launch_conv_cfg(const ConvParams &p, hipStream_t stream)
     s.s_vec = (V * ses) % 8 == 0 && (uintptr_t)p.state % piece == 0 && p.st_row * ses % piece == 0 &&
               (s.layout == kTapsInside || p.st_tap * ses % piece == 0);
     const int64_t blocks = ((int64_t)s.cols * s.tiles + 255) / 256;
-    if (blocks * p.batch > 0x7fffffff)
+    if (!launchable((__int128)blocks * p.batch, 256))
         return hipErrorInvalidConfiguration;
     s.row_blocks = (uint32_t)blocks;
     hipLaunchKernelGGL((ssu_conv_kernel<T, V, W>), dim3((unsigned)(blocks * p.batch)), dim3(256), 0, stream, p, s);

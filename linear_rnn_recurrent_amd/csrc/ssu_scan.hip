@@ -121,7 +121,7 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     q.rows = true;
     for (int waves = 4; waves <= 16 && seq_len > 1; waves *= 2) {
         const double us = sweep_us(waves, ragged, blocks, tiles, seq_len);
-        if (us < best) {
+        if (us < best && launchable(blocks, 64 * waves)) {
             best = us;
             q.rows = false;
             q.sweep = waves;
@@ -137,7 +137,9 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     if (len < 32)
         len = 32;
     chunks = (seq_len + len - 1) / len;
-    if (seq_len <= 16 || best <= chunks_us(chunks > 1, ragged, tiles, seq_len, mega))
+    const __int128 packed = (__int128)batch * seq_len * ngroups * tiles;  // sixteens of B and C
+    if (seq_len <= 16 || best <= chunks_us(chunks > 1, ragged, tiles, seq_len, mega) ||
+        !launchable(packed, kStates) || !launchable(waves * chunks, 64))
         return q;
     q.rows = false;
     q.sweep = 0;

@@ -767,7 +767,8 @@ hipError_t launch_chunks(const ScanParams &p, const ScanPlan &q, hipStream_t str
     const ChunkShape &s = q.s;
     const int64_t cells = (int64_t)p.batch * s.blocks * ((s.chunks + s.team - 1) / s.team);
     const int64_t packed = q.bc_floats / 2 - kStates;
-    if (cells > 0x7fffffff || (packed + 255) / 256 > 0x7fffffff)
+    if (!launchable(cells, 64 * s.team * s.tiles) || !launchable((packed + 255) / 256, 256) ||
+        !launchable((int64_t)p.batch * s.blocks, 1024))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(ssu_scan_pack_kernel, dim3((unsigned)((packed + 255) / 256)), dim3(256), 0,
                        stream, p, s, packed);
@@ -805,7 +806,7 @@ hipError_t launch_sweep(const ScanParams &p, hipStream_t stream)
 {
     const int per_group = (p.dim / p.ngroups + 15) / 16, blocks = per_group * p.ngroups;
     const int tiles = (p.dstate + kStates - 1) / kStates;
-    if ((int64_t)p.batch * blocks > 0x7fffffff)
+    if (!launchable((int64_t)p.batch * blocks, 64 * WAVES))
         return hipErrorInvalidConfiguration;
     const int lds = 4 * (WAVES * 16 * vu_pitch(sweep_tokens(WAVES)) + 2 * WAVES * 64 * 8 + 2 * tiles * 64 * 4 +
                          WAVES * sweep_tokens(WAVES) * 16);

@@ -256,7 +256,7 @@ hipError_t launch_tiles(Kernel kernel, const ScanParams &p, int channels, hipStr
 {
     const int tiles = (p.dim + channels - 1) / channels;
     const int64_t blocks = (int64_t)p.batch * tiles;
-    if (blocks > 0x7fffffff)
+    if (!launchable(blocks, 256))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p, tiles);
     return hipGetLastError();

@@ -213,3 +213,29 @@ def test_sequence_major_activations_are_taken(lib, bs, ts, taken):
         kw[name + "_batch_stride"], kw[name + "_row_stride"] = bs, ts
         rc = lib.ssu_draft_verify(S.ssu_verify_dims(*kw.values()), *([None] * 11), 0, None)
         told(rc, "'tokens'" if taken else f"{name}_probs batch stride")
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="its pointers may not reach a launch on a GPU")
+@pytest.mark.parametrize("batch,seq_len,channels,V", [
+    (1, 8380000, (1 << 20) + 1, 1),   # sixteens of tokens fit a launch, eights do not
+    (1, 1 << 20, 65537, 1),           # workgroups fit in 31 bits, threads do not in 32
+    (1 << 20, 1 << 20, 1 << 20, 8), ((1 << 31) - 1, 1 << 30, (1 << 31) - 1, 1)])
+def test_convolutions_past_one_launch_are_refused(lib, batch, seq_len, channels, V):
+    p = 0x100000
+    d = conv_dims(batch=batch, channels=channels)
+    assert lib.ssu_conv_prefill(d, seq_len, p, p, None, p, p + (16 if V == 8 else 2), 1, 1, None, p, None) == 2
+    assert "too large" in lib.ssu_last_error().decode()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="its pointers may not reach a launch on a GPU")
+@pytest.mark.parametrize("seq_len", [1, 2])
+@pytest.mark.parametrize("batch,dim,dstate", [(1 << 14, 1 << 14, 256), (1 << 16, 1 << 13, 64)])
+def test_scans_past_one_launch_are_refused(lib, seq_len, batch, dim, dstate):
+    p = 0x100000
+    d = scan_dims(batch=batch, dim=dim, dstate=dstate)
+    args = [p] * 5 + [None] * 3 + [p, p + 16, 1]
+    if seq_len == 1:
+        rc = lib.ssu_scan_decode(d, *args, p, None)
+    else:
+        rc = lib.ssu_scan_prefill(d, seq_len, *args, 1, None, p, p, 1 << 60, None)
+    assert rc == 2 and "too large" in lib.ssu_last_error().decode()
