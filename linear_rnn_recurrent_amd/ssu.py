@@ -250,6 +250,8 @@ def _scratch(workspace, need, device, stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         _dense(workspace, "workspace", (torch.uint8,))
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the call on {device}")
     return workspace, workspace.data_ptr(), workspace.numel()
 
 

@@ -239,3 +239,27 @@ def test_scans_past_one_launch_are_refused(lib, seq_len, batch, dim, dstate):
     else:
         rc = lib.ssu_scan_prefill(d, seq_len, *args, 1, None, p, p, 1 << 60, None)
     assert rc == 2 and "too large" in lib.ssu_last_error().decode()
+
+
+@pytest.mark.parametrize("stream", [None, 7040])
+def test_a_workspace_on_another_device_is_refused(stream):
+    class Block:
+        is_cuda, dtype, shape = True, torch.uint8, (100,)
+
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 4096
+
+        def numel(self):
+            return 100
+
+    dev = torch.device("cuda:0")
+    with pytest.raises(ValueError, match="workspace.*cuda:1.*cuda:0"):
+        S._scratch(Block("cuda:1"), 100, dev, stream)
+    here = Block("cuda:0")
+    assert S._scratch(here, 100, dev, stream) == (here, 4096, 100)
