@@ -843,7 +843,7 @@ def _conv_call(x, weight, bias, conv_state, out, silu, update_state, context_len
     else:
         if width != 1:
             _fail("conv_state is required")
-        rows, sdt, ss, sp = batch, dtype, (0, 0, 0), 0
+        rows, sdt, ss, sp = max(batch, 1), dtype, (0, 0, 0), 0
     ip = _vector(state_indices, "state_indices", torch.int32, (batch,), dev)
     d = ssu_conv_dims(batch, channels, width, rows, _DT[dtype], _DT[wdt], _DT[sdt], 0, *xs, *os_,
                       *ss)

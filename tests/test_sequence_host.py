@@ -263,3 +263,8 @@ def test_a_workspace_on_another_device_is_refused(stream):
         S._scratch(Block("cuda:1"), 100, dev, stream)
     here = Block("cuda:0")
     assert S._scratch(here, 100, dev, stream) == (here, 4096, 100)
+
+
+def test_an_empty_convolution_of_width_one_is_a_call_without_work(lib, launched):
+    conv_prefill(None, batch=0, width=1)
+    assert launched[0][1][0].pool_rows > 0  # the library refuses a pool without rows
