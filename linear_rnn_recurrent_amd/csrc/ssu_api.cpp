@@ -761,7 +761,9 @@ ssu_status ssu_scan_prefill(const ssu_scan_dims *dims, int32_t seq_len, const vo
 int64_t ssu_scan_workspace_bytes(const ssu_scan_dims *dims, int32_t seq_len)
 {
     if (!dims || dims->batch < 0 || dims->dim <= 0 || dims->dstate <= 0 || dims->ngroups <= 0 ||
-        dims->dim % dims->ngroups != 0 || seq_len < 0)
+        dims->dim % dims->ngroups != 0 || dims->dstate % 4 != 0 || dims->dstate > 256 ||
+        dims->dim > (1 << 25) || (int64_t)dims->batch * dims->dim > 0x7fffffff || seq_len < 0 ||
+        seq_len > (1 << 30))
         return -1;
     return 4 * ssu::scan_workspace_floats(dims->batch, dims->dim, dims->dstate, dims->ngroups,
                                           seq_len);

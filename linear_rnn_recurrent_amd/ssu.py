@@ -947,14 +947,17 @@ def ssu_scan_prefill(x, A, B, C, dt, state, out, *, dt_bias=None, D=None, z=None
     dt_bias, D [dim] fp32; state [rows, dim, dstate], updated in place unless update_state is
     False; context_lengths, state_indices [batch] int32. out (and C) may be None when only
     the state is wanted (commit of a window: context_lengths = accepted lengths). workspace: a
-    uint8 GPU tensor of at least scan_workspace_bytes(...) bytes (allocated here when None).
+    uint8 GPU tensor of at least scan_workspace_bytes(...) bytes for this call's sizes
+    (allocated here when None).
     """
     return _scan_call(x, A, B, C, dt, state, out, dt_bias, D, z, dt_softplus, update_state,
                       context_lengths, state_indices, workspace, stream, False)
 
 
 def scan_workspace_bytes(batch, seq_len, dim, dstate, ngroups=1):
-    """Bytes of the workspace ssu_scan_prefill needs (no GPU needed)."""
+    """Bytes of the workspace ssu_scan_prefill needs for exactly these sizes (no GPU needed;
+    -1 for sizes that the call refuses). They do not grow with batch or seq_len: a workspace
+    for several shapes needs the largest of their sizes, each of them asked for."""
     d = ssu_scan_dims(batch, dim, dstate, ngroups)
     return int(load_library().ssu_scan_workspace_bytes(d, seq_len))
 

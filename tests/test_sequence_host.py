@@ -268,3 +268,31 @@ def test_a_workspace_on_another_device_is_refused(stream):
 def test_an_empty_convolution_of_width_one_is_a_call_without_work(lib, launched):
     conv_prefill(None, batch=0, width=1)
     assert launched[0][1][0].pool_rows > 0  # the library refuses a pool without rows
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate,ngroups", [
+    (1, 64, 5120, 18, 1), (1, 64, 5120, 260, 1), (1, 64, 5120, 0, 1), (1, (1 << 30) + 1, 64, 16, 1),
+    (1, -1, 64, 16, 1), (-1, 64, 64, 16, 1), (1, 64, 64, 16, 3), (1, 64, (1 << 25) + 1, 16, 1),
+    (1 << 20, 64, 1 << 11, 16, 1)])
+def test_workspace_of_sizes_that_the_scan_refuses(lib, batch, seq_len, dim, dstate, ngroups):
+    assert S.scan_workspace_bytes(batch, seq_len, dim, dstate, ngroups) == -1
+    d = scan_dims(batch=batch, dim=dim, dstate=dstate, ngroups=ngroups, pool_rows=(1 << 31) - 1)
+    assert lib.ssu_scan_prefill(d, seq_len, *([None] * 10), 1, 1, None, None, None, 0, None) in (1, 2)
+    assert "'x'" not in lib.ssu_last_error().decode()
+
+
+def test_workspace_of_a_scan_is_that_of_its_sizes_alone(lib):
+    """What the header says of it: neither batch nor seq_len bounds it, and nothing but
+    the five sizes counts."""
+    need = [S.scan_workspace_bytes(b, 4096, 5120, 16) for b in (1, 2, 4, 8, 16)]
+    assert need[0] > need[2] > 0 and need[3] == 0 < need[4]
+    assert S.scan_workspace_bytes(4, 2048, 5120, 16) == 0 < S.scan_workspace_bytes(1, 2048, 5120, 16)
+    for types in range(3):
+        d = scan_dims(batch=1, dim=5120, pool_rows=9 + types, state_dtype=types, io_dtype=types, dt_dtype=types,
+                      bc_dtype=2 - types, x_token_stride=6000, b_token_stride=33, state_row_stride=5120 * 20)
+        assert lib.ssu_scan_workspace_bytes(d, 4096) == need[0]
+    d = scan_dims(batch=4, dim=5120, pool_rows=4)
+    for given in (need[2] - 1, need[3]):
+        rc = lib.ssu_scan_prefill(d, 4096, *([0x100000] * 5), None, None, None, 0x100000, 0x200000, 1, 1, None,
+                                  None, 0x100000, given, None)
+        assert rc == 1 and f"{need[2]} required" in lib.ssu_last_error().decode()
