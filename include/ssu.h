@@ -430,7 +430,10 @@ ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float
  * call and rounded once, at its end. Long calls run the tokens in chunks side by
  * side: they agree with the token-by-token recurrence to fp32 rounding, not
  * bitwise. dim and the activations' token strides up to 2^25, seq_len up to 2^30
- * (else SSU_ENOTSUP). An infinite entry of A acts as the largest finite one.
+ * (else SSU_ENOTSUP). An infinite entry of A acts as the largest finite one. Where
+ * A dt' > 0, growth past the range of fp32 over some of a call's tokens is taken as
+ * its largest value: a state of 0 stays 0 and large ones overflow, as they do token
+ * by token, but a state far below 1 that would end up finite does not follow.
  * workspace: caller-owned device scratch of at least
  * ssu_scan_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
  * that is 0); contents on entry ignored, on return unspecified; calls sharing a

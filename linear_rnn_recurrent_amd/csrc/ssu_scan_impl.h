@@ -42,6 +42,14 @@ __device__ __forceinline__ float log2_rate(float a)
     return __builtin_isinf(r) ? copysignf(3.402823466e38f, r) : r;
 }
 
+// The decay over several tokens whose dt' sum to `sum`. Growth past the range of
+// fp32 (A dt' > 0) is its largest value: the tokens one by one leave a 0 at 0. (A NaN
+// is in the tokens' own end as well.)
+__device__ __forceinline__ float whole_decay(float rate, float sum)
+{
+    return fminf(__builtin_amdgcn_exp2f(rate * sum), 3.402823466e38f);
+}
+
 __device__ __forceinline__ int row_tokens(const ScanParams &p, int b, int *row)
 {
     *row = p.idx ? p.idx[b] : b;

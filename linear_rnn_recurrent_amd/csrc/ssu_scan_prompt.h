@@ -273,7 +273,7 @@ __device__ __forceinline__ void fold_ends(const ScanParams &p, const ChunkShape 
                     use(c + i, h);
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
-                    h[j] = fmaf(h[j], __builtin_amdgcn_exp2f(a[j] * total[i]), end[i][j]);
+                    h[j] = fmaf(h[j], whole_decay(a[j], total[i]), end[i][j]);
             }
         }
     }
@@ -666,8 +666,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
                 std::make_integer_sequence<int, kSub / 2>());
             float4 *mine = ends + ((buf * WAVES + wave) * 64 + lane) * 2;
             mine[0] = make_float4(h[0], h[1], h[2], h[3]);
-            mine[1] = make_float4(__builtin_amdgcn_exp2f(a[0] * sum), __builtin_amdgcn_exp2f(a[1] * sum),
-                                  __builtin_amdgcn_exp2f(a[2] * sum), __builtin_amdgcn_exp2f(a[3] * sum));
+            mine[1] = make_float4(whole_decay(a[0], sum), whole_decay(a[1], sum), whole_decay(a[2], sum),
+                                  whole_decay(a[3], sum));
             __syncthreads();
             // the wave's start
             const float4 s0 = starts[(starts_now * tiles + k) * 64 + lane];

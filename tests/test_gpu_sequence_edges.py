@@ -1,12 +1,14 @@
 """Calls of the convolution, scan and draft verification at the edges of what the
 header allows: empty batches, streams, layouts."""
+import numpy as np
 import pytest
 import torch
 
 import linear_rnn_recurrent_amd as L
+import oracle
 from gpu_helpers import assert_bitwise, gpu
 from linear_rnn_recurrent_amd import inputs
-from sequence_helpers import conv_inputs, scan_inputs, verify_inputs
+from sequence_helpers import check, conv_inputs, f64, scan_bound, scan_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -212,3 +214,28 @@ def test_sequence_major_verification(vocab):
         got.append((acc, nxt, ids))
     for a, b in zip(got[1], got[0]):
         assert_bitwise(a, b, "result")
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [
+    (64, 17, 600, 16), (8, 64, 2560, 16), (2, 300, 33, 16), (1, 512, 1536, 16), (1, 1900, 40, 16), (2, 300, 48, 128)])
+def test_growth_past_fp32_leaves_a_state_of_zero(batch, seq_len, dim, dstate):
+    """A positive entry of A over tokens without input: token by token a state of 0
+    stays 0, although the growth over all of them is beyond fp32. Five tokens of
+    input at the end. The exponent 12 is known to 2 u relative (A log2 e and its
+    product with dt'), a factor of 24 u a token, over the five 120 u of the term:
+    within the 6 u a token of the bound at 32 tokens or more, and within its 32 u
+    more at 17."""
+    T = scan_inputs(94, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate, io="f32", gate=False, bias=False)
+    T["A"][:, 2] = 12.0
+    T["dt"][:] = 1.0
+    T["x"][:, :-5] = 0.0
+    T["state"].zero_()
+    A, x, B, C, dt = (f64(T[k]) for k in ("A", "x", "B", "C", "dt"))
+    state = np.zeros(T["state"].shape)
+    ref, mag, smag = oracle.channel_scan(x, A, B, C, dt, state, D=f64(T["D"]), softplus=False, idx=f64(T["idx"]))
+    assert np.abs(ref).max() < 1e30
+    out = torch.full_like(T["x"], float("nan"))
+    L.ssu_scan_prefill(T["x"], T["A"], T["B"], T["C"], T["dt"], T["state"], out, D=T["D"], dt_softplus=False,
+                       state_indices=T["idx"])
+    check(out, ref, scan_bound(mag, seq_len, dstate), torch.float32, "out")
+    check(T["state"], state, scan_bound(smag, seq_len, 0), torch.float32, "state")
