@@ -1,4 +1,5 @@
-// What the scan's kernels share: small device helpers, and the plan of a call.
+// What the scan's kernels share: small device helpers, and the plan of a call
+// (ssu_scan_plan.h).
 #pragma once
 
 #include <atomic>
@@ -8,13 +9,12 @@
 #include "ssu_device.h"
 #include "ssu_dpp.h"
 #include "ssu_internal.h"
+#include "ssu_scan_plan.h"
 
 namespace ssu {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kStates = 16;  // state entries of a lane in the chunk kernels
-constexpr int kBatch = 4;    // tokens loaded together
 
 // Rounds to nearest even in one instruction (bf16: v_cvt_pk_bf16_f32).
 template <typename T>
@@ -128,29 +128,5 @@ __device__ __forceinline__ void st1(void *p, int64_t i, float v, int dt)
 }
 
 }  // namespace
-
-// Workspace, in floats: packed B | C [batch][seq_len][ngroups][tiles][2][16],
-// and a line of 32 zeros; chunk ends [batch][chunks + 1][blocks][tiles][16][64]
-// (slot 0 a copy of the pool's state, so that the kernel that writes the pool
-// does not read it; slot c + 1 chunk c's end); chunk sums of dt'
-// [batch][chunks + 1][blocks][64], slot c + 1 likewise. A block is 64 channels
-// of one group.
-struct ChunkShape {
-    int32_t tiles, per_group, blocks, chunk, chunks;
-    int32_t team;  // chunks of one block that share a workgroup: 1, 2 or 4
-    int64_t zeros;  // offset of the zero line in bc
-    float *bc, *start, *sum;
-};
-
-// Tokens of a sweeping wave and step
-constexpr int sweep_tokens(int waves) { return waves == 4 ? 8 : 16; }
-
-// How a call is evaluated (scan_plan).
-struct ScanPlan {
-    bool rows;
-    int32_t sweep;  // waves of a sweeping workgroup: 4, 8 or 16; 0: chunks
-    ChunkShape s;
-    int64_t bc_floats, start_floats, sum_floats;
-};
 
 }  // namespace ssu
