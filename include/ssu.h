@@ -376,7 +376,8 @@ ssu_status ssu_conv_prefill(const ssu_conv_dims *dims, int32_t seq_len, const vo
                             const int32_t *state_indices, hipStream_t stream);
 
 /* ssu_conv_decode -- the same for one token: x, out [batch, channels] (the
- * token strides are ignored). The state is updated. out may be x. */
+ * token strides are ignored). The state is updated. out may be x, with x's
+ * strides. */
 ssu_status ssu_conv_decode(const ssu_conv_dims *dims, const void *x, const void *weight,
                            const void *bias, void *conv_state, void *out, int32_t silu,
                            const int32_t *state_indices, hipStream_t stream);
@@ -411,7 +412,8 @@ typedef struct ssu_scan_dims {
  * [batch, ngroups, dstate]; A [dim, dstate], dt_bias, D [dim] fp32, dense;
  * state [pool_rows, dim, dstate], rows dense, updated in place. A and state
  * are aligned to four elements. Optional: dt_bias, D, z, state_indices.
- * Padding rows: out[b] = +0.0, no pool access. out may be x or z. */
+ * Padding rows: out[b] = +0.0, no pool access. out may be x or z, with its
+ * strides, and overlaps no other input. */
 ssu_status ssu_scan_decode(const ssu_scan_dims *dims, const void *x, const float *A,
                            const void *B, const void *C, const void *dt, const float *dt_bias,
                            const float *D, const void *z, void *state, void *out,

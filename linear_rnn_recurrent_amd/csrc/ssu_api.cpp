@@ -586,6 +586,8 @@ ssu_status conv_call(const char *fn, const ssu_conv_dims *dims, int32_t seq_len,
     SSU_OPTIONAL_PTR(state_indices, 4, fn);
     if (!step && out == x)
         return fail(SSU_EINVAL, "%s: out must not overlap x", fn);
+    if (out == x && d.batch > 1 && p.out_bs != p.x_bs)
+        return fail(SSU_EINVAL, "%s: out in x's place has other strides", fn);
     p.x = x;
     p.weight = weight;
     p.bias = bias;
@@ -680,8 +682,11 @@ ssu_status scan_call(const char *fn, const ssu_scan_dims *dims, int32_t seq_len,
     SSU_OPTIONAL_PTR(z, io, fn);
     SSU_OPTIONAL_PTR(context_lengths, 4, fn);
     SSU_OPTIONAL_PTR(state_indices, 4, fn);
-    if (!step && out && (out == x || out == z || out == dt || out == B || out == C))
+    if (out && (out == B || out == C || (!step && (out == x || out == z || out == dt))))
         return fail(SSU_EINVAL, "%s: out must not overlap an input", fn);
+    if (step && d.batch > 1 && ((out == x && p.out_bs != p.x_bs) || (out == z && p.out_bs != p.z_bs) ||
+                                (out == dt && (p.out_bs != p.dt_bs || d.dt_dtype != d.io_dtype))))
+        return fail(SSU_EINVAL, "%s: out in an input's place has other strides", fn);
     if (!step) {
         const int64_t need = ssu_scan_workspace_bytes(dims, seq_len);
         if (need > 0)

@@ -296,3 +296,28 @@ def test_workspace_of_a_scan_is_that_of_its_sizes_alone(lib):
         rc = lib.ssu_scan_prefill(d, 4096, *([0x100000] * 5), None, None, None, 0x100000, 0x200000, 1, 1, None,
                                   None, 0x100000, given, None)
         assert rc == 1 and f"{need[2]} required" in lib.ssu_last_error().decode()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="its pointers may not reach a launch on a GPU")
+def test_single_tokens_in_an_inputs_place(lib):
+    """out may be x or z of the same strides; rows of other strides would overlap other
+    rows' inputs, and B and C are read by every channel."""
+    p, q = 0x100000, 0x200000
+    told = lambda: lib.ssu_last_error().decode()  # noqa: E731
+
+    def scan(x=p, z=None, B=p, C=p, dt=p, **kw):
+        d = scan_dims(batch=2, **kw)
+        return lib.ssu_scan_decode(d, x, p, B, C, dt, None, None, z, p, q, 1, None, None)
+
+    def conv(x, **kw):
+        return lib.ssu_conv_decode(conv_dims(batch=2, **kw), x, p, None, p, q, 1, None, None)
+
+    for kw in (dict(B=q), dict(C=q)):
+        assert scan(**kw) == 1 and "overlap" in told(), kw
+    for kw in (dict(x=q, x_batch_stride=32), dict(z=q, out_batch_stride=24), dict(x=q, z=q, z_batch_stride=48)):
+        assert scan(**kw) == 1 and "strides" in told(), kw
+    assert conv(q, x_batch_stride=32) == 1 and "strides" in told()
+    # taken (the launch fails without a GPU)
+    for rc in (scan(x=q), scan(z=q), scan(x=q, x_batch_stride=24, out_batch_stride=24), conv(q),
+               conv(q, x_batch_stride=17, out_batch_stride=17), scan(x=p, x_batch_stride=32)):
+        assert rc == 3, told()
