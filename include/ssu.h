@@ -332,11 +332,15 @@ int64_t ssu_gdn_workspace_bytes(const ssu_gdn_dims *dims);
  * token strides are given in elements (0 = dense; a token stride is at least
  * the row's length). Either axis may lie outside the other, batch-major
  * (batch stride >= the row's tokens) or sequence-major (token stride >= the
- * batch's rows); other strides are refused, as they could overlap. All pointers need the alignment of their element unless
- * stated. Pool rows, negative state_indices and context_lengths are as in
- * ssu_decode and ssu_prefill. A call that needs 2^32 threads or more is refused
- * (SSU_ENOTSUP): a convolution's thread takes eight tokens of 2 to 16 bytes of
- * channels, a scan's of one token four state entries of one or two channels.
+ * batch's rows); other strides are refused, as they could overlap. All
+ * pointers need the alignment of their element unless stated. Pool rows,
+ * negative state_indices and context_lengths are as in ssu_decode and
+ * ssu_prefill; indices are below pool_rows, and those of a call that updates
+ * the pool are distinct (update_state == 0 may name a row more than once,
+ * several windows on one state). A call that needs 2^32 threads or more is
+ * refused (SSU_ENOTSUP): a convolution's thread takes eight tokens of 2 to 16
+ * bytes of channels, a scan's of one token four state entries of one or two
+ * channels.
  * ---------------------------------------------------------------------- */
 typedef struct ssu_conv_dims {
     int32_t batch;

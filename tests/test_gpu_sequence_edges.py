@@ -239,3 +239,26 @@ def test_growth_past_fp32_leaves_a_state_of_zero(batch, seq_len, dim, dstate):
                        state_indices=T["idx"])
     check(out, ref, scan_bound(mag, seq_len, dstate), torch.float32, "out")
     check(T["state"], state, scan_bound(smag, seq_len, 0), torch.float32, "state")
+
+
+@pytest.mark.parametrize("batch,seq_len,dim,dstate", [(16, 5, 1100, 16), (8, 40, 1000, 24), (3, 2000, 90, 12)])
+def test_several_windows_on_one_state(batch, seq_len, dim, dstate):
+    """Read-only calls may name a pool row more than once: each window's outputs are
+    those of the window alone."""
+    T = scan_inputs(95, batch=batch, seq_len=seq_len, dim=dim, dstate=dstate, idx=[2] * batch)
+    c = conv_inputs(96, batch=batch, seq_len=seq_len, channels=dim, width=4, idx=[1] * batch)
+    pools = T["state"].clone(), c["conv_state"].clone()
+    spread = T["state"][2:3].repeat(batch, 1, 1), c["conv_state"][1:2].repeat(batch, 1, 1)
+    got = []
+    for scan_pool, conv_pool, scan_idx, conv_idx in ((T["state"], c["conv_state"], T["idx"], c["idx"]),
+                                                     (*spread, None, None)):
+        out, u = torch.full_like(T["x"], 7.0), torch.full_like(c["x"], 7.0)
+        L.ssu_scan_prefill(T["x"], T["A"], T["B"], T["C"], T["dt"], scan_pool, out, dt_bias=T["dt_bias"],
+                           D=T["D"], z=T["z"], state_indices=scan_idx, update_state=False)
+        L.ssu_conv_prefill(c["x"], c["weight"], c["bias"], conv_pool, u, state_indices=conv_idx,
+                           update_state=False)
+        got.append((out, u))
+    for a, b in zip(*got):
+        assert_bitwise(a, b, "window")
+    assert_bitwise(T["state"], pools[0], "state")
+    assert_bitwise(c["conv_state"], pools[1], "conv_state")
