@@ -262,3 +262,48 @@ def test_several_windows_on_one_state(batch, seq_len, dim, dstate):
         assert_bitwise(a, b, "window")
     assert_bitwise(T["state"], pools[0], "state")
     assert_bitwise(c["conv_state"], pools[1], "conv_state")
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_calls_on_a_stream_of_their_own_in_a_graph(fork):
+    """Captured with stream=, the capture's own or one that forks off it: the scratch
+    stays the graph's, whatever is allocated and freed between replays."""
+    T = scan_inputs(97, batch=1, seq_len=1900, dim=200, dstate=16)
+    V = verify_inputs(98, batch=3, tokens=4, vocab=70001)
+    start, out = T["state"].clone(), torch.zeros_like(T["x"])
+    acc, nxt = (torch.full((3,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+
+    def calls(stream=None):
+        L.ssu_scan_prefill(T["x"], T["A"], T["B"], T["C"], T["dt"], T["state"], out, dt_bias=T["dt_bias"],
+                           D=T["D"], z=T["z"], state_indices=T["idx"], stream=stream)
+        L.ssu_draft_verify(V["tokens"], V["target"], V["uniforms"], acc, nxt, draft_probs=V["draft"],
+                           stream=stream)
+
+    calls()
+    want = [t.clone() for t in (out, T["state"], acc, nxt)]
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        stream = side if fork else here
+        if fork:
+            side.wait_stream(here)
+        calls(stream)
+        if fork:
+            here.wait_stream(side)
+    for rep in range(3):
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 14, 1 << 18, 1 << 20, 1 << 22)]
+        with torch.cuda.stream(side):
+            junk += [torch.full((n,), float("nan"), device="cuda") for n in (1 << 14, 1 << 18, 1 << 20, 1 << 22)]
+        T["state"].copy_(start)
+        out.zero_(), acc.zero_(), nxt.zero_()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in junk]
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((out, T["state"], acc, nxt), want):
+            assert_bitwise(a, b, f"replay {rep}")
+        for a, b in zip(junk, kept):
+            assert_bitwise(a, b, "memory of others")
+        del junk, kept
