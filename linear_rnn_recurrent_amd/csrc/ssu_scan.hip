@@ -18,7 +18,8 @@
 // their true start. Per token, channel and state entry that is a product, an
 // exponential at half rate, two products with B and two multiply-adds for the
 // state, one for the output: 8 issue slots of the vector ALU, which bounds it (11
-// counted, with softplus, gate and exchange: busy 72% of 57 us at 8 x 777 x 2560).
+// counted, with softplus, gate and exchange: busy 72% of 57 us at 8 x 777 x 2560 with
+// the uneven lengths that the counters were taken with; 50 to 74 us by the lengths).
 //
 // Chunks (ssu_scan_prompt.h; long prompts of few channels): a lane is a channel
 // and holds 16 state entries, which makes B and C the same for the whole wave

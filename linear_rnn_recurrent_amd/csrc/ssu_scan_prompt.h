@@ -523,11 +523,13 @@ __device__ __forceinline__ void ld_bc4(const char *base, uint32_t off, int dt, f
 //
 // kSub: 16 spreads a step's exchange over more tokens, 8 wastes less at the rows'
 // ends and holds half the decays. 4 waves are what short and uneven rows take, with
-// 8 (us with 8 | 16: 8 x 777 x 2560 uneven 59 | 64, 32 x 128 x 2560 74 | 83,
-// 4 x 512 x 2560 54 | 52); 8 and 16 waves take longer rows, with 16 (8 waves: 53 |
-// 50, 16 waves: 1 x 2048 x 1536 72 | 66; all before C went through LDS). The rest
-// beside the vector ALU is the exchange's barriers and the rows' ends. Four waves a
-// SIMD leave the 128 registers that kSub 16 needs: at five it spills (115 us for 64).
+// 8 (us with 8 | 16: 8 x 777 x 2560 uneven 74 | 77, 32 x 128 x 2560 73 | 80,
+// 4 x 512 x 2560 51 | 47, where 8 waves take 45); 8 and 16 waves take longer rows,
+// with 16 (8 waves, with 8 | 16: 4 x 512 x 2560 50 | 45, 1 x 2048 x 1536 88 | 74; 16
+// waves: 1 x 2048 x 1536 71 | 60, 2 x 509 x 1536 dstate 64 59 | 51). The rest beside
+// the vector ALU is the exchange's barriers and the rows' ends. Four waves a SIMD
+// leave the 128 registers that kSub 16 needs: at five it spills (115 us for 64, before
+// C went through LDS).
 template <typename IOT, typename DTT, int BC, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 4) void ssu_scan_sweep_kernel(
     const ScanParams p, int per_group, int blocks, int tiles)

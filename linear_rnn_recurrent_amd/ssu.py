@@ -246,8 +246,11 @@ def _scratch(workspace, need, device, stream):
     if workspace is None:
         if need <= 0:
             return None, 0, 0
-        with _on(stream, device):
+        if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with _on(stream, device):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
         _dense(workspace, "workspace", (torch.uint8,))
         if workspace.device != device:
@@ -864,7 +867,7 @@ def ssu_conv_prefill(x, weight, bias, conv_state, out, *, silu=True, context_len
 
     x, out [batch, seq_len, channels] (slices of wider tensors are fine: channels dense,
     the other two axes in either order); weight [channels, width]; bias [channels] or None; conv_state
-    [rows, channels, width-1], any strides, updated in place unless update_state is False;
+    [rows, channels, width-1], its axes in any order, updated in place unless update_state is False;
     context_lengths, state_indices [batch] int32. out may be None when only the state is
     wanted (commit of a window: context_lengths = accepted lengths).
     """
