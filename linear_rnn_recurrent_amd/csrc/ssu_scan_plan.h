@@ -111,7 +111,11 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     int64_t held = 4;  // states that a channel's lanes hold: a power of two
     while (held < dstate)
         held *= 2;
-    double best = rows_us(ragged, seq_len, mega * held / (tiles * kStates));
+    // (INFINITY: the evaluation does not fit one launch)
+    const int64_t lanes = held > 16 ? held / 4 : 4, per_wg = 256 / lanes * (seq_len > 1 ? 1 : 2);
+    double best = launchable((__int128)batch * ((dim + per_wg - 1) / per_wg), 256)
+                      ? rows_us(ragged, seq_len, mega * held / (tiles * kStates))
+                      : INFINITY;
     q.rows = true;
     for (int waves = 4; waves <= 16 && seq_len > 1; waves *= 2) {
         const double us = sweep_us(waves, ragged, blocks, tiles, seq_len);
@@ -131,16 +135,18 @@ ScanPlan scan_plan(int64_t batch, int64_t dim, int64_t dstate, int64_t ngroups, 
     if (len < 32)
         len = 32;
     chunks = (seq_len + len - 1) / len;
+    const int most = tiles <= 4 ? 4 : tiles <= 8 ? 2 : 1;
+    const int team = chunks == 1 ? 1 : (chunks == 2 && most > 2) ? 2 : most;
     const __int128 packed = (__int128)batch * seq_len * ngroups * tiles;  // sixteens of B and C
     if (seq_len <= 16 || best <= chunks_us(chunks > 1, ragged, tiles, seq_len, mega) ||
-        !launchable(packed, kStates) || !launchable(waves * chunks, 64))
+        !launchable(packed, kStates) ||
+        !launchable(batch * q.s.blocks * ((chunks + team - 1) / team), (int)(64 * team * tiles)))
         return q;
     q.rows = false;
     q.sweep = 0;
     q.s.chunk = (int32_t)(len > seq_len ? seq_len : len);
     q.s.chunks = (int32_t)chunks;
-    const int most = q.s.tiles <= 4 ? 4 : q.s.tiles <= 8 ? 2 : 1;
-    q.s.team = chunks == 1 ? 1 : (chunks == 2 && most > 2) ? 2 : most;
+    q.s.team = team;
     q.bc_floats = (batch * seq_len * ngroups * q.s.tiles + 1) * (2 * kStates);
     q.start_floats = batch * (chunks + 1) * q.s.blocks * q.s.tiles * (kStates * 64);
     q.sum_floats = batch * (chunks + 1) * q.s.blocks * 64;

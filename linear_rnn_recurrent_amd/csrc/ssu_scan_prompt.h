@@ -3,6 +3,8 @@
 // out by ssu_scan_prompt_{f32,f16,bf16}.hip.
 #pragma once
 
+#include <algorithm>
+
 #include "ssu_scan_impl.h"
 
 namespace ssu {
@@ -16,10 +18,10 @@ struct Place {
     int b, team, blk, g, d, dl;  // .., group, channel (clamped), whether its lane is live
 };
 
-__device__ __forceinline__ Place place(const ScanParams &p, const ChunkShape &s, int teams)
+__device__ __forceinline__ Place place(const ScanParams &p, const ChunkShape &s, int teams, int first = 0)
 {
     Place q;
-    int i = blockIdx.x;
+    int i = first + blockIdx.x;
     q.blk = i % s.blocks;
     i /= s.blocks;
     q.team = i % teams;
@@ -281,10 +283,11 @@ __device__ __forceinline__ void fold_ends(const ScanParams &p, const ChunkShape 
 }
 
 // The last state where no outputs are wanted; a wave has one state entry of a
-// tile.
-__global__ __launch_bounds__(1024) void ssu_scan_last_kernel(const ScanParams p, const ChunkShape s)
+// tile. `first`: the launch's first block.
+__global__ __launch_bounds__(1024) void ssu_scan_last_kernel(const ScanParams p, const ChunkShape s,
+                                                             int first)
 {
-    const Place q = place(p, s, 1);
+    const Place q = place(p, s, 1, first);
     const int tile = blockIdx.y;
     int row;
     const int len = row_tokens(p, q.b, &row);
@@ -769,8 +772,7 @@ hipError_t launch_chunks(const ScanParams &p, const ScanPlan &q, hipStream_t str
     const ChunkShape &s = q.s;
     const int64_t cells = (int64_t)p.batch * s.blocks * ((s.chunks + s.team - 1) / s.team);
     const int64_t packed = q.bc_floats / 2 - kStates;
-    if (!launchable(cells, 64 * s.team * s.tiles) || !launchable((packed + 255) / 256, 256) ||
-        !launchable((int64_t)p.batch * s.blocks, 1024))
+    if (!launchable(cells, 64 * s.team * s.tiles) || !launchable((packed + 255) / 256, 256))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(ssu_scan_pack_kernel, dim3((unsigned)((packed + 255) / 256)), dim3(256), 0,
                        stream, p, s, packed);
@@ -783,9 +785,14 @@ hipError_t launch_chunks(const ScanParams &p, const ScanPlan &q, hipStream_t str
     if (e != hipSuccess)
         return e;
     if (!p.out) {
-        hipLaunchKernelGGL(ssu_scan_last_kernel, dim3((unsigned)(p.batch * s.blocks), s.tiles),
-                           dim3(1024), 0, stream, p, s);
-        return hipGetLastError();
+        constexpr int MOST = 1 << 21;  // workgroups of a launch: 2^31 threads
+        for (int first = 0; e == hipSuccess && first < p.batch * s.blocks; first += MOST) {
+            hipLaunchKernelGGL(ssu_scan_last_kernel,
+                               dim3((unsigned)std::min(MOST, p.batch * s.blocks - first), s.tiles),
+                               dim3(1024), 0, stream, p, s, first);
+            e = hipGetLastError();
+        }
+        return e;
     }
     const int lds = 4 * 64 * s.team * s.tiles *
                     ((s.chunks > 1 ? kStates : 0) + (s.tiles > 1 ? 2 * kBatch : 0));

@@ -307,3 +307,23 @@ def test_calls_on_a_stream_of_their_own_in_a_graph(fork):
         for a, b in zip(junk, kept):
             assert_bitwise(a, b, "memory of others")
         del junk, kept
+
+
+def test_commit_of_more_blocks_than_a_launch_holds():
+    """A group of each channel, so that every channel is a block of its own: 2,252,800
+    blocks, above the 2^21 that one launch of the last states takes. The reference is
+    the recurrence in 64 bits."""
+    batch, seq_len, dim, dstate = 2200, 17, 1024, 16
+    g = torch.Generator(device="cuda").manual_seed(99)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, dt = r(batch, seq_len, dim).bfloat16(), r(batch, seq_len, dim).bfloat16()
+    B = r(batch, seq_len, dim, dstate).bfloat16()
+    A, state = -torch.exp(r(dim, dstate)), r(batch, dim, dstate)
+    h, mag = state.double(), state.double().abs()
+    for t in range(seq_len):
+        v = torch.nn.functional.softplus(dt[:, t].double())[..., None]
+        decay, u = torch.exp(v * A.double()), B[:, t].double() * v * x[:, t].double()[..., None]
+        h, mag = h * decay + u, mag * decay + u.abs()
+    assert L.scan_workspace_bytes(batch, seq_len, dim, dstate, dim) > 0
+    L.ssu_scan_prefill(x, A, B, None, dt, state, None)
+    assert bool(((state.double() - h).abs() <= (32 + 6 * seq_len) * 2.0 ** -24 * mag + 1e-37).all())

@@ -86,3 +86,14 @@ def test_sizes_past_one_launch_take_no_chunks(plan):
     for size in [(64, 65536, 1024, 128, 8, False), (1, 1 << 30, 64, 16, 4, True), (1, 1 << 28, 64, 16, 1, False)]:
         assert plan([size])[0][0] != "chunks", size
     assert plan([(1, (1 << 28) - 1, 64, 16, 1, False)])[0][0] == "chunks"
+
+
+@pytest.mark.parametrize("size,kind", [
+    # a block of each channel, 2^22 blocks and more: chunks as long as their own launches fit
+    ((4096, 40, 1024, 16, 1024, False), "chunks"), ((8192, 20, 1024, 16, 1024, False), "chunks"),
+    # rows of 64 lanes past 2^32 threads, sweeps within
+    ((8192, 2, 8192, 256, 1, False), "sweep"), ((8192, 3, 8192, 256, 1, True), "sweep"),
+    # the rows' launch just fits
+    ((4095, 2, 16384, 256, 1, False), "rows"), ((1 << 16, 1, 1 << 15, 16, 1, False), "rows")])
+def test_the_choice_keeps_to_what_one_launch_holds(plan, size, kind):
+    assert plan([size])[0][0] == kind
