@@ -101,9 +101,9 @@ struct GdnParams {
 int64_t gdn_workspace_floats(int64_t batch, int64_t hidden, int64_t hq, int64_t hv, int64_t d);
 hipError_t launch_gdn(const GdnParams &p, hipStream_t stream);
 
-// Whether one launch may have so many workgroups: HIP wants less than 2^32 threads
-// along an axis. Launches of the sequence calls that may not return
-// hipErrorInvalidConfiguration before they launch anything.
+// Whether one launch may have so many workgroups along an axis: HIP takes less than
+// 2^32 threads. A sequence call that needs more is not launched: its launch_* returns
+// hipErrorInvalidConfiguration.
 inline bool launchable(__int128 groups, int threads) { return groups * threads < ((__int128)1 << 32); }
 
 // Causal convolution over seq_len tokens (1 for a single token). Strides in

@@ -327,3 +327,50 @@ def test_commit_of_more_blocks_than_a_launch_holds():
     assert L.scan_workspace_bytes(batch, seq_len, dim, dstate, dim) > 0
     L.ssu_scan_prefill(x, A, B, None, dt, state, None)
     assert bool(((state.double() - h).abs() <= (32 + 6 * seq_len) * 2.0 ** -24 * mag + 1e-37).all())
+
+
+def test_older_calls_on_a_forked_stream_in_a_graph():
+    """What a tree verify and a gated-delta-rule step allocate for a stream that forks
+    off a capture stays the graph's."""
+    side = torch.cuda.Stream()
+    w = inputs.tree_workload(batch=3, num_nodes=24, nheads=2, dim=32, dstate=32, ngroups=1, pool_rows=5, seed=33)
+    T = {k: gpu(v) for k, v in w.tensors.items()}
+    d = inputs.gdn_workload(batch=5, hidden=256, num_q_heads=2, num_v_heads=4, head_dim=64, conv_width=4,
+                            pool_rows=8, seed=34)
+    G = {k: gpu(v) for k, v in d.tensors.items()}
+    start = {k: G[k].clone() for k in ("conv_state", "ssm_state")}
+    out = torch.zeros_like(T["x"])
+
+    def calls(stream=None):
+        L.ssu_tree_verify(T["x"], T["A"], T["B"], T["C"], T["dt"], T["state"], out, T["parent_ids"],
+                          depths=T["depths"], dt_bias=T["dt_bias"], D=T["D"], z=T["z"],
+                          state_indices=T["state_indices"], stream=stream)
+        return L.ssu_gdn_decode(G["hidden_states"], G["w_ba"], G["mixed_qkv"], G["conv_weight"], G["conv_bias"],
+                                G["conv_state"], G["A_log"], G["dt_bias"], d.dims["scale"], G["ssm_state"],
+                                G["state_indices"], num_q_heads=2, stream=stream)
+
+    def reset():
+        for k, v in start.items():
+            G[k].copy_(v)
+        out.zero_()
+
+    y = calls()
+    want = [t.clone() for t in (out, y, G["conv_state"], G["ssm_state"])]
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        y = calls(side)
+        here.wait_stream(side)
+    for rep in range(3):
+        reset()
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 8, 1 << 14, 1 << 18)]
+        with torch.cuda.stream(side):
+            junk += [torch.full((n,), float("nan"), device="cuda") for n in (1 << 8, 1 << 14, 1 << 18)]
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((out, y, G["conv_state"], G["ssm_state"]), want):
+            assert_bitwise(a, b, f"replay {rep}")
+        assert all(bool(torch.isnan(t).all()) for t in junk)
