@@ -525,6 +525,174 @@ ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
 int64_t ssu_verify_workspace_bytes(const ssu_verify_dims *dims);
 
 /* ------------------------------------------------------------------------
+ * The gated delta rule on given q, k and v, over a paged state pool: prompts,
+ * windows of drafted tokens and single tokens of the layer whose fused
+ * single-token step is ssu_gdn_decode. Strides, pool rows, negative
+ * state_indices and context_lengths are as in the scan above; a token's
+ * [heads, head_dim] is dense.
+ * ---------------------------------------------------------------------- */
+typedef struct ssu_delta_dims {
+    int32_t batch;
+    int32_t num_q_heads;  /* Hq: q and k heads */
+    int32_t num_v_heads;  /* HV: value heads, a multiple of Hq; value head h reads q/k head h / (HV/Hq) */
+    int32_t head_dim;     /* D = K = V, in {32, 64, 128, 256} (else SSU_ENOTSUP) */
+    int32_t pool_rows;
+    int32_t use_qk_l2norm;
+    int32_t state_dtype;  /* state: SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t io_dtype;     /* q, k, v, out */
+    int32_t gate_dtype;   /* a, b */
+    int32_t bias_dtype;   /* dt_bias */
+    int64_t state_row_stride; /* elements; 0 = HV * D * D */
+    int64_t q_batch_stride, q_token_stride;
+    int64_t k_batch_stride, k_token_stride;
+    int64_t v_batch_stride, v_token_stride;
+    int64_t a_batch_stride, a_token_stride;
+    int64_t b_batch_stride, b_token_stride;
+    int64_t out_batch_stride, out_token_stride;
+} ssu_delta_dims;
+
+/* ssu_delta_decode -- one token. With r = state_indices[b] (or b), value head h
+ * and j = h / (HV/Hq):
+ *   g    = -exp(A_log[h]) * softplus(a[b,h] + dt_bias[h]), beta = sigmoid(b[b,h]);
+ *          with A_log NULL g = a[b,h] and beta = b[b,h] (dt_bias is NULL then)
+ *   q, k = q[b,j], k[b,j], each divided by sqrt(its sum of squares + 1e-6) when
+ *          use_qk_l2norm; q *= scale (scale <= 0 or NaN selects 1/sqrt(D))
+ *   S    = state[r,h] ([D(v), D(k)], V-major, K-last) * exp(g)
+ *   S[v][:] += beta * (v[b,h,v] - S[v][:].k) k;   out[b,h,v] = S[v][:].q
+ * Layouts: q, k [batch, Hq, D]; v, out [batch, HV, D]; a, b [batch, HV] (the
+ * token strides are ignored); A_log [HV] fp32, dt_bias [HV]; state
+ * [pool_rows, HV, D, D], rows dense, updated in place, 16-byte aligned, as are
+ * its rows. g is meant to be at most 0; a larger one is followed as it is.
+ * Optional: A_log, dt_bias, state_indices. Padding rows: out[b] = +0.0, no pool
+ * access. out may be v, with its strides, and overlaps no other input. */
+ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const void *k,
+                            const void *v, const void *a, const void *b, const float *A_log,
+                            const void *dt_bias, float scale, void *state, void *out,
+                            const int32_t *state_indices, hipStream_t stream);
+
+/* ssu_delta_prefill -- seq_len tokens in one call: row b runs its first
+ * L_b = clamp(context_lengths[b], 0, seq_len) tokens through the step of
+ * ssu_delta_decode in order; out[b,t] = +0.0 for t >= L_b, where no input is
+ * read. q, k [batch, seq_len, Hq, D]; v, out [batch, seq_len, HV, D]; a, b
+ * [batch, seq_len, HV]. With update_state == 0 the pool is only read (a window
+ * of drafted tokens; to commit k of them, call again with context_lengths = k).
+ * out may be NULL when the state is updated (q is not read then and may be
+ * NULL). out must not overlap an input (equal pointers are refused). Rows with
+ * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
+ * call and rounded once, at its end. Long calls with fp16 or bf16 q, k, v and
+ * out, 16-byte aligned rows of them and D in {64, 128} run the tokens in chunks
+ * on the matrix cores: they agree with the token-by-token recurrence to fp32
+ * rounding, not bitwise. A row of q or k whose sum of squares leaves fp32's
+ * range is undefined. seq_len up to 2^30 and token strides up to 2^25 (else
+ * SSU_ENOTSUP), and so is a call that needs 2^32 threads (a thread has eight
+ * state entries of four or eight rows).
+ * workspace: caller-owned device scratch of at least
+ * ssu_delta_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
+ * that is 0); contents on entry ignored, on return unspecified; calls sharing a
+ * workspace must be ordered (one stream). */
+ssu_status ssu_delta_prefill(const ssu_delta_dims *dims, int32_t seq_len, const void *q,
+                             const void *k, const void *v, const void *a, const void *b,
+                             const float *A_log, const void *dt_bias, float scale, void *state,
+                             void *out, int32_t update_state, const int32_t *context_lengths,
+                             const int32_t *state_indices, void *workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace ssu_delta_prefill needs for exactly this batch, heads,
+ * head_dim, io_dtype and seq_len (nothing else in dims counts); 0 where the
+ * tokens run one by one. -1 if dims is NULL or the call refuses one of these.
+ * No HIP call. */
+int64_t ssu_delta_workspace_bytes(const ssu_delta_dims *dims, int32_t seq_len);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm around the recurrences.
+ * ---------------------------------------------------------------------- */
+#define SSU_E4M3 4 /* 8 bits: sign, 4 of exponent (bias 7), 3 of mantissa, no infinities; ssu_rms_norm's out only */
+
+typedef struct ssu_norm_dims {
+    int32_t batch;
+    int32_t num_tokens;     /* rows: batch * num_tokens */
+    int32_t columns;        /* n */
+    int32_t group;          /* entries that are normed together; divides n */
+    int32_t scale_block;    /* columns that share a scale (SSU_E4M3); divides n; 0 otherwise */
+    int32_t weight_columns; /* length of weight: n or group */
+    int32_t io_dtype;       /* x, z: SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t weight_dtype;   /* the same three */
+    int32_t residual_dtype; /* the same three */
+    int32_t out_dtype;      /* the same three, or SSU_E4M3 */
+    int32_t unit_offset;    /* non-zero: the factor is 1 + weight */
+    int32_t gate_first;     /* non-zero: the gate comes before the norm, else behind it */
+    int64_t x_batch_stride, x_token_stride;
+    int64_t z_batch_stride, z_token_stride;
+    int64_t residual_batch_stride, residual_token_stride;
+    int64_t out_batch_stride, out_token_stride;
+} ssu_norm_dims;
+
+/* ssu_rms_norm -- for every row, in fp32:
+ *   h = x;  h += residual, and residual = h (rounded), if residual is given
+ *   h *= silu(z) if z is given and gate_first
+ *   y = h / sqrt(mean of h^2 over its group + eps) * weight (or 1 + weight)
+ *   y *= silu(z) if z is given and not gate_first
+ *   out = y rounded; for SSU_E4M3, per block of scale_block columns,
+ *   scales = max(max |y| / 448, 2^-126) and out = y / scales rounded to nearest
+ *   even (a block of zeros has the scale 2^-126; a NaN makes its block's scale NaN).
+ * Layouts: x, z, residual, out [batch, num_tokens, n], strides as in the scan;
+ * weight dense, [n] or, the same for each group, [group]; scales dense
+ * [batch, num_tokens, n / scale_block] fp32. The group (for SSU_E4M3 the larger
+ * of group and scale_block) is at most 2^15 columns (else SSU_ENOTSUP). With
+ * SSU_E4M3 and group != scale_block the larger is a multiple of the smaller, which
+ * is a power of two from 8 to 512 (else SSU_ENOTSUP). Optional: residual, z,
+ * scales (given for SSU_E4M3 only). out may be x or z with its type and strides;
+ * residual overlaps nothing. eps is at least 0. */
+ssu_status ssu_rms_norm(const ssu_norm_dims *dims, const void *x, const void *weight,
+                        void *residual, const void *z, void *out, float *scales, float eps,
+                        hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities
+ * ---------------------------------------------------------------------- */
+#define SSU_MAX_TOP 32 /* most alternatives of ssu_token_logprobs */
+
+typedef struct ssu_logprob_dims {
+    int32_t batch;
+    int32_t num_tokens; /* T */
+    int32_t vocab;      /* V, 1..2^24 */
+    int32_t top;        /* k: alternatives, 0..min(SSU_MAX_TOP, V) */
+    int32_t logit_dtype; /* SSU_F32, SSU_F16 or SSU_BF16 */
+    int32_t reserved;   /* must be 0 */
+    int64_t logit_batch_stride, logit_row_stride; /* elements, as the activations' above */
+} ssu_logprob_dims;
+
+/* ssu_token_logprobs -- for every row b and t < L_b = clamp(context_lengths[b], 0, T),
+ * with x = logits[b,t], m = max x and lse = m + log sum exp(x - m):
+ *   logprobs[b,t]       = x[tokens[b,t]] - lse (-inf for a token outside [0, V))
+ *   entropy[b,t]        = -sum p log p, p = exp(x - lse)
+ *   top_ids[b,t,i]      = the k largest x in descending order, equal ones by index
+ *   top_logprobs[b,t,i] = x[top_ids[b,t,i]] - lse
+ * A logit of -inf has no probability; a row of nothing else has log
+ * probabilities of -inf, entropy 0 and the ids 0..k-1. A row with a NaN or
+ * +inf has NaN log probabilities (but of tokens outside [0, V)) and entropy,
+ * and as ids k different ones of [0, V). For t >= L_b and padding rows
+ * (state_indices[b] < 0): 0, 0, -1, 0, and no logit is read.
+ * Layouts: logits [batch, T, V], tokens, logprobs, entropy [batch, T],
+ * top_ids, top_logprobs [batch, T, k], all but logits dense. Optional: entropy,
+ * top_ids, top_logprobs (both or neither; top > 0 with them, ignored without),
+ * context_lengths, state_indices. batch * T up to 2^25 (else SSU_ENOTSUP).
+ * workspace: caller-owned device scratch of at least
+ * ssu_logprobs_workspace_bytes(dims) bytes, 16-byte aligned (NULL where that is
+ * 0: many rows); contents on entry ignored, on return unspecified; calls sharing
+ * a workspace must be ordered (one stream). */
+ssu_status ssu_token_logprobs(const ssu_logprob_dims *dims, const void *logits,
+                              const int32_t *tokens, const int32_t *context_lengths,
+                              const int32_t *state_indices, float *logprobs, float *entropy,
+                              int32_t *top_ids, float *top_logprobs, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace ssu_token_logprobs needs for exactly these batch,
+ * num_tokens, vocab and top (the parts of a split vocabulary); -1 if dims is
+ * NULL or one of them is out of range. No HIP call. */
+int64_t ssu_logprobs_workspace_bytes(const ssu_logprob_dims *dims);
+
+/* ------------------------------------------------------------------------
  * Row movement between a resident pool and contiguous working rows. A row is
  * row_bytes bytes (the trailing dimensions of one pool row, any dtype); rows
  * of a buffer are `stride` bytes apart (0 = row_bytes, >= row_bytes

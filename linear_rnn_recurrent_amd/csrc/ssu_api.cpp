@@ -858,6 +858,322 @@ ssu_status ssu_draft_verify(const ssu_verify_dims *dims, const int32_t *tokens,
 
 namespace {
 
+ssu_status delta_call(const char *fn, const ssu_delta_dims *dims, int32_t seq_len, const void *q,
+                      const void *k, const void *v, const void *a, const void *b,
+                      const float *A_log, const void *dt_bias, float scale, void *state, void *out,
+                      int32_t update_state, const int32_t *context_lengths,
+                      const int32_t *state_indices, void *workspace, int64_t workspace_bytes,
+                      bool step, hipStream_t stream)
+{
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_delta_dims &d = *dims;
+    if (d.batch < 0 || seq_len < 0)
+        return fail(SSU_EINVAL, "%s: batch %d and seq_len %d must be >= 0", fn, d.batch, seq_len);
+    if (d.num_q_heads <= 0 || d.num_v_heads <= 0 || d.pool_rows <= 0)
+        return fail(SSU_EINVAL, "%s: num_q_heads/num_v_heads/pool_rows must be > 0 (got %d/%d/%d)",
+                    fn, d.num_q_heads, d.num_v_heads, d.pool_rows);
+    if (d.num_v_heads % d.num_q_heads != 0)
+        return fail(SSU_EINVAL, "%s: num_v_heads %d is not a multiple of num_q_heads %d", fn,
+                    d.num_v_heads, d.num_q_heads);
+    if (d.head_dim != 32 && d.head_dim != 64 && d.head_dim != 128 && d.head_dim != 256)
+        return fail(SSU_ENOTSUP, "%s: head_dim %d not in {32, 64, 128, 256}", fn, d.head_dim);
+    if (!compute_dtype(d.state_dtype) || !compute_dtype(d.io_dtype) ||
+        !compute_dtype(d.gate_dtype) || !compute_dtype(d.bias_dtype))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype (state %d, io %d, gate %d, bias %d)", fn,
+                    d.state_dtype, d.io_dtype, d.gate_dtype, d.bias_dtype);
+    if (!state_indices && d.batch > d.pool_rows)
+        return fail(SSU_EINVAL, "%s: batch %d > pool_rows %d with no state_indices", fn, d.batch,
+                    d.pool_rows);
+    ssu::DeltaParams p = {};
+    const int64_t tile = (int64_t)d.num_v_heads * d.head_dim * d.head_dim;
+    p.row_stride = d.state_row_stride ? d.state_row_stride : tile;
+    if (p.row_stride < tile)
+        return fail(SSU_EINVAL, "%s: state_row_stride %lld < HV*D*D %lld", fn,
+                    (long long)d.state_row_stride, (long long)tile);
+    if (p.row_stride % (16 / (int64_t)dtype_bytes(d.state_dtype)) != 0)
+        return fail(SSU_EINVAL, "%s: state_row_stride %lld does not keep rows 16-byte aligned", fn,
+                    (long long)p.row_stride);
+    const int64_t qd = (int64_t)d.num_q_heads * d.head_dim, vd = (int64_t)d.num_v_heads * d.head_dim;
+    struct { const char *name; int64_t bs, ts, row; int64_t *obs, *ots; } const views[] = {
+        {"q", d.q_batch_stride, d.q_token_stride, qd, &p.q_bs, &p.q_ts},
+        {"k", d.k_batch_stride, d.k_token_stride, qd, &p.k_bs, &p.k_ts},
+        {"v", d.v_batch_stride, d.v_token_stride, vd, &p.v_bs, &p.v_ts},
+        {"a", d.a_batch_stride, d.a_token_stride, d.num_v_heads, &p.a_bs, &p.a_ts},
+        {"b", d.b_batch_stride, d.b_token_stride, d.num_v_heads, &p.b_bs, &p.b_ts},
+        {"out", d.out_batch_stride, d.out_token_stride, vd, &p.out_bs, &p.out_ts},
+    };
+    for (const auto &w : views) {
+        const ssu_status st = check_strides(fn, w.name, w.bs, step ? 0 : w.ts, w.row, d.batch,
+                                            seq_len, w.obs, w.ots);
+        if (st != SSU_OK)
+            return st;
+        if (*w.ots > (1 << 25))
+            return fail(SSU_ENOTSUP, "%s: %s has rows or a token stride above 2^25", fn, w.name);
+    }
+    if (seq_len > (1 << 30) || (int64_t)d.batch * d.num_v_heads > 0x7fffffff)
+        return fail(SSU_ENOTSUP, "%s: seq_len or batch * num_v_heads too large", fn);
+    if (d.batch == 0 || seq_len == 0)
+        return ok();
+    const size_t io = io_bytes(d.io_dtype), ga = io_bytes(d.gate_dtype);
+    if (step || !update_state)
+        SSU_REQUIRE_PTR(out, io, fn);
+    SSU_OPTIONAL_PTR(out, io, fn);
+    if (out)
+        SSU_REQUIRE_PTR(q, io, fn);
+    SSU_OPTIONAL_PTR(q, io, fn);
+    SSU_REQUIRE_PTR(k, io, fn);
+    SSU_REQUIRE_PTR(v, io, fn);
+    SSU_REQUIRE_PTR(a, ga, fn);
+    SSU_REQUIRE_PTR(b, ga, fn);
+    SSU_OPTIONAL_PTR(A_log, 4, fn);
+    SSU_OPTIONAL_PTR(dt_bias, io_bytes(d.bias_dtype), fn);
+    SSU_REQUIRE_PTR(state, 16, fn);
+    SSU_OPTIONAL_PTR(context_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(state_indices, 4, fn);
+    if (dt_bias && !A_log)
+        return fail(SSU_EINVAL, "%s: dt_bias without A_log", fn);
+    if (out && (out == q || out == k || out == a || out == b || (!step && out == v)))
+        return fail(SSU_EINVAL, "%s: out must not overlap an input", fn);
+    if (step && d.batch > 1 && out == v && p.out_bs != p.v_bs)
+        return fail(SSU_EINVAL, "%s: out in v's place has other strides", fn);
+    if (!step) {
+        const int64_t need = ssu_delta_workspace_bytes(dims, seq_len);
+        if (need > 0)
+            SSU_REQUIRE_PTR(workspace, 16, fn);
+        if (workspace_bytes < need)
+            return fail(SSU_EINVAL, "%s: workspace_bytes %lld < %lld required", fn,
+                        (long long)workspace_bytes, (long long)need);
+        p.workspace = workspace;
+    }
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.a = a;
+    p.b = b;
+    p.A_log = A_log;
+    p.dt_bias = dt_bias;
+    p.state = state;
+    p.out = out;
+    p.ctx = context_lengths;
+    p.idx = state_indices;
+    p.scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)d.head_dim);
+    p.batch = d.batch;
+    p.hq = d.num_q_heads;
+    p.hv = d.num_v_heads;
+    p.d = d.head_dim;
+    p.seq_len = seq_len;
+    p.state_dtype = d.state_dtype;
+    p.io_dtype = d.io_dtype;
+    p.gate_dtype = d.gate_dtype;
+    p.bias_dtype = d.bias_dtype;
+    p.use_l2 = d.use_qk_l2norm ? 1 : 0;
+    p.update = update_state ? 1 : 0;
+    return launch_status(ssu::launch_delta(p, stream), fn);
+}
+
+}  // namespace
+
+ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const void *k,
+                            const void *v, const void *a, const void *b, const float *A_log,
+                            const void *dt_bias, float scale, void *state, void *out,
+                            const int32_t *state_indices, hipStream_t stream)
+{
+    return delta_call("ssu_delta_decode", dims, 1, q, k, v, a, b, A_log, dt_bias, scale, state, out,
+                      1, nullptr, state_indices, nullptr, 0, true, stream);
+}
+
+ssu_status ssu_delta_prefill(const ssu_delta_dims *dims, int32_t seq_len, const void *q,
+                             const void *k, const void *v, const void *a, const void *b,
+                             const float *A_log, const void *dt_bias, float scale, void *state,
+                             void *out, int32_t update_state, const int32_t *context_lengths,
+                             const int32_t *state_indices, void *workspace,
+                             int64_t workspace_bytes, hipStream_t stream)
+{
+    return delta_call("ssu_delta_prefill", dims, seq_len, q, k, v, a, b, A_log, dt_bias, scale,
+                      state, out, update_state, context_lengths, state_indices, workspace,
+                      workspace_bytes, false, stream);
+}
+
+int64_t ssu_delta_workspace_bytes(const ssu_delta_dims *dims, int32_t seq_len)
+{
+    if (!dims || dims->batch < 0 || dims->num_q_heads <= 0 || dims->num_v_heads <= 0 ||
+        dims->num_v_heads % dims->num_q_heads != 0 ||
+        (dims->head_dim != 32 && dims->head_dim != 64 && dims->head_dim != 128 &&
+         dims->head_dim != 256) ||
+        !compute_dtype(dims->io_dtype) || (int64_t)dims->batch * dims->num_v_heads > 0x7fffffff ||
+        seq_len < 0 || seq_len > (1 << 30))
+        return -1;
+    return ssu::delta_workspace_bytes(dims->batch, dims->num_q_heads, dims->num_v_heads,
+                                      dims->head_dim, seq_len, dims->io_dtype);
+}
+
+ssu_status ssu_rms_norm(const ssu_norm_dims *dims, const void *x, const void *weight,
+                        void *residual, const void *z, void *out, float *scales, float eps,
+                        hipStream_t stream)
+{
+    const char *fn = "ssu_rms_norm";
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_norm_dims &d = *dims;
+    if (d.batch < 0 || d.num_tokens < 0)
+        return fail(SSU_EINVAL, "%s: batch %d and num_tokens %d must be >= 0", fn, d.batch,
+                    d.num_tokens);
+    if (d.columns <= 0 || d.group <= 0)
+        return fail(SSU_EINVAL, "%s: columns/group must be > 0 (got %d/%d)", fn, d.columns, d.group);
+    if (d.columns % d.group != 0)
+        return fail(SSU_EINVAL, "%s: columns %d is not a multiple of group %d", fn, d.columns, d.group);
+    if (d.weight_columns != d.columns && d.weight_columns != d.group)
+        return fail(SSU_EINVAL, "%s: weight_columns %d is neither columns %d nor group %d", fn,
+                    d.weight_columns, d.columns, d.group);
+    const bool coded = d.out_dtype == SSU_E4M3;
+    if (!compute_dtype(d.io_dtype) || !compute_dtype(d.weight_dtype) ||
+        !compute_dtype(d.residual_dtype) || (!compute_dtype(d.out_dtype) && !coded))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype (io %d, weight %d, residual %d, out %d)", fn,
+                    d.io_dtype, d.weight_dtype, d.residual_dtype, d.out_dtype);
+    if (!(eps >= 0.0f))
+        return fail(SSU_EINVAL, "%s: eps must be >= 0", fn);
+    if (coded) {
+        if (d.scale_block <= 0 || d.columns % d.scale_block != 0)
+            return fail(SSU_EINVAL, "%s: columns %d is not a multiple of scale_block %d", fn,
+                        d.columns, d.scale_block);
+        const int32_t lo = std::min(d.group, d.scale_block), hi = std::max(d.group, d.scale_block);
+        if (lo != hi && (hi % lo != 0 || lo < 8 || lo > 512 || (lo & (lo - 1)) != 0))
+            return fail(SSU_ENOTSUP,
+                        "%s: group %d and scale_block %d: the smaller has to be a power of two from 8 "
+                        "to 512 that divides the larger",
+                        fn, d.group, d.scale_block);
+    } else if (d.scale_block != 0 || scales) {
+        return fail(SSU_EINVAL, "%s: scales are for an output in SSU_E4M3", fn);
+    }
+    if (std::max(d.group, d.scale_block) > ssu::kNormSpan)
+        return fail(SSU_ENOTSUP, "%s: group or scale_block above %d columns", fn, ssu::kNormSpan);
+    ssu::NormParams p = {};
+    struct { const char *name; int64_t bs, ts; int64_t *obs, *ots; } const views[] = {
+        {"x", d.x_batch_stride, d.x_token_stride, &p.x_bs, &p.x_ts},
+        {"z", d.z_batch_stride, d.z_token_stride, &p.z_bs, &p.z_ts},
+        {"residual", d.residual_batch_stride, d.residual_token_stride, &p.r_bs, &p.r_ts},
+        {"out", d.out_batch_stride, d.out_token_stride, &p.out_bs, &p.out_ts},
+    };
+    for (const auto &w : views) {
+        const ssu_status st = check_strides(fn, w.name, w.bs, w.ts, d.columns, d.batch, d.num_tokens,
+                                            w.obs, w.ots);
+        if (st != SSU_OK)
+            return st;
+    }
+    if (d.batch == 0 || d.num_tokens == 0)
+        return ok();
+    const size_t io = io_bytes(d.io_dtype);
+    SSU_REQUIRE_PTR(x, io, fn);
+    SSU_REQUIRE_PTR(weight, io_bytes(d.weight_dtype), fn);
+    SSU_OPTIONAL_PTR(residual, io_bytes(d.residual_dtype), fn);
+    SSU_OPTIONAL_PTR(z, io, fn);
+    SSU_REQUIRE_PTR(out, coded ? 1 : io_bytes(d.out_dtype), fn);
+    if (coded)
+        SSU_REQUIRE_PTR(scales, 4, fn);
+    if (residual && (residual == x || residual == z || residual == out))
+        return fail(SSU_EINVAL, "%s: residual must not overlap another tensor", fn);
+    const bool many = (int64_t)d.batch * d.num_tokens > 1;
+    if ((out == x && (d.out_dtype != d.io_dtype || (many && (p.out_bs != p.x_bs || p.out_ts != p.x_ts)))) ||
+        (out == z && (d.out_dtype != d.io_dtype || (many && (p.out_bs != p.z_bs || p.out_ts != p.z_ts)))))
+        return fail(SSU_EINVAL, "%s: out in an input's place has another type or other strides", fn);
+    p.x = x;
+    p.weight = weight;
+    p.z = z;
+    p.residual = residual;
+    p.out = out;
+    p.scales = scales;
+    p.rows = (int64_t)d.batch * d.num_tokens;
+    p.tokens = d.num_tokens;
+    p.columns = d.columns;
+    p.group = d.group;
+    p.block = d.scale_block;
+    p.weight_columns = d.weight_columns;
+    p.io_dtype = d.io_dtype;
+    p.weight_dtype = d.weight_dtype;
+    p.residual_dtype = d.residual_dtype;
+    p.out_dtype = d.out_dtype;
+    p.unit_offset = d.unit_offset ? 1 : 0;
+    p.gate_first = d.gate_first ? 1 : 0;
+    p.eps = eps;
+    return launch_status(ssu::launch_norm(p, stream), fn);
+}
+
+int64_t ssu_logprobs_workspace_bytes(const ssu_logprob_dims *dims)
+{
+    if (!dims || dims->batch < 0 || dims->num_tokens < 0 || dims->vocab < 1 ||
+        dims->vocab > (1 << 24) || dims->top < 0 || dims->top > SSU_MAX_TOP || dims->top > dims->vocab ||
+        (int64_t)dims->batch * dims->num_tokens > (1 << 25))
+        return -1;
+    return ssu::logprobs_workspace_bytes((int64_t)dims->batch * dims->num_tokens, dims->vocab,
+                                         dims->top);
+}
+
+ssu_status ssu_token_logprobs(const ssu_logprob_dims *dims, const void *logits,
+                              const int32_t *tokens, const int32_t *context_lengths,
+                              const int32_t *state_indices, float *logprobs, float *entropy,
+                              int32_t *top_ids, float *top_logprobs, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream)
+{
+    const char *fn = "ssu_token_logprobs";
+    if (!dims)
+        return fail(SSU_EINVAL, "%s: dims is NULL", fn);
+    const ssu_logprob_dims &d = *dims;
+    if (d.reserved != 0)
+        return fail(SSU_EINVAL, "%s: dims.reserved must be 0", fn);
+    if (d.batch < 0 || d.num_tokens < 0)
+        return fail(SSU_EINVAL, "%s: batch %d and num_tokens %d must be >= 0", fn, d.batch,
+                    d.num_tokens);
+    if (d.vocab < 1 || d.vocab > (1 << 24))
+        return fail(SSU_EINVAL, "%s: vocab %d outside [1, 2^24]", fn, d.vocab);
+    if (!compute_dtype(d.logit_dtype))
+        return fail(SSU_ENOTSUP, "%s: unsupported dtype %d", fn, d.logit_dtype);
+    if ((top_ids == nullptr) != (top_logprobs == nullptr))
+        return fail(SSU_EINVAL, "%s: top_ids and top_logprobs go together", fn);
+    if (top_ids && (d.top < 1 || d.top > SSU_MAX_TOP || d.top > d.vocab))
+        return fail(SSU_EINVAL, "%s: top %d outside [1, min(%d, vocab)]", fn, d.top, SSU_MAX_TOP);
+    if ((int64_t)d.batch * d.num_tokens > (1 << 25))
+        return fail(SSU_ENOTSUP, "%s: batch * num_tokens above 2^25", fn);
+    ssu::LogprobParams p = {};
+    const ssu_status st = check_strides(fn, "logits", d.logit_batch_stride, d.logit_row_stride,
+                                        d.vocab, d.batch, d.num_tokens, &p.l_bs, &p.l_rs);
+    if (st != SSU_OK)
+        return st;
+    if (d.batch == 0 || d.num_tokens == 0)
+        return ok();
+    SSU_REQUIRE_PTR(logits, io_bytes(d.logit_dtype), fn);
+    SSU_REQUIRE_PTR(tokens, 4, fn);
+    SSU_OPTIONAL_PTR(context_lengths, 4, fn);
+    SSU_OPTIONAL_PTR(state_indices, 4, fn);
+    SSU_REQUIRE_PTR(logprobs, 4, fn);
+    SSU_OPTIONAL_PTR(entropy, 4, fn);
+    SSU_OPTIONAL_PTR(top_ids, 4, fn);
+    SSU_OPTIONAL_PTR(top_logprobs, 4, fn);
+    p.top = top_ids ? d.top : 0;
+    const int64_t need = ssu::logprobs_workspace_bytes((int64_t)d.batch * d.num_tokens, d.vocab, p.top);
+    if (need > 0)
+        SSU_REQUIRE_PTR(workspace, 16, fn);
+    if (workspace_bytes < need)
+        return fail(SSU_EINVAL, "%s: workspace_bytes %lld < %lld required", fn,
+                    (long long)workspace_bytes, (long long)need);
+    p.logits = logits;
+    p.tokens = tokens;
+    p.ctx = context_lengths;
+    p.idx = state_indices;
+    p.logprobs = logprobs;
+    p.entropy = entropy;
+    p.top_ids = top_ids;
+    p.top_logprobs = top_logprobs;
+    p.workspace = workspace;
+    p.batch = d.batch;
+    p.num_tokens = d.num_tokens;
+    p.vocab = d.vocab;
+    p.dtype = d.logit_dtype;
+    return launch_status(ssu::launch_logprobs(p, stream), fn);
+}
+
+namespace {
+
 ssu_status check_rows(const char *fn, int32_t rows, int64_t stride, int64_t row_bytes,
                       int32_t batch, int64_t *eff_stride)
 {

@@ -1,0 +1,11 @@
+// The gated delta rule token by token with bf16 q, k, v and out (see ssu_delta_rows.h).
+#include "ssu_delta_rows.h"
+
+namespace ssu {
+
+hipError_t launch_delta_rows_bf16(const DeltaParams &p, hipStream_t stream)
+{
+    return launch_delta_rows_io<bf16_t>(p, stream);
+}
+
+}  // namespace ssu

@@ -155,6 +155,55 @@ struct VerifyParams {
 };
 hipError_t launch_verify(const VerifyParams &p, hipStream_t stream);
 
+// The gated delta rule over seq_len tokens (1 for a single token).
+struct DeltaParams {
+    const void *q, *k, *v, *a, *b;
+    const float *A_log;   // null: a and b are the decay's logarithm and beta themselves
+    const void *dt_bias;
+    void *state, *out;  // out null: only the state is updated
+    const int32_t *ctx, *idx;
+    int64_t row_stride;
+    int64_t q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, a_bs, a_ts, b_bs, b_ts, out_bs, out_ts;
+    float scale;
+    int32_t batch, hq, hv, d, seq_len;
+    int32_t state_dtype, io_dtype, gate_dtype, bias_dtype;
+    int32_t use_l2, update;
+    void *workspace;  // delta_workspace_bytes(), 16-byte aligned
+};
+int64_t delta_workspace_bytes(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len,
+                              int32_t io_dtype);
+hipError_t launch_delta(const DeltaParams &p, hipStream_t stream);
+
+// RMS norm. Row strides in elements, all filled in.
+constexpr int kE4m3 = 4;
+constexpr int kNormSpan = 1 << 15;  // most columns that a workgroup holds
+struct NormParams {
+    const void *x, *weight, *z;
+    void *residual, *out;
+    float *scales;
+    int64_t x_bs, x_ts, z_bs, z_ts, r_bs, r_ts, out_bs, out_ts;
+    int64_t rows;  // batch * tokens
+    int32_t tokens, columns, group, block, weight_columns;
+    int32_t io_dtype, weight_dtype, residual_dtype, out_dtype;
+    int32_t unit_offset, gate_first;
+    float eps;
+};
+hipError_t launch_norm(const NormParams &p, hipStream_t stream);
+
+// Log probabilities of given tokens.
+struct LogprobParams {
+    const void *logits;
+    const int32_t *tokens, *ctx, *idx;
+    float *logprobs, *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+    void *workspace;
+    int64_t l_bs, l_rs;
+    int32_t batch, num_tokens, vocab, top, dtype;
+};
+int64_t logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top);
+hipError_t launch_logprobs(const LogprobParams &p, hipStream_t stream);
+
 // One set of row moves: for b < rows, dst row (dst_idx ? dst_idx[b] : b) gets
 // src row (src_idx ? src_idx[b] : b); a negative destination index skips the
 // row, a negative source index (or src == null) writes zeros; with skip_same,

@@ -1,0 +1,366 @@
+// Root-mean-square norm of rows, with the residual's addition before it, a gate
+// before or behind it, and an output in a float type or in e4m3 with scales:
+//   h = x + residual;  y = h rsqrt(mean h^2 + eps) w;  code = e4m3(y / s), s = max |y| / 448
+// Every tensor is read and written once: the span of columns that a sum or a
+// maximum runs over (the group, or the block of a scale where that is larger)
+// stays in registers between its passes. HBM bounds it.
+//
+// A span belongs to a team of threads, each with NV vectors of eight columns,
+// vector m + TEAM j for thread m, so that a load instruction takes consecutive
+// memory. Spans of up to 512 columns have teams of 1 to 64 lanes (several spans a
+// wave, sums by lane exchange); longer ones have a workgroup, whose waves meet
+// once in LDS for each sum. The smaller of group and block is a power of two of at most 64
+// vectors, which lie in consecutive lanes of one wave.
+#include "ssu_device.h"
+#include "ssu_dpp.h"
+#include "ssu_internal.h"
+
+namespace ssu {
+namespace {
+
+// Eight values of runtime type dt as their bits, converted later so that the
+// loads of all tensors are in flight together
+struct Raw8 {
+    u32x4 w[2];
+};
+
+template <bool VEC>
+__device__ __forceinline__ Raw8 ld_raw8(const void *p, int64_t i, int dt, int n)
+{
+    Raw8 r = {};
+    if constexpr (VEC) {
+        if (dt == kF32) {
+            const u32x4 *q = reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i);
+            r.w[0] = q[0];
+            r.w[1] = q[1];
+        } else {
+            r.w[0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+        }
+    } else if (dt == kF32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                r.w[e / 4][e % 4] = static_cast<const uint32_t *>(p)[i + e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                r.w[0][e / 2] |= (uint32_t)static_cast<const uint16_t *>(p)[i + e] << (16 * (e % 2));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void cvt_raw8(const Raw8 &r, int dt, float (&v)[8])
+{
+    if (dt == kF32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = __uint_as_float(r.w[e / 4][e % 4]);
+    } else if (dt == kBF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(r.w[0][e] << 16);
+            v[2 * e + 1] = __uint_as_float(r.w[0][e] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = f16_to_f32(r.w[0][e] & 0xffffu);
+            v[2 * e + 1] = f16_to_f32(r.w[0][e] >> 16);
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float (&v)[8], int n)
+{
+    if constexpr (VEC) {
+        if (dt == kF32) {
+            u32x4 *q = reinterpret_cast<u32x4 *>(static_cast<float *>(p) + i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                q[k] = u32x4{__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                             __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3])};
+        } else {
+            u32x4 w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = dt == kBF16 ? f32_to_bf16(v[2 * k]) | (f32_to_bf16(v[2 * k + 1]) << 16)
+                                   : f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
+            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                st_io(p, i + e, v[e], dt);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void st_e4m3(void *p, int64_t i, const float (&v)[8], float inv, int n)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k] * inv, v[4 * k + 1] * inv, 0, false);
+        w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k + 2] * inv, v[4 * k + 3] * inv, c, true);
+    }
+    uint8_t *q = static_cast<uint8_t *>(p) + i;
+    if constexpr (VEC) {
+        *reinterpret_cast<u32x2 *>(q) = u32x2{w[0], w[1]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                q[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+    }
+}
+
+// Sum, and maximum of bits, over aligned runs of `width` lanes (a power of two);
+// as unsigned numbers the bits of magnitudes order as they do, NaN above all.
+__device__ __forceinline__ float lanes_sum(float v, int width)
+{
+    if (width == 64)
+        return wave_sum(v);
+    for (int m = 1; m < width; m <<= 1)
+        v += __shfl_xor(v, m, 64);
+    return v;
+}
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int width)
+{
+    for (int m = 1; m < width; m <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)v, m, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// WG: the span belongs to the workgroup, otherwise to `team` lanes. vecs: vectors of a span.
+template <int NV, bool WG, bool VEC>
+__global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int team, int vecs,
+                                                    int sub, int64_t spans)
+{
+    __shared__ float part_f[16];
+    __shared__ uint32_t part_u[16];
+    constexpr bool EARLY = NV <= 2;  // z and the weights loaded with the rest (registers for four vectors do not reach)
+    const int nt = blockDim.x;
+    const int m = WG ? threadIdx.x : (threadIdx.x & (team - 1));
+    const int64_t s = WG ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * nt + threadIdx.x) / team;
+    // lanes past the last span keep their wave whole for the exchanges
+    const bool live = s < spans;
+    const int per_row = p.columns / span;
+    const int64_t row = live ? s / per_row : 0;
+    const int64_t b = row / p.tokens, t = row - b * p.tokens;
+    const int c0 = live ? (int)(s - row * per_row) * span : 0;
+
+    Raw8 rx[NV], rr[NV], rz[NV], rw[NV];
+    int cols[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = m + (WG ? nt : team) * j;
+        cols[j] = live && i < vecs ? min(8, span - 8 * i) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (cols[j] > 0) {
+            const int c = c0 + 8 * (m + (WG ? nt : team) * j);
+            rx[j] = ld_raw8<VEC>(p.x, b * p.x_bs + t * p.x_ts + c, p.io_dtype, cols[j]);
+            if (p.residual)
+                rr[j] = ld_raw8<VEC>(p.residual, b * p.r_bs + t * p.r_ts + c, p.residual_dtype, cols[j]);
+            if (EARLY && p.z)
+                rz[j] = ld_raw8<VEC>(p.z, b * p.z_bs + t * p.z_ts + c, p.io_dtype, cols[j]);
+            if (EARLY)
+                rw[j] = ld_raw8<VEC>(p.weight, p.weight_columns == p.columns ? c : c % p.group,
+                                     p.weight_dtype, cols[j]);
+        }
+    }
+
+    float h[NV][8];
+    float sq[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        sq[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[j][e] = 0.0f;
+        if (cols[j] > 0) {
+            const int c = c0 + 8 * (m + (WG ? nt : team) * j);
+            cvt_raw8(rx[j], p.io_dtype, h[j]);
+            if (p.residual) {
+                float r[8];
+                cvt_raw8(rr[j], p.residual_dtype, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[j][e] += r[e];
+                st_vec8<VEC>(p.residual, b * p.r_bs + t * p.r_ts + c, p.residual_dtype, h[j], cols[j]);
+            }
+            if (p.z && p.gate_first) {
+                float z[8];
+                if (!EARLY)
+                    rz[j] = ld_raw8<VEC>(p.z, b * p.z_bs + t * p.z_ts + c, p.io_dtype, cols[j]);
+                cvt_raw8(rz[j], p.io_dtype, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[j][e] *= silu_f32(z[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sq[j] += e < cols[j] ? h[j][e] * h[j][e] : 0.0f;
+        }
+    }
+
+    // sums of squares of the groups
+    if (p.group < span) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            sq[j] = lanes_sum(sq[j], sub);
+    } else {
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            a += sq[j];
+        if constexpr (WG) {
+            a = wave_sum(a);
+            if (nt > 64) {
+                if ((threadIdx.x & 63) == 0)
+                    part_f[threadIdx.x >> 6] = a;
+                __syncthreads();
+                a = 0.0f;
+                for (int w = 0; w < nt / 64; ++w)
+                    a += part_f[w];
+            }
+        } else {
+            a = lanes_sum(a, team);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            sq[j] = a;
+    }
+
+    uint32_t most[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        most[j] = 0;
+        const float inv = 1.0f / sqrtf(sq[j] / (float)p.group + p.eps);
+        if (cols[j] > 0) {
+            float w[8], z[8];
+            if (!EARLY) {
+                const int c = c0 + 8 * (m + (WG ? nt : team) * j);
+                rw[j] = ld_raw8<VEC>(p.weight, p.weight_columns == p.columns ? c : c % p.group,
+                                     p.weight_dtype, cols[j]);
+                if (p.z && !p.gate_first)
+                    rz[j] = ld_raw8<VEC>(p.z, b * p.z_bs + t * p.z_ts + c, p.io_dtype, cols[j]);
+            }
+            cvt_raw8(rw[j], p.weight_dtype, w);
+            if (p.z && !p.gate_first)
+                cvt_raw8(rz[j], p.io_dtype, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float y = h[j][e] * inv * (p.unit_offset ? 1.0f + w[e] : w[e]);
+                if (p.z && !p.gate_first)
+                    y *= silu_f32(z[e]);
+                h[j][e] = y;
+                const uint32_t mag = e < cols[j] ? __float_as_uint(y) & 0x7fffffffu : 0u;
+                most[j] = mag > most[j] ? mag : most[j];
+            }
+        }
+    }
+    if (p.out_dtype != kE4m3) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (cols[j] > 0)
+                st_vec8<VEC>(p.out, b * p.out_bs + t * p.out_ts + c0 + 8 * (m + (WG ? nt : team) * j),
+                             p.out_dtype, h[j], cols[j]);
+        return;
+    }
+
+    // maxima of the scales' blocks
+    if (p.block < span) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            most[j] = lanes_max(most[j], sub);
+    } else {
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            a = most[j] > a ? most[j] : a;
+        a = lanes_max(a, WG ? 64 : team);
+        if constexpr (WG) {
+            if (nt > 64) {
+                if ((threadIdx.x & 63) == 0)
+                    part_u[threadIdx.x >> 6] = a;
+                __syncthreads();
+                for (int w = 0; w < nt / 64; ++w)
+                    a = part_u[w] > a ? part_u[w] : a;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            most[j] = a;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (cols[j] > 0) {
+            const int i = m + (WG ? nt : team) * j, c = c0 + 8 * i;
+            const float a = __uint_as_float(most[j]) / 448.0f;
+            const float scale = a < 0x1p-126f ? 0x1p-126f : a;  // a NaN stays
+            st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], 1.0f / scale, cols[j]);
+            if ((8 * i) % p.block == 0)
+                p.scales[row * (p.columns / p.block) + c / p.block] = scale;
+        }
+}
+
+bool norm_aligned(const NormParams &p, int span)
+{
+    auto fine = [](const void *t, int64_t bs, int64_t ts, int dt) {
+        const int64_t e = dt == kF32 ? 4 : dt == kE4m3 ? 1 : 2, to = e == 1 ? 8 : 16;
+        return !t || ((uintptr_t)t | (uintptr_t)(bs * e) | (uintptr_t)(ts * e)) % to == 0;
+    };
+    return span % 8 == 0 && p.group % 8 == 0 && fine(p.x, p.x_bs, p.x_ts, p.io_dtype) &&
+           fine(p.z, p.z_bs, p.z_ts, p.io_dtype) &&
+           fine(p.residual, p.r_bs, p.r_ts, p.residual_dtype) &&
+           fine(p.out, p.out_bs, p.out_ts, p.out_dtype) && fine(p.weight, 0, 0, p.weight_dtype);
+}
+
+template <int NV, bool WG>
+hipError_t launch_norm_nv(const NormParams &p, int span, int team, int threads, hipStream_t stream)
+{
+    const int64_t spans = p.rows * (p.columns / span);
+    const int vecs = (span + 7) / 8;
+    const int sub = (p.out_dtype == kE4m3 ? min(p.group, p.block) : p.group) / 8;
+    const __int128 groups = WG ? spans : ((__int128)spans * team + threads - 1) / threads;
+    if (!launchable(groups, threads))
+        return hipErrorInvalidConfiguration;
+    if (norm_aligned(p, span))
+        norm_kernel<NV, WG, true><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, team, vecs,
+                                                                                  sub, spans);
+    else
+        norm_kernel<NV, WG, false><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, team, vecs,
+                                                                                   sub, spans);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormParams &p, hipStream_t stream)
+{
+    (void)hipGetLastError();  // report only this launch's status
+    const int span = p.out_dtype == kE4m3 && p.block > p.group ? p.block : p.group;
+    const int vecs = (span + 7) / 8;
+    if (vecs <= 64) {
+        int team = 1;
+        while (team < vecs)
+            team *= 2;
+        return launch_norm_nv<1, false>(p, span, team, 256, stream);
+    }
+    int threads = 64;
+    while (threads < 1024 && 2 * threads < vecs)
+        threads *= 2;
+    const int nv = (vecs + threads - 1) / threads;
+    if (nv <= 2)
+        return launch_norm_nv<2, true>(p, span, 0, threads, stream);
+    return launch_norm_nv<4, true>(p, span, 0, threads, stream);
+}
+
+}  // namespace ssu

@@ -17,7 +17,8 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssu.so")
 
 SSU_OK, SSU_EINVAL, SSU_ENOTSUP, SSU_EHIP, SSU_ENOMEM = 0, 1, 2, 3, 4
-SSU_F32, SSU_F16, SSU_BF16, SSU_U8 = 0, 1, 2, 3
+SSU_F32, SSU_F16, SSU_BF16, SSU_U8, SSU_E4M3 = 0, 1, 2, 3, 4
+SSU_MAX_TOP = 32
 _DT = {torch.float32: SSU_F32, torch.float16: SSU_F16, torch.bfloat16: SSU_BF16,
        torch.uint8: SSU_U8}
 
@@ -25,7 +26,9 @@ EXPORTS = ("ssu_decode", "ssu_prefill", "ssu_replay", "ssu_tree_verify",
            "ssu_tree_verify_noalloc", "ssu_replay_layers",
            "ssu_state_clear_layers", "ssu_state_gather", "ssu_state_scatter", "ssu_state_pack",
            "ssu_state_unpack", "ssu_conv_prefill", "ssu_conv_decode", "ssu_scan_prefill",
-           "ssu_scan_decode", "ssu_scan_workspace_bytes", "ssu_draft_verify", "ssu_verify_workspace_bytes", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
+           "ssu_scan_decode", "ssu_scan_workspace_bytes", "ssu_draft_verify", "ssu_verify_workspace_bytes", "ssu_delta_prefill",
+           "ssu_delta_decode", "ssu_delta_workspace_bytes", "ssu_rms_norm", "ssu_token_logprobs",
+           "ssu_logprobs_workspace_bytes", "ssu_gdn_decode", "ssu_gdn_workspace_bytes", "ssu_tree_workspace_bytes",
            "ssu_pool_bytes_per_slot", "ssu_pool_slab_bytes", "ssu_pool_spec", "ssu_pool_specs",
            "ssu_pool_name", "ssu_pool_owns_memory",
            "ssu_pool_alloc", "ssu_pool_free", "ssu_pool_info", "ssu_pool_state_ptr",
@@ -97,6 +100,36 @@ class ssu_verify_dims(ctypes.Structure):
                                                  "draft_batch_stride", "draft_row_stride")])
 
 
+class ssu_delta_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_q_heads", "num_v_heads", "head_dim",
+                                               "pool_rows", "use_qk_l2norm", "state_dtype",
+                                               "io_dtype", "gate_dtype", "bias_dtype")]
+                + [(n, ctypes.c_int64) for n in ("state_row_stride",
+                                                 "q_batch_stride", "q_token_stride",
+                                                 "k_batch_stride", "k_token_stride",
+                                                 "v_batch_stride", "v_token_stride",
+                                                 "a_batch_stride", "a_token_stride",
+                                                 "b_batch_stride", "b_token_stride",
+                                                 "out_batch_stride", "out_token_stride")])
+
+
+class ssu_norm_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_tokens", "columns", "group",
+                                               "scale_block", "weight_columns", "io_dtype",
+                                               "weight_dtype", "residual_dtype", "out_dtype",
+                                               "unit_offset", "gate_first")]
+                + [(n, ctypes.c_int64) for n in ("x_batch_stride", "x_token_stride",
+                                                 "z_batch_stride", "z_token_stride",
+                                                 "residual_batch_stride", "residual_token_stride",
+                                                 "out_batch_stride", "out_token_stride")])
+
+
+class ssu_logprob_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_tokens", "vocab", "top",
+                                               "logit_dtype", "reserved")]
+                + [(n, ctypes.c_int64) for n in ("logit_batch_stride", "logit_row_stride")])
+
+
 class ssu_state_spec(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("layer", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("shape", ctypes.c_int64 * 4)]
@@ -146,6 +179,14 @@ def load_library(path: Optional[str] = None):
                             _I32, _P, _P],
         "ssu_draft_verify": [ctypes.POINTER(ssu_verify_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P,
                              _P, _P, ctypes.c_int64, _P],
+        "ssu_delta_prefill": [ctypes.POINTER(ssu_delta_dims), _I32, _P, _P, _P, _P, _P, _P, _P,
+                              ctypes.c_float, _P, _P, _I32, _P, _P, _P, ctypes.c_int64, _P],
+        "ssu_delta_decode": [ctypes.POINTER(ssu_delta_dims), _P, _P, _P, _P, _P, _P, _P,
+                             ctypes.c_float, _P, _P, _P, _P],
+        "ssu_rms_norm": [ctypes.POINTER(ssu_norm_dims), _P, _P, _P, _P, _P, _P, ctypes.c_float,
+                         _P],
+        "ssu_token_logprobs": [ctypes.POINTER(ssu_logprob_dims), _P, _P, _P, _P, _P, _P, _P, _P,
+                               _P, ctypes.c_int64, _P],
         "ssu_state_unpack": [_P, _I32, ctypes.c_int64, ctypes.c_int64, _P, _I32, _P, _I32, _P, _P],
         "ssu_pool_bytes_per_slot": [S, _I32, ctypes.POINTER(ctypes.c_size_t)],
         "ssu_pool_slab_bytes": [S, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)],
@@ -180,6 +221,10 @@ def load_library(path: Optional[str] = None):
     lib.ssu_scan_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_verify_workspace_bytes.argtypes = [ctypes.POINTER(ssu_verify_dims)]
     lib.ssu_verify_workspace_bytes.restype = ctypes.c_int64
+    lib.ssu_delta_workspace_bytes.argtypes = [ctypes.POINTER(ssu_delta_dims), _I32]
+    lib.ssu_delta_workspace_bytes.restype = ctypes.c_int64
+    lib.ssu_logprobs_workspace_bytes.argtypes = [ctypes.POINTER(ssu_logprob_dims)]
+    lib.ssu_logprobs_workspace_bytes.restype = ctypes.c_int64
     lib.ssu_last_error.argtypes = []
     lib.ssu_last_error.restype = ctypes.c_char_p
     lib.ssu_version.argtypes = []
@@ -1029,6 +1074,211 @@ def ssu_draft_verify(tokens, target_probs, uniforms, accepted_lengths, next_toke
     _launch(dev, stream, lib.ssu_draft_verify, d, tp, target_probs.data_ptr(), qp, up, pp, cp, ip,
             ap, kp, np_, wp, wn)
     return accepted_lengths, next_tokens
+
+
+# ---------------------------------------------------------------------------
+# Gated delta rule, RMS norm, log probabilities
+# ---------------------------------------------------------------------------
+def _delta_call(q, k, v, a, b, state, out, A_log, dt_bias, scale, use_qk_l2norm, update_state,
+                context_lengths, state_indices, workspace, stream, step):
+    lib = _LIB or load_library()
+    dev = _first(v, "v", 3 if step else 4, "[batch, HV, D]" if step else "[batch, seq_len, HV, D]")
+    shape, dtype = v.shape, v.dtype
+    batch, hv, d = shape[0], shape[-2], shape[-1]
+    kshape, gdt, sdt = k.shape, a.dtype, state.dtype
+    if len(kshape) != len(shape) or kshape[:-2] != shape[:-2] or kshape[-1] != d:
+        _fail("k must be [batch, Hq, D]" if step else "k must be [batch, seq_len, Hq, D]")
+    hq = kshape[-2]
+    if gdt not in _FLOAT or sdt not in _FLOAT:
+        _fail("a, b and state are fp32, fp16 or bf16")
+    ks = _view(k, "k", dtype, kshape, dev, step)
+    vs = _view(v, "v", dtype, shape, dev, step)
+    as_ = _view(a, "a", gdt, shape[:-1], dev, step)
+    bs = _view(b, "b", gdt, shape[:-1], dev, step)
+    qs = os_ = _DENSE
+    qp = op = 0
+    if q is not None:
+        qs, qp = _view(q, "q", dtype, kshape, dev, step), q.data_ptr()
+    if out is not None:
+        if q is None:
+            _fail("q is required")
+        os_, op = _view(out, "out", dtype, shape, dev, step), out.data_ptr()
+    ap = _vector(A_log, "A_log", torch.float32, (hv,), dev)
+    hdt = torch.float32
+    if dt_bias is not None:
+        hdt = dt_bias.dtype
+        if hdt not in _FLOAT:
+            _fail("dt_bias is fp32, fp16 or bf16")
+    hp = _vector(dt_bias, "dt_bias", hdt, (hv,), dev)
+    sshape, st = state.shape, state.stride()
+    if state.device.index != dev or len(sshape) != 4 or tuple(sshape[1:]) != (hv, d, d):
+        _fail(f"state must be [rows, {hv}, {d}, {d}] on cuda:{dev}, got {tuple(sshape)} on "
+              f"{state.device}")
+    rows = sshape[0]
+    if st[3] != 1 or st[2] != d or (st[1] != d * d and hv > 1):
+        _fail("state rows must be dense ([HV, D, D] contiguous)")
+    if rows > 1 and st[0] < hv * d * d:
+        _fail("state row stride too small")
+    if rows > 1 << 30:
+        _fail("state has more than 2^30 rows")
+    ip = _vector(state_indices, "state_indices", torch.int32, (batch,), dev)
+    dims = ssu_delta_dims(batch, hq, hv, d, rows, 1 if use_qk_l2norm else 0, _DT[sdt], _DT[dtype],
+                          _DT[gdt], _DT[hdt], st[0] if rows > 1 else 0, *qs, *ks, *vs, *as_, *bs,
+                          *os_)
+    sc = 0.0 if scale is None else float(scale)
+    if step:
+        _launch(dev, stream, lib.ssu_delta_decode, dims, qp, k.data_ptr(), v.data_ptr(),
+                a.data_ptr(), b.data_ptr(), ap, hp, sc, state.data_ptr(), op, ip)
+        return out
+    cp = _vector(context_lengths, "context_lengths", torch.int32, (batch,), dev)
+    workspace, wp, wn = _scratch(workspace, lib.ssu_delta_workspace_bytes(dims, shape[1]), v.device,
+                                 stream)
+    _launch(dev, stream, lib.ssu_delta_prefill, dims, shape[1], qp, k.data_ptr(), v.data_ptr(),
+            a.data_ptr(), b.data_ptr(), ap, hp, sc, state.data_ptr(), op, 1 if update_state else 0,
+            cp, ip, wp, wn)
+    return out
+
+
+def ssu_delta_prefill(q, k, v, a, b, state, out, *, A_log=None, dt_bias=None, scale=None,
+                      use_qk_l2norm=True, context_lengths=None, state_indices=None,
+                      update_state=True, workspace=None, stream=None):
+    """Gated delta rule of seq_len tokens.
+
+    q, k [batch, seq_len, Hq, D]; v, out [batch, seq_len, HV, D], HV a multiple of Hq; a, b
+    [batch, seq_len, HV] (slices of wider tensors are fine: a token's entries dense, the other
+    two axes in either order); state [rows, HV, D, D], updated in place unless update_state is
+    False; A_log [HV] fp32 and dt_bias [HV] make the decays and betas of a and b as
+    ssu_gdn_decode does, without A_log they are the decays' logarithms and the betas;
+    context_lengths, state_indices [batch] int32. out (and q) may be None when only the state
+    is wanted (commit of a window: context_lengths = accepted lengths). workspace: a uint8 GPU
+    tensor of at least delta_workspace_bytes(...) bytes for this call's sizes (allocated here
+    when None).
+    """
+    return _delta_call(q, k, v, a, b, state, out, A_log, dt_bias, scale, use_qk_l2norm,
+                       update_state, context_lengths, state_indices, workspace, stream, False)
+
+
+def ssu_delta_decode(q, k, v, a, b, state, out, *, A_log=None, dt_bias=None, scale=None,
+                     use_qk_l2norm=True, state_indices=None, stream=None):
+    """One token of the gated delta rule: q, k [batch, Hq, D]; v, out [batch, HV, D]; a, b
+    [batch, HV]; the rest as ssu_delta_prefill. out may be v."""
+    return _delta_call(q, k, v, a, b, state, out, A_log, dt_bias, scale, use_qk_l2norm, True, None,
+                       state_indices, None, stream, True)
+
+
+def delta_workspace_bytes(batch, seq_len, num_q_heads, num_v_heads, head_dim,
+                          dtype=torch.bfloat16):
+    """Bytes of the workspace ssu_delta_prefill needs for exactly these sizes and type of q, k
+    and v (no GPU needed; -1 for what the call refuses)."""
+    d = ssu_delta_dims(batch, num_q_heads, num_v_heads, head_dim, 1, 1, 0, _DT[dtype])
+    return int(load_library().ssu_delta_workspace_bytes(d, seq_len))
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def ssu_rms_norm(x, weight, out, *, residual=None, z=None, scales=None, group_size=None, eps=1e-6,
+                 unit_offset=False, gate_first=False, stream=None):
+    """RMS norm of the rows of x, over groups of group_size columns (None: whole rows).
+
+    x, z, residual, out [rows, n] or [batch, tokens, n] (slices of wider tensors are fine);
+    weight [n] or [group_size]; unit_offset: the factor is 1 + weight. residual is added to x
+    first and receives the sum; z gates by silu(z), behind the norm or, with gate_first, before
+    it. out in float8_e4m3fn takes scales fp32 [.., m]: each of m blocks of a row is divided by
+    its scale, its largest magnitude / 448. out may be x or z.
+    """
+    lib = _LIB or load_library()
+    two = x.dim() == 2
+    dev = _first(x, "x", 2 if two else 3, "[rows, n] or [batch, tokens, n]")
+    shape, dtype = x.shape, x.dtype
+    n = shape[-1]
+    xs = _DENSE if x.is_contiguous() else _outer(x.stride(), shape, "x", two)
+    zs = rs = _DENSE
+    zp = rp = 0
+    if z is not None:
+        zs, zp = _view(z, "z", dtype, shape, dev, two), z.data_ptr()
+    rdt = dtype
+    if residual is not None:
+        rdt = residual.dtype
+        if rdt not in _FLOAT:
+            _fail("residual is fp32, fp16 or bf16")
+        rs, rp = _view(residual, "residual", rdt, shape, dev, two), residual.data_ptr()
+    odt, wdt = out.dtype, weight.dtype
+    if odt not in _FLOAT and odt is not _E4M3:
+        _fail("out is fp32, fp16, bf16 or float8_e4m3fn")
+    os_ = _view(out, "out", odt, shape, dev, two)
+    group = n if group_size is None else int(group_size)
+    if group <= 0 or n == 0 or n % group:
+        _fail(f"group_size {group} does not divide {n} columns")
+    if wdt not in _FLOAT or weight.dim() != 1 or weight.shape[0] not in (n, group):
+        _fail(f"weight must be [{n}] or [{group}], fp32, fp16 or bf16")
+    wp = _vector(weight, "weight", wdt, weight.shape, dev)
+    block = sp = 0
+    if odt is _E4M3:
+        if scales is None:
+            _fail("an output in float8_e4m3fn needs scales")
+        m = scales.shape[-1] if scales.dim() else 0
+        if m == 0 or n % m:
+            _fail(f"scales must be [.., m] with m a divisor of {n}")
+        sp = _vector(scales, "scales", torch.float32, shape[:-1] + (m,), dev)
+        block = n // m
+    elif scales is not None:
+        _fail("scales are for an output in float8_e4m3fn")
+    # the rows of a two-dimensional x are a batch of single tokens
+    d = ssu_norm_dims(shape[0], 1 if two else shape[1], n, group, block, weight.shape[0],
+                      _DT[dtype], _DT[wdt], _DT[rdt], SSU_E4M3 if block else _DT[odt],
+                      1 if unit_offset else 0, 1 if gate_first else 0, *xs, *zs, *rs, *os_)
+    _launch(dev, stream, lib.ssu_rms_norm, d, x.data_ptr(), wp, rp, zp, out.data_ptr(), sp,
+            float(eps))
+    return out
+
+
+def logprobs_workspace_bytes(batch, num_tokens, vocab, top=0):
+    """Bytes of the workspace ssu_token_logprobs needs for exactly these sizes (no GPU needed;
+    -1 for what the call refuses)."""
+    d = ssu_logprob_dims(batch, num_tokens, vocab, top)
+    return int(load_library().ssu_logprobs_workspace_bytes(d))
+
+
+def ssu_token_logprobs(logits, tokens, logprobs, *, entropy=None, top_ids=None, top_logprobs=None,
+                       context_lengths=None, state_indices=None, workspace=None, stream=None):
+    """Log probabilities of given tokens, the entropy and the most probable alternatives.
+
+    logits [rows, vocab] or [batch, num_tokens, vocab] (slices of wider tensors are fine: the
+    vocabulary dense); tokens int32, logprobs and entropy fp32 [rows] or [batch, num_tokens];
+    top_ids int32 and top_logprobs fp32 [.., k], k up to 32, in descending order, equal logits
+    by index. context_lengths, state_indices [batch] int32: rows past a length, and of negative
+    indices, are not read. workspace: a uint8 GPU tensor of at least
+    logprobs_workspace_bytes(...) bytes for this call's sizes (allocated here when None).
+    """
+    lib = _LIB or load_library()
+    two = logits.dim() == 2
+    dev = _first(logits, "logits", 2 if two else 3, "[rows, vocab] or [batch, num_tokens, vocab]")
+    shape, dtype = logits.shape, logits.dtype
+    vocab, lead = shape[-1], shape[:-1]
+    if vocab < 1 or vocab > 1 << 24:
+        _fail(f"vocab {vocab} outside [1, 2^24]")
+    ls = _DENSE if logits.is_contiguous() else _outer(logits.stride(), shape, "logits", two)
+    f32, i32 = torch.float32, torch.int32
+    tp = _vector(tokens, "tokens", i32, lead, dev)
+    pp = _vector(logprobs, "logprobs", f32, lead, dev)
+    ep = _vector(entropy, "entropy", f32, lead, dev)
+    top = tip = tlp = 0
+    if (top_ids is None) != (top_logprobs is None):
+        _fail("top_ids and top_logprobs go together")
+    if top_ids is not None:
+        top = top_ids.shape[-1] if top_ids.dim() else 0
+        if not 1 <= top <= min(SSU_MAX_TOP, vocab):
+            _fail(f"top_ids must be [.., k] with k in [1, {min(SSU_MAX_TOP, vocab)}]")
+        tip = _vector(top_ids, "top_ids", i32, lead + (top,), dev)
+        tlp = _vector(top_logprobs, "top_logprobs", f32, lead + (top,), dev)
+    cp = _vector(context_lengths, "context_lengths", i32, shape[:1], dev)
+    ip = _vector(state_indices, "state_indices", i32, shape[:1], dev)
+    d = ssu_logprob_dims(shape[0], 1 if two else shape[1], vocab, top, _DT[dtype], 0, *ls)
+    workspace, wp, wn = _scratch(workspace, lib.ssu_logprobs_workspace_bytes(d), logits.device, stream)
+    _launch(dev, stream, lib.ssu_token_logprobs, d, logits.data_ptr(), tp, cp, ip, pp, ep, tip, tlp,
+            wp, wn)
+    return logprobs
 
 
 # ---------------------------------------------------------------------------
