@@ -24,7 +24,8 @@ SOURCES = ["ssu_api.cpp", "ssu_decode.hip", "ssu_decode_f32.hip", "ssu_decode_f1
            "ssu_tree_f16.hip", "ssu_tree_bf16.hip", "ssu_gdn.hip", "ssu_conv.hip", "ssu_scan.hip",
            "ssu_scan_rows.hip", "ssu_scan_prompt_f32.hip", "ssu_scan_prompt_f16.hip",
            "ssu_scan_prompt_bf16.hip", "ssu_verify.hip", "ssu_delta.hip", "ssu_delta_rows_f32.hip",
-           "ssu_delta_rows_f16.hip", "ssu_delta_rows_bf16.hip", "ssu_norm.hip", "ssu_logprobs.hip",
+           "ssu_delta_rows_f16.hip", "ssu_delta_rows_bf16.hip",
+           "ssu_delta_chunks_f16.hip", "ssu_delta_chunks_bf16.hip", "ssu_norm.hip", "ssu_logprobs.hip",
            "ssu_pool_kernels.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,4 +1,9 @@
-// The gated delta rule on given q, k and v over a paged state pool.
+// The gated delta rule on given q, k and v over a paged state pool:
+//   S <- alpha S;  u = beta (v - S k);  S <- S + u k^T;  o = scale S q
+//
+// Two evaluations, by the sizes (delta_plan): token by token (ssu_delta_rows.h; single
+// tokens, windows, what the matrix cores do not take) and in chunks of 64
+// tokens on the matrix cores (ssu_delta_chunks.h; prompts).
 #include "ssu_delta_impl.h"
 
 namespace ssu {
@@ -6,12 +11,47 @@ namespace ssu {
 hipError_t launch_delta_rows_f32(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_rows_f16(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_rows_bf16(const DeltaParams &p, hipStream_t stream);
+hipError_t launch_delta_chunks_f16(const DeltaParams &p, const DeltaPlan &plan, hipStream_t stream);
+hipError_t launch_delta_chunks_bf16(const DeltaParams &p, const DeltaPlan &plan, hipStream_t stream);
 
-int64_t delta_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int32_t) { return 0; }
+namespace {
+
+constexpr int kDeltaLeast = 32;                      // tokens from which chunks are taken
+constexpr int64_t kDeltaSegment = (int64_t)96 << 20;  // bytes handed over at a time
+
+}  // namespace
+
+DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len, int32_t io_dtype)
+{
+    DeltaPlan q = {};
+    if (batch <= 0 || batch > 65535 || seq_len < kDeltaLeast || io_dtype == kF32 || (d != 64 && d != 128))
+        return q;
+    q.chunks = (int32_t)((seq_len + 63) / 64);
+    const int64_t kq = batch * hq * 256 * d, head = batch * hv * (22 * 1024);
+    int64_t segment = kDeltaSegment / (kq + head);
+    segment = segment < 1 ? 1 : segment > q.chunks ? q.chunks : segment;
+    q.segment = (int32_t)segment;
+    q.nv = 1;
+    q.kq_bytes = kq * segment;
+    q.head_bytes = head * segment;
+    q.carry_bytes = segment < q.chunks ? 4 * batch * hv * d * d : 0;
+    return q;
+}
+
+int64_t delta_workspace_bytes(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len,
+                              int32_t io_dtype)
+{
+    const DeltaPlan q = delta_plan(batch, hq, hv, d, seq_len, io_dtype);
+    return q.chunks ? q.kq_bytes + q.head_bytes + q.carry_bytes : 0;
+}
 
 hipError_t launch_delta(const DeltaParams &p, hipStream_t stream)
 {
     (void)hipGetLastError();  // report only this launch's status
+    const DeltaPlan q = delta_plan(p.batch, p.hq, p.hv, p.d, p.seq_len, p.io_dtype);
+    if (q.chunks && p.workspace && delta_rows_aligned(p, 16, true))
+        return p.io_dtype == kF16 ? launch_delta_chunks_f16(p, q, stream)
+                                  : launch_delta_chunks_bf16(p, q, stream);
     switch (p.io_dtype) {
     case kF32: return launch_delta_rows_f32(p, stream);
     case kF16: return launch_delta_rows_f16(p, stream);

@@ -173,6 +173,14 @@ struct DeltaParams {
 int64_t delta_workspace_bytes(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len,
                               int32_t io_dtype);
 hipError_t launch_delta(const DeltaParams &p, hipStream_t stream);
+// The evaluation in chunks: their number, those of one segment (prep and sweep follow each
+// other by segments, so that what is handed over stays in the last-level cache), value
+// tiles of a wave, bytes of the workspace's parts. chunks == 0: token by token.
+struct DeltaPlan {
+    int32_t chunks, segment, nv;
+    int64_t kq_bytes, head_bytes, carry_bytes;
+};
+DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len, int32_t io_dtype);
 
 // RMS norm. Row strides in elements, all filled in.
 constexpr int kE4m3 = 4;
