@@ -49,17 +49,27 @@ namespace ssu {
 namespace {
 
 constexpr int kDcC = 64;          // tokens of a chunk
-constexpr int kDcTile = 1024;     // bytes of a 16 x 16 tile as [hi | lo]
-// Block of a value head and chunk: 4 inverses, 6 tiles of L, scalars, 10 tiles of P
-constexpr int kDcL = 4 * kDcTile, kDcScalars = 10 * kDcTile, kDcP = 12 * kDcTile;
-constexpr int kDcHead = 22 * kDcTile;
+constexpr int kDcTile = 1024;     // bytes of an inverse as [hi | lo], or of a plane (hi or lo) of two tiles
+// Block of a value head and chunk: 4 inverses, 4 pairs of tiles of L (the second of rows
+// 1 and 3's last is zero), scalars, 6 pairs of P (what lies above the diagonal is zero)
+constexpr int kDcL = 4 * kDcTile, kDcScalars = 12 * kDcTile, kDcP = 14 * kDcTile;
+constexpr int kDcHead = kDeltaHeadBytes;
+static_assert(kDcHead == 26 * kDcTile, "tiles of a head");
+__device__ __forceinline__ constexpr int dc_l_pair(int i, int p) { return kDcL + (i - 1 + p) * 2 * kDcTile; }
+__device__ __forceinline__ constexpr int dc_p_pair(int i, int p)
+{
+    return kDcP + (i < 2 ? i : 2 * i - 2 + p) * 2 * kDcTile;
+}
 // Scalars: arrays of 64 floats
 enum : int { kScBeta, kScGk, kScWk, kScAlpha, kScKs, kScGo, kScQo, kScMisc };
 
 typedef _Float16 dc_f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 dc_f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 dc_f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 dc_bf16x2 __attribute__((ext_vector_type(2)));
 typedef float dc_f32x2 __attribute__((ext_vector_type(2)));
 typedef float dc_f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t dc_u16x2 __attribute__((ext_vector_type(2)));
 typedef short dc_i16x4 __attribute__((ext_vector_type(4)));
 
 struct DeltaWork {
@@ -76,17 +86,38 @@ __device__ __forceinline__ dc_f32x4 dc_mfma(const u32x4 &a, const u32x4 &b, cons
                                                   __builtin_bit_cast(dc_f16x8, b), c, 0, 0, 0);
 }
 
-// Four fp32 values as fp16 pairs: hi (2 words) and what is left (2 words).
+__device__ __forceinline__ dc_f32x4 dc_mfma16(const u32x2 &a, const u32x2 &b, const dc_f32x4 &c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(dc_f16x4, a),
+                                                 __builtin_bit_cast(dc_f16x4, b), c, 0, 0, 0);
+}
+
+// Four fp32 values as fp16 pairs: hi (2 words) and what is left (2 words). The factor -1
+// comes from a register, so that the difference is one v_fma_mix_f32, which
+// takes the fp16 as it is.
 __device__ __forceinline__ void dc_split(const dc_f32x4 &f, u32x2 &hi, u32x2 &lo)
 {
+    float minus;
+    asm("v_mov_b32 %0, -1.0" : "=v"(minus));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const float a = f[2 * e], b = f[2 * e + 1];
         const dc_f16x2 h = __builtin_convertvector((dc_f32x2){a, b}, dc_f16x2);
-        const dc_f16x2 l = __builtin_convertvector((dc_f32x2){a - (float)h[0], b - (float)h[1]}, dc_f16x2);
+        const dc_f16x2 l = __builtin_convertvector(
+            (dc_f32x2){fmaf((float)h[0], minus, a), fmaf((float)h[1], minus, b)}, dc_f16x2);
         hi[e] = __builtin_bit_cast(uint32_t, h);
         lo[e] = __builtin_bit_cast(uint32_t, l);
     }
+}
+
+// Two values rounded to nearest even in a 16-bit type
+template <typename IO>
+__device__ __forceinline__ uint32_t dc_pack(float a, float b)
+{
+    if constexpr (__is_same(IO, _Float16))
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((dc_f32x2){a, b}, dc_f16x2));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((dc_f32x2){a, b}, dc_bf16x2));
 }
 
 // Byte offset in a K or Q image of the 8 bytes with keys 16 n + 4 g .. + 3 of token `tok`
@@ -344,9 +375,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
                         v[r] = f * ((kind ? qk[jt][r] : kk[jt][r]) * tail[r]);
                     u32x2 hi, lo;
                     dc_split(v, hi, lo);
-                    const int tile = kind ? i * (i + 1) / 2 + jt : i * (i - 1) / 2 + jt;
-                    *reinterpret_cast<u32x4 *>(to + (kind ? kDcP : kDcL) + tile * kDcTile + lane * 16) =
-                        u32x4{hi[0], hi[1], lo[0], lo[1]};
+                    unsigned char *at8 = to + (kind ? dc_p_pair(i, jt >> 1) : dc_l_pair(i, jt >> 1)) + lane * 16 + 8 * (jt & 1);
+                    *reinterpret_cast<u32x2 *>(at8) = hi;
+                    *reinterpret_cast<u32x2 *>(at8 + kDcTile) = lo;
                 }
                 // diagonal tile: decays behind s through t by adding from t downwards
                 float sum = 0.0f;
@@ -391,8 +422,19 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
                 }
                 u32x2 hi, lo;
                 dc_split(v, hi, lo);
-                *reinterpret_cast<u32x4 *>(to + (kind ? kDcP + (i * (i + 1) / 2 + i) * kDcTile : i * kDcTile) + lane * 16) =
-                    u32x4{hi[0], hi[1], lo[0], lo[1]};
+                if (kind == 0) {
+                    *reinterpret_cast<u32x4 *>(to + i * kDcTile + lane * 16) = u32x4{hi[0], hi[1], lo[0], lo[1]};
+                    if (i & 1) {  // the second tile of this row's last pair
+                        unsigned char *at8 = to + dc_l_pair(i, i >> 1) + lane * 16 + 8;
+                        *reinterpret_cast<u32x2 *>(at8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile) = u32x2{0, 0};
+                    }
+                } else {
+                    unsigned char *at8 = to + dc_p_pair(i, i >> 1) + lane * 16 + 8 * (i & 1);
+                    *reinterpret_cast<u32x2 *>(at8) = hi;
+                    *reinterpret_cast<u32x2 *>(at8 + kDcTile) = lo;
+                    if (!(i & 1))
+                        *reinterpret_cast<u32x2 *>(at8 + 8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile + 8) = u32x2{0, 0};
+                }
             }
         }
         __syncthreads();
@@ -402,6 +444,18 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
 // ---------------------------------------------------------------------------
 
 typedef __attribute__((address_space(3))) dc_i16x4 *dc_lds_v4;
+
+// 16 bytes a lane from global memory to LDS: `to` is the wave's, lane i's land at to + 16 i.
+// In assembly, as with the builtin the compiler waits for these loads in front of the
+// next LDS read of any address; they are waited for once a chunk, by hand. No register
+// receives anything. The addresses of lanes are read at issue.
+__device__ __forceinline__ void dc_to_lds(const unsigned char *from, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(to), "v"(from)
+                 : "memory", "m0");
+}
 
 // K^T operand: rows keys 16 n + c, contraction the tokens 16 i + 4 g + r of tiles i = 2 s, 2 s + 1
 template <int D>
@@ -415,22 +469,46 @@ __device__ __forceinline__ u32x4 dc_ld_kt(unsigned char *image, int n, int s, in
     return u32x4{a2[0], a2[1], b2[0], b2[1]};
 }
 
+// Values of token rows in LDS: four tokens 4 g + r of tile i, column c of the wave's (as bits)
+template <int PITCH>
+__device__ __forceinline__ u32x2 dc_ld_v(unsigned char *rows, int i, int lane)
+{
+    const int g = lane >> 4, x = lane & 15;
+    unsigned char *p = rows + (16 * i + 4 * g + (x >> 2)) * PITCH + (x & 3) * 8;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((dc_lds_v4)p));
+}
+
+// The largest magnitude of tile maxima m (bits of 16-bit values, two tiles a word) over
+// the four lane groups
+__device__ __forceinline__ uint32_t dc_max2_groups(uint32_t m)
+{
+    auto larger = [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(dc_u16x2, a),
+                                                                      __builtin_bit_cast(dc_u16x2, b)));
+    };
+    const auto a = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = larger(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    return larger(b[0], b[1]);
+}
+
 // One wave: value columns [16 NV (..)] of value head h, batch entry b.
-template <typename IO, int D, int NV>
-__global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, DeltaWork w, int swizzle)
+template <typename IO, int D, int NV, int W, bool OUT>
+__global__ __launch_bounds__(64 * W, W / 4) void delta_sweep_kernel(DeltaParams p, DeltaWork w, int swizzle)
 {
     constexpr int KS = D / 32, KT = D / 16, C = kDcC;
-    constexpr int TILES = D / (64 * NV);              // workgroups a head
-    constexpr int KQ = 4 * C * D, BUF = KQ + kDcHead;  // bytes of a chunk in LDS
-    constexpr int LOADS = (BUF / 16 + 255) / 256;
+    constexpr int TILES = D / (16 * W * NV);           // workgroups a head
+    constexpr int KQ = 4 * C * D, VP = 32 * W * NV;    // bytes of K and Q, of a token's values
+    constexpr int BUF = KQ + kDcHead + C * VP;         // of a chunk in LDS
+    static_assert(TILES * 16 * W * NV == D, "value columns of a head");
     __shared__ __attribute__((aligned(16))) unsigned char lds[2 * BUF];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     // workgroups are dealt out over eight XCDs: those of one q head go to the same one
     const uint32_t id = swizzle ? (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3) : blockIdx.x;
     const int64_t bh = id / TILES;
     const int b = (int)(bh / p.hv), h = (int)(bh - (int64_t)b * p.hv);
-    const int v0 = ((int)(id - bh * TILES) * 4 + wave) * 16 * NV;
+    const int wg_v0 = (int)(id - bh * TILES) * (16 * W * NV), v0 = wg_v0 + wave * 16 * NV;
     const int j = h / (p.hv / p.hq);
     const int pool = p.idx ? p.idx[b] : b;
     const int len = pool < 0 ? 0 : (p.ctx ? clamp_len(p.ctx[b], p.seq_len) : p.seq_len);
@@ -438,65 +516,81 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
     if (len <= 0 || (mine <= 0 && !(w.last && p.update && !w.first)))
         return;
     const int chunks = mine > 0 ? (mine + C - 1) / C : 0;
-    const bool outs = p.out != nullptr;
+
+    // What prep left of a chunk, and its values, go to LDS past the registers, 1 KiB an
+    // instruction, while the chunk before it is worked on
+    const unsigned char *kq = w.kq + ((int64_t)b * w.chunks * p.hq + j) * KQ + lane * 16;
+    const unsigned char *hd = w.head + ((int64_t)b * w.chunks * p.hv + h) * kDcHead + lane * 16;
+    const int64_t kq_step = (int64_t)p.hq * KQ, hd_step = (int64_t)p.hv * kDcHead;
+    constexpr int VL = VP / 16, VR = 64 / VL;  // lanes a token's values, tokens an instruction
+    const uint16_t *vp = static_cast<const uint16_t *>(p.v) + b * p.v_bs + (int64_t)w.chunk0 * C * p.v_ts +
+                         (int64_t)h * D + wg_v0 + 8 * (lane % VL);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds;
+    // part 0 .. 3 of four (the CU takes 64 bytes a cycle: issued at once, they would stall the wave)
+    auto fetch = [&](int ch, int part) {
+        uint32_t to = lds0 + (ch & 1) * BUF;
+        const unsigned char *from = kq + ch * kq_step;
+        constexpr int QK = OUT ? KQ : KQ / 2;
+#pragma unroll
+        for (int o = 0; o < QK; o += W * 1024)
+            if (o / (W * 1024) % 4 == part)
+                dc_to_lds(from + o + wave * 1024, to + o + wave * 1024);
+        to += KQ;
+        from = hd + ch * hd_step;
+        constexpr int HD = OUT ? kDcHead : kDcP;
+#pragma unroll
+        for (int o = 0; o < HD; o += W * 1024)
+            if (o / (W * 1024) % 4 == part && (o + W * 1024 <= HD || o + wave * 1024 < HD))
+                dc_to_lds(from + o + wave * 1024, to + o + wave * 1024);
+        to += kDcHead;
+#pragma unroll
+        for (int q = 0; q < C / VR; q += W)
+            if (q / W % 4 == part) {
+                const int t = ch * C + (q + wave) * VR + lane / VL;  // rows behind the end repeat the last
+                dc_to_lds(reinterpret_cast<const unsigned char *>(vp + (int64_t)min(t, mine - 1) * p.v_ts),
+                          to + (q + wave) * 1024);
+            }
+    };
+    if (chunks > 0)
+#pragma unroll
+        for (int part = 0; part < 4; ++part)
+            fetch(0, part);
 
     // The state: S^T, tile n of keys; rows (keys) 4 g + r, column (value) c
     dc_f32x4 S[NV][KT];
     const int64_t head_at = pool * p.row_stride + (int64_t)h * D * D;
     float *carry = w.carry + ((int64_t)b * p.hv + h) * D * D;
+    if (!w.first || p.state_dtype == kF32) {
+        const float *s = (w.first ? static_cast<const float *>(p.state) + head_at : carry) + (v0 + c) * D + 4 * g;
 #pragma unroll
-    for (int x = 0; x < NV; ++x)
+        for (int x = 0; x < NV; ++x)
 #pragma unroll
-        for (int n = 0; n < KT; ++n) {
-            const int o = (v0 + 16 * x + c) * D + 16 * n + 4 * g;
-            if (!w.first || p.state_dtype == kF32) {
-                const float *s = w.first ? static_cast<const float *>(p.state) + head_at : carry;
-                S[x][n] = *reinterpret_cast<const dc_f32x4 *>(s + o);
-            } else {
-                const u32x2 r = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(p.state) + head_at + o);
+            for (int n = 0; n < KT; ++n)
+                S[x][n] = *reinterpret_cast<const dc_f32x4 *>(s + 16 * x * D + 16 * n);
+    } else {
+        const uint16_t *s = static_cast<const uint16_t *>(p.state) + head_at + (v0 + c) * D + 4 * g;
+        u32x2 raw[NV][KT];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    S[x][n][2 * e] = lo16(r[e], p.state_dtype);
-                    S[x][n][2 * e + 1] = hi16(r[e], p.state_dtype);
-                }
-            }
-        }
-
-    const unsigned char *kq = w.kq + ((int64_t)b * w.chunks * p.hq + j) * KQ;
-    const unsigned char *hd = w.head + ((int64_t)b * w.chunks * p.hv + h) * kDcHead;
-    const int64_t kq_step = (int64_t)p.hq * KQ, hd_step = (int64_t)p.hv * kDcHead;
-    u32x4 pre[LOADS];
-    auto fetch = [&](int ch) {
+        for (int x = 0; x < NV; ++x)
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int o = (i * 256 + threadIdx.x) * 16;
-            if (o < KQ)
-                pre[i] = *reinterpret_cast<const u32x4 *>(kq + ch * kq_step + o);
-            else if (o < BUF)
-                pre[i] = *reinterpret_cast<const u32x4 *>(hd + ch * hd_step + (o - KQ));
-        }
-    };
-    auto stage = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int o = (i * 256 + threadIdx.x) * 16;
-            if (o < BUF)
-                *reinterpret_cast<u32x4 *>(lds + buf * BUF + o) = pre[i];
-        }
-    };
-    const uint16_t *vp = static_cast<const uint16_t *>(p.v) + b * p.v_bs + (int64_t)h * D + v0 + c;
-    uint16_t vraw[NV][16];
-    auto fetch_v = [&](int ch) {
-        const int t0 = ch * C;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+            for (int n = 0; n < KT; ++n)
+                raw[x][n] = *reinterpret_cast<const u32x2 *>(s + 16 * x * D + 16 * n);
+        auto widen = [&](auto tag) {
 #pragma unroll
             for (int x = 0; x < NV; ++x)
-                vraw[x][i] = t < mine ? vp[(int64_t)(w.chunk0 * C + t) * p.v_ts + 16 * x] : 0;
-        }
-    };
-
+#pragma unroll
+                for (int n = 0; n < KT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[x][n][r] = cvt_raw1<decltype(tag)>(r % 2 ? raw[x][n][r / 2] >> 16 : raw[x][n][r / 2] & 0xffffu);
+        };
+        if (p.state_dtype == kF16)
+            widen(_Float16{});
+        else
+            widen(bf16_t{});
+    }
+    uint16_t *op = static_cast<uint16_t *>(p.out) + b * p.out_bs + (int64_t)h * D + v0;
+    const int o_off = c * (int)p.out_ts + 4 * g;
     float sc[NV];        // scale of the value column of this lane
     float isc[NV][4];    // 1 / scale of value columns 4 g + r
 #pragma unroll
@@ -507,28 +601,40 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
             isc[x][r] = 1.0f;
     }
 
-    if (chunks > 0) {
-        fetch(0);
-        fetch_v(0);
-        stage(0);
-    }
-    __syncthreads();
     for (int ch = 0; ch < chunks; ++ch) {
+        // this chunk's LDS is filled (by every wave: behind the barrier), the other one read
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
         unsigned char *image = lds + (ch & 1) * BUF;
         const unsigned char *blk = image + KQ;
         const float *scal = reinterpret_cast<const float *>(blk + kDcScalars);
-        float v[NV][16];
+        const int t0 = ch * C, n_tok = min(mine - t0, C);
+        const int64_t tok0 = (int64_t)w.chunk0 * C + t0;
+        const bool more = ch + 1 < chunks;
+        if (more)
+            fetch(ch + 1, 0);
+        u32x2 raw[NV][4];
 #pragma unroll
         for (int x = 0; x < NV; ++x)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[x][i] = cvt_raw1<IO>(vraw[x][i]);
-        if (ch + 1 < chunks) {
-            fetch(ch + 1);
-            fetch_v(ch + 1);
+            for (int i = 0; i < 4; ++i)
+                raw[x][i] = dc_ld_v<VP>(image + KQ + kDcHead + (wave * NV + x) * 32, i, lane);
+        if (n_tok < C) {  // what was read in the place of tokens behind the end
+#pragma unroll
+            for (int x = 0; x < NV; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 16 * i + 4 * g + 2 * e;
+                        raw[x][i][e] &= (t < n_tok ? 0xffffu : 0u) | (t + 1 < n_tok ? 0xffff0000u : 0u);
+                    }
         }
-        const int t0 = ch * C, n_tok = min(mine - t0, C);
-        const int64_t tok0 = (int64_t)w.chunk0 * C + t0;
+
+        u32x4 kf[4];  // in flight over the scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            kf[i] = dc_ld_op<D>(image, i, 0, lane);
 
         // scales, and whether the chunk may run on the matrix cores
         const float all = scal[kScMisc * 64], kind = scal[kScMisc * 64 + 1];
@@ -539,29 +645,35 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
         float z[NV];
 #pragma unroll
         for (int x = 0; x < NV; ++x) {
-            uint32_t ms = 0, mv = 0;
+            float ms[2] = {0.0f, 0.0f};  // a NaN of the state reaches every token of the chunk anyway
 #pragma unroll
             for (int n = 0; n < KT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    ms = max(ms, __float_as_uint(S[x][n][r]) & 0x7fffffffu);
-            ms = dc_max_groups(ms);
-            uint32_t least = 0x7f800000u;
+                ms[n & 1] = fmaxf(fmaxf(fmaxf(ms[n & 1], fabsf(S[x][n][0])), fabsf(S[x][n][1])),
+                                  fmaxf(fabsf(S[x][n][2]), fabsf(S[x][n][3])));
+            uint32_t tile[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    m = max(m, __float_as_uint(v[x][4 * i + r]) & 0x7fffffffu);
-                m = dc_max_groups(m);
-                mv = max(mv, m);
-                least = 16 * i + 16 <= n_tok ? min(least, m) : least;
+                const uint32_t m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+                    __builtin_bit_cast(dc_u16x2, raw[x][i][0] & 0x7fff7fffu),
+                    __builtin_bit_cast(dc_u16x2, raw[x][i][1] & 0x7fff7fffu)));
+                tile[i] = max(m & 0xffffu, m >> 16);
             }
-            slow |= ms >= 0x7f800000u || mv >= 0x7f800000u;
-            const float v_max = __uint_as_float(mv) * sc[x];
-            z[x] = v_max + (D > 64 ? 12.0f : 8.5f) * __uint_as_float(ms);
+            constexpr uint32_t kInf = __is_same(IO, _Float16) ? 0x7c00u : 0x7f80u;
+            const uint32_t mv = max(max(tile[0], tile[1]), max(tile[2], tile[3]));
+            slow |= mv >= kInf;
+            // z from one exchange: twice the larger of its two parts
+            const float part = fmaxf(cvt_raw1<IO>(mv) * sc[x], (D > 64 ? 12.0f : 8.5f) * fmaxf(ms[0], ms[1]));
+            z[x] = 2.0f * __uint_as_float(dc_max_groups(__float_as_uint(part)));
             slow |= !(z[x] < __builtin_inff());
-            slow |= fades && __uint_as_float(least) * sc[x] < z[x] * 0x1p-8f;
+            if (fades) {
+                const uint32_t m01 = dc_max2_groups(tile[0] | tile[1] << 16);
+                const uint32_t m23 = dc_max2_groups(tile[2] | tile[3] << 16);
+                uint32_t least = n_tok >= 16 ? m01 & 0xffffu : kInf;  // of whole tiles
+                least = n_tok >= 32 ? min(least, m01 >> 16) : least;
+                least = n_tok >= 48 ? min(least, m23 & 0xffffu) : least;
+                least = n_tok >= 64 ? min(least, m23 >> 16) : least;
+                slow |= cvt_raw1<IO>(least) * sc[x] < z[x] * 0x1p-8f;
+            }
             move |= z[x] > top || (z[x] <= top * 0x1p-3f && z[x] > 0.0f);
         }
         slow = __ballot(slow) != 0;
@@ -604,24 +716,40 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
                     sh[x] = u32x4{h0[0], h0[1], h1[0], h1[1]};
                     sl[x] = u32x4{l0[0], l0[1], l1[0], l1[1]};
                 }
+                u32x4 qf[4], kn[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const u32x4 kf = dc_ld_op<D>(image, i, ks, lane);
+                    if (OUT)
+                        qf[i] = dc_ld_op<D>(image + KQ / 2, i, ks, lane);
+                    if (ks + 1 < KS)
+                        kn[i] = dc_ld_op<D>(image, i, ks + 1, lane);
+                }
+#pragma unroll
+                for (int x = 0; x < NV; ++x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        X[x][i] = dc_mfma(kf[i], sh[x], X[x][i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        X[x][i] = dc_mfma(kf[i], sl[x], X[x][i]);
+                }
+                if (OUT)
 #pragma unroll
                     for (int x = 0; x < NV; ++x) {
-                        X[x][i] = dc_mfma(kf, sh[x], X[x][i]);
-                        X[x][i] = dc_mfma(kf, sl[x], X[x][i]);
-                    }
-                    if (outs) {
-                        const u32x4 qf = dc_ld_op<D>(image + KQ / 2, i, ks, lane);
 #pragma unroll
-                        for (int x = 0; x < NV; ++x) {
-                            O[x][i] = dc_mfma(sh[x], qf, O[x][i]);
-                            O[x][i] = dc_mfma(sl[x], qf, O[x][i]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            O[x][i] = dc_mfma(sh[x], qf[i], O[x][i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            O[x][i] = dc_mfma(sl[x], qf[i], O[x][i]);
                     }
-                }
+                if (ks + 1 < KS)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        kf[i] = kn[i];
             }
+            if (more)
+                fetch(ch + 1, 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const dc_f32x4 beta = *reinterpret_cast<const dc_f32x4 *>(scal + kScBeta * 64 + 16 * i + 4 * g);
@@ -630,31 +758,87 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
                 for (int x = 0; x < NV; ++x)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        X[x][i][r] = beta[r] * (v[x][4 * i + r] * sc[x] - gk[r] * X[x][i][r]);
+                    {
+                        const float vt = cvt_raw1<IO>(r % 2 ? raw[x][i][r / 2] >> 16 : raw[x][i][r / 2] & 0xffffu);
+                        X[x][i][r] = beta[r] * (vt * sc[x] - gk[r] * X[x][i][r]);
+                    }
             }
-            // U, tile after tile
-            u32x2 uh[NV][4], ul[NV][4];
+            if (more)
+                fetch(ch + 1, 2);
+            // U, tile after tile: 32-deep operands are pairs of tiles
+            u32x4 uh[NV][2], ul[NV][2];
+#pragma unroll
+            for (int x = 0; x < NV; ++x)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    uh[x][q] = ul[x][q] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int jt = 0; jt < i; ++jt) {
-                    const u32x4 lf = *reinterpret_cast<const u32x4 *>(blk + kDcL + (i * (i - 1) / 2 + jt) * kDcTile + lane * 16);
+                for (int q = 0; 2 * q < i; ++q) {
+                    const u32x4 lh = *reinterpret_cast<const u32x4 *>(blk + dc_l_pair(i, q) + lane * 16);
+                    const u32x4 ll = *reinterpret_cast<const u32x4 *>(blk + dc_l_pair(i, q) + kDcTile + lane * 16);
 #pragma unroll
                     for (int x = 0; x < NV; ++x) {
-                        X[x][i] = dc_mfma(lf, u32x4{ul[x][jt][0], ul[x][jt][1], 0, 0}, X[x][i]);
-                        X[x][i] = dc_mfma(lf, u32x4{uh[x][jt][0], uh[x][jt][1], uh[x][jt][0], uh[x][jt][1]}, X[x][i]);
+                        X[x][i] = dc_mfma(ll, uh[x][q], X[x][i]);
+                        X[x][i] = dc_mfma(lh, ul[x][q], X[x][i]);
+                        X[x][i] = dc_mfma(lh, uh[x][q], X[x][i]);
                     }
                 }
                 const u32x4 df = *reinterpret_cast<const u32x4 *>(blk + i * kDcTile + lane * 16);
+                const u32x2 dh = {df[0], df[1]}, dl = {df[2], df[3]};
 #pragma unroll
                 for (int x = 0; x < NV; ++x) {
                     u32x2 hi, lo;
                     dc_split(X[x][i], hi, lo);
                     dc_f32x4 u = {0, 0, 0, 0};
-                    u = dc_mfma(df, u32x4{lo[0], lo[1], 0, 0}, u);
-                    u = dc_mfma(df, u32x4{hi[0], hi[1], hi[0], hi[1]}, u);
+                    u = dc_mfma16(dl, hi, u);
+                    u = dc_mfma16(dh, lo, u);
+                    u = dc_mfma16(dh, hi, u);
                     X[x][i] = u;
-                    dc_split(u, uh[x][i], ul[x][i]);
+                    dc_split(u, hi, lo);
+                    uh[x][i >> 1][2 * (i & 1)] = hi[0];
+                    uh[x][i >> 1][2 * (i & 1) + 1] = hi[1];
+                    ul[x][i >> 1][2 * (i & 1)] = lo[0];
+                    ul[x][i >> 1][2 * (i & 1) + 1] = lo[1];
+                }
+            }
+            if (more)
+                fetch(ch + 1, 3);
+            if (OUT) {
+                dc_f32x4 Q[NV][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 2 * r; i < 4; ++i) {
+                        const u32x4 ph = *reinterpret_cast<const u32x4 *>(blk + dc_p_pair(i, r) + lane * 16);
+                        const u32x4 pl = *reinterpret_cast<const u32x4 *>(blk + dc_p_pair(i, r) + kDcTile + lane * 16);
+#pragma unroll
+                        for (int x = 0; x < NV; ++x) {
+                            if (r == 0)
+                                Q[x][i] = dc_f32x4{0, 0, 0, 0};
+                            Q[x][i] = dc_mfma(uh[x][r], pl, Q[x][i]);
+                            Q[x][i] = dc_mfma(ul[x][r], ph, Q[x][i]);
+                            Q[x][i] = dc_mfma(uh[x][r], ph, Q[x][i]);
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float go = scal[kScGo * 64 + 16 * i + c], qo = scal[kScQo * 64 + 16 * i + c];
+#pragma unroll
+                    for (int x = 0; x < NV; ++x) {
+                        float o[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            o[r] = isc[x][r] * (go * O[x][i][r] + qo * Q[x][i][r]);
+                        const u32x2 bits = {dc_pack<IO>(o[0], o[1]), dc_pack<IO>(o[2], o[3])};
+                        u32x2 *to = reinterpret_cast<u32x2 *>(op + (tok0 + 16 * i) * p.out_ts + (o_off + 16 * x));
+                        if (n_tok == C) {
+                            *to = bits;
+                        } else if (tok0 + 16 * i + c < p.seq_len) {
+                            *to = 16 * i + c < n_tok ? bits : u32x2{0, 0};
+                        }
+                    }
                 }
             }
             // the state behind the chunk
@@ -688,46 +872,18 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
                     }
                 }
             }
-            if (outs) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 16 * i + c;
-                    const float go = scal[kScGo * 64 + t], qo = scal[kScQo * 64 + t];
-                    dc_f32x4 q[NV];
-#pragma unroll
-                    for (int x = 0; x < NV; ++x)
-                        q[x] = dc_f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int jt = 0; jt <= i; ++jt) {
-                        const u32x4 pf = *reinterpret_cast<const u32x4 *>(blk + kDcP + (i * (i + 1) / 2 + jt) * kDcTile + lane * 16);
-#pragma unroll
-                        for (int x = 0; x < NV; ++x) {
-                            q[x] = dc_mfma(u32x4{ul[x][jt][0], ul[x][jt][1], 0, 0}, pf, q[x]);
-                            q[x] = dc_mfma(u32x4{uh[x][jt][0], uh[x][jt][1], uh[x][jt][0], uh[x][jt][1]}, pf, q[x]);
-                        }
-                    }
-                    const bool in = tok0 + t < p.seq_len;
-                    const bool live = t < n_tok;
-#pragma unroll
-                    for (int x = 0; x < NV; ++x) {
-                        float o[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            o[r] = live ? isc[x][r] * (go * O[x][i][r] + qo * q[x][r]) : 0.0f;
-                        if (in)
-                            st_raw4<IO>(static_cast<uint16_t *>(p.out) + b * p.out_bs + (tok0 + t) * p.out_ts +
-                                            (int64_t)h * D + v0 + 16 * x + 4 * g, 0, o);
-                    }
-                }
-            }
         } else {
+            if (more)
+#pragma unroll
+                for (int part = 1; part < 4; ++part)
+                    fetch(ch + 1, part);
             // token by token, in the scaled units that the state has
             for (int t = 0; t < n_tok; ++t) {
                 const float alpha = scal[kScAlpha * 64 + t], ks = scal[kScKs * 64 + t];
                 const float beta = scal[kScBeta * 64 + t], qs = scal[kScQo * 64 + t];
 #pragma unroll
                 for (int x = 0; x < NV; ++x) {
-                    const float vt = cvt_raw1<IO>(vp[(tok0 + t) * p.v_ts + 16 * x]);
+                    const float vt = ld_elem<IO>(image + KQ + kDcHead + t * VP, (wave * NV + x) * 16 + c);
                     float sum = 0.0f;
                     dc_f32x4 k[KT];
 #pragma unroll
@@ -747,7 +903,7 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             S[x][n][r] = S[x][n][r] * alpha + uk * k[n][r];
-                    if (outs) {
+                    if (OUT) {
                         float o = 0.0f;
 #pragma unroll
                         for (int n = 0; n < KT; ++n) {
@@ -762,16 +918,13 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
                     }
                 }
             }
-            if (outs)
+            if (OUT)
                 for (int t = n_tok; t < C && tok0 + t < p.seq_len; ++t)
                     if (g == 0)
 #pragma unroll
                         for (int x = 0; x < NV; ++x)
                             st_elem<IO>(p.out, b * p.out_bs + (tok0 + t) * p.out_ts + (int64_t)h * D + v0 + 16 * x + c, 0.0f);
         }
-        if (ch + 1 < chunks)
-            stage((ch + 1) & 1);
-        __syncthreads();
     }
 
     if (w.last && !p.update)
@@ -795,14 +948,17 @@ __global__ __launch_bounds__(256, 1) void delta_sweep_kernel(DeltaParams p, Delt
         }
 }
 
-template <typename IO, int D, int NV>
+template <typename IO, int D, int NV, int W>
 hipError_t launch_delta_sweep(const DeltaParams &p, const DeltaWork &w, hipStream_t stream)
 {
-    const __int128 groups = (__int128)p.batch * p.hv * (D / (64 * NV));
-    if (!launchable(groups, 256))
+    const __int128 groups = (__int128)p.batch * p.hv * (D / (16 * W * NV));
+    if (!launchable(groups, 64 * W))
         return hipErrorInvalidConfiguration;
     const uint32_t n = (uint32_t)groups;
-    delta_sweep_kernel<IO, D, NV><<<dim3(n), 256, 0, stream>>>(p, w, n % 8 == 0);
+    if (p.out)
+        delta_sweep_kernel<IO, D, NV, W, true><<<dim3(n), 64 * W, 0, stream>>>(p, w, n % 8 == 0);
+    else
+        delta_sweep_kernel<IO, D, NV, W, false><<<dim3(n), 64 * W, 0, stream>>>(p, w, n % 8 == 0);
     return hipGetLastError();
 }
 
@@ -825,8 +981,8 @@ hipError_t launch_delta_chunks_d(const DeltaParams &p, const DeltaPlan &plan, hi
         delta_prep_kernel<IO, D><<<dim3((uint32_t)(w.chunks * p.hq), p.batch), 256, 0, stream>>>(p, w);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess)
-            e = plan.nv == 2 ? launch_delta_sweep<IO, D, D >= 128 ? 2 : 1>(p, w, stream)
-                             : launch_delta_sweep<IO, D, 1>(p, w, stream);
+            e = plan.wide ? launch_delta_sweep<IO, D, 1, D / 16>(p, w, stream)
+                          : launch_delta_sweep<IO, D, 1, 4>(p, w, stream);
         if (e != hipSuccess)
             return e;
     }
