@@ -7,8 +7,8 @@
 // The k largest logits of a wave stand in its lanes, entry i in lane i, ordered
 // by (value descending, index ascending). A tile of 64 x 16 logits is compared
 // with the last of them by the lanes' maxima: most tiles after the first few hold
-// nothing that gets in. In the first tile the k-th largest of the 64 lanes' maxima bounds
-// the k-th largest logit from below, which leaves little more than k to insert.
+// nothing that gets in. The k-th largest of the 64 lanes' maxima over all tiles so far
+// bounds the k-th largest logit from below, which leaves little more than k to insert.
 //
 // A row goes to one workgroup where there are rows enough, else to several:
 // their sums and lists go through the workspace to a second launch, one
@@ -29,23 +29,22 @@ constexpr int kWaves = 4;          // waves of a workgroup
 constexpr int kMaxTop = SSU_MAX_TOP;
 constexpr float kFloor = -200.0f;  // e^x is 0 in fp32 far above
 
-// What a part of a row comes to.
+// What a part of a row comes to; s is NaN where a logit is NaN or +inf.
 struct Sums {
     float m, s, t;
-    int bad;  // a NaN or +inf among the logits
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// x - m, where -inf (of a masked logit, or of an m without any logit) counts as far below
-__device__ __forceinline__ float below(float x, float m)
-{
-    return fmaxf(x - (m == neg_inf() ? 0.0f : m), kFloor);
-}
+// An m that may be subtracted: one of -inf has no logit to it
+__device__ __forceinline__ float anchor(float m) { return m == neg_inf() ? 0.0f : m; }
+
+// e^x by the hardware's 2^x (within an ulp; the argument's own rounding is |x| 2^-24 of the value)
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
 
 __device__ __forceinline__ void rescale(Sums &a, float m)
 {
-    const float d = below(a.m, m), e = expf(d);
+    const float d = fmaxf(a.m - anchor(m), kFloor), e = exp_of(d);
     a.t = e * (a.t + d * a.s);
     a.s *= e;
     a.m = m;
@@ -56,7 +55,7 @@ __device__ __forceinline__ Sums join(Sums a, Sums b)
     const float m = fmaxf(a.m, b.m);
     rescale(a, m);
     rescale(b, m);
-    return {m, a.s + b.s, a.t + b.t, a.bad | b.bad};
+    return {m, a.s + b.s, a.t + b.t};
 }
 
 __device__ __forceinline__ bool better(float x, int i, float y, int j)
@@ -80,8 +79,9 @@ struct Top {
     __device__ __forceinline__ void insert(float x, int i, int k, int lane)
     {
         const int at = __popcll(__ballot(lane < k && better(v, id, x, i)));
-        const float pv = __shfl_up(v, 1, 64);
-        const int pi = __shfl_up(id, 1, 64);
+        // DPP wave_shr:1, a lane's value from the lane before it
+        const float pv = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x138, 0xF, 0xF, false));
+        const int pi = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xF, 0xF, false);
         v = lane == at ? x : lane > at ? pv : v;
         id = lane == at ? i : lane > at ? pi : id;
         last_v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), k - 1));
@@ -96,7 +96,7 @@ __device__ __forceinline__ float kth_of_lanes(float x, int k)
     const uint32_t b = __float_as_uint(x);
     const uint32_t key = b & 0x80000000u ? ~b : b | 0x80000000u;
     uint32_t bound = 0;
-    for (int bit = 31; bit >= 8; --bit) {  // the low bits are left at 0: still a bound from below
+    for (int bit = 31; bit >= 16; --bit) {  // the low bits are left at 0: still a bound from below
         const uint32_t next = bound | (1u << bit);
         if (__popcll(__ballot(key >= next)) >= k)
             bound = next;
@@ -152,74 +152,74 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
                           Top &top)
 {
     using Tile = LogitTile<T>;
-    sums = {neg_inf(), 0.0f, 0.0f, 0};
+    sums = {neg_inf(), 0.0f, 0.0f};
     top.clear();
     constexpr int N = 64 * kTile;
     Tile next;
     if (begin < end)
         next.template load<VEC>(row + begin, end - begin, lane);
-    bool first = true;
-    bool bad = false;
+    float most = neg_inf();   // of the lane, over all tiles
+    float bound = neg_inf();  // at least k logits reach it
     for (int64_t base = begin; base < end; base += (int64_t)step * N) {
         const Tile cur = next;
         const int left = end - (int)base;
         if (base + (int64_t)step * N < end)
             next.template load<VEC>(row + base + (int64_t)step * N, left - step * N, lane);
         float x[kTile];
-        float m = neg_inf();
 #pragma unroll
         for (int l = 0; l < Tile::NL; ++l)
 #pragma unroll
-            for (int e = 0; e < Tile::VE; ++e) {
-                float v = cur.value(l, e);
-                if (left < N)
-                    v = Tile::at(lane, l, e) < left ? v : neg_inf();
-                bad |= !(v <= 3.4028234663852886e38f);
-                m = fmaxf(m, v);
-                x[l * Tile::VE + e] = v;
-            }
+            for (int e = 0; e < Tile::VE; ++e)
+                x[l * Tile::VE + e] = cur.value(l, e);
+        if (left < N) {
+#pragma unroll
+            for (int l = 0; l < Tile::NL; ++l)
+#pragma unroll
+                for (int e = 0; e < Tile::VE; ++e)
+                    if (Tile::at(lane, l, e) >= left)
+                        x[l * Tile::VE + e] = neg_inf();
+        }
+        float m = neg_inf();
+#pragma unroll
+        for (int e = 0; e < kTile; ++e)
+            m = fmaxf(m, x[e]);
         if (m > sums.m)
             rescale(sums, m);
+        const float from = anchor(sums.m);
 #pragma unroll
         for (int e = 0; e < kTile; ++e) {
-            const float d = below(x[e], sums.m), p = expf(d);
+            const float d = x[e] - from, p = exp_of(d);  // a NaN stays one in s
             sums.s += p;
-            sums.t += p * d;
+            sums.t += p * fmaxf(d, kFloor);
         }
-        if (k > 0) {
-            float bound = neg_inf();
-            if (first)
-                bound = kth_of_lanes(m, k);
-            first = false;
-            if (__ballot(m >= bound && m >= top.last_v)) {
+        if (k > 0 && __ballot(m >= bound && m >= top.last_v)) {
+            most = fmaxf(most, m);
+            bound = fmaxf(bound, kth_of_lanes(most, k));
 #pragma unroll
-                for (int l = 0; l < Tile::NL; ++l)
+            for (int l = 0; l < Tile::NL; ++l)
 #pragma unroll
-                    for (int e = 0; e < Tile::VE; ++e) {
-                        const float v = x[l * Tile::VE + e];
-                        const int at = Tile::at(lane, l, e), id = (int)base + at;
-                        const bool in = at < left && v >= bound;
-                        uint64_t todo = __ballot(in && better(v, id, top.last_v, top.last_id));
-                        while (todo) {
-                            const int from = __ffsll((unsigned long long)todo) - 1;
-                            top.insert(__builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                                                                     __builtin_bit_cast(int, v), from)),
-                                       __builtin_amdgcn_readlane(id, from), k, lane);
-                            todo &= todo - 1;
-                            todo &= __ballot(in && better(v, id, top.last_v, top.last_id));
-                        }
+                for (int e = 0; e < Tile::VE; ++e) {
+                    const float v = x[l * Tile::VE + e];
+                    const int at = Tile::at(lane, l, e), id = (int)base + at;
+                    const bool in = at < left && v >= bound;
+                    uint64_t todo = __ballot(in && better(v, id, top.last_v, top.last_id));
+                    while (todo) {
+                        const int one = __ffsll((unsigned long long)todo) - 1;
+                        top.insert(__builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                                 __builtin_bit_cast(int, v), one)),
+                                   __builtin_amdgcn_readlane(id, one), k, lane);
+                        todo &= todo - 1;
+                        todo &= __ballot(in && better(v, id, top.last_v, top.last_id));
                     }
-            }
+                }
         }
     }
-    sums.bad = bad;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         Sums b;
         b.m = __shfl_xor(sums.m, o, 64);
         b.s = __shfl_xor(sums.s, o, 64);
         b.t = __shfl_xor(sums.t, o, 64);
-        b.bad = __shfl_xor(sums.bad, o, 64);
         sums = join(sums, b);
     }
 }
@@ -237,15 +237,16 @@ __device__ void write_row(const LogprobParams &p, int64_t row, const T *logits, 
 {
     const float nan = __builtin_nanf("");
     const float log_s = logf(a.s);
+    const bool bad = a.s != a.s;
     // x - lse as (x - m) - log s: exact differences of large logits first
     auto logprob = [&](float x) {
-        return a.bad ? nan : x == neg_inf() ? neg_inf() : (x - a.m) - log_s;
+        return bad ? nan : x == neg_inf() ? neg_inf() : (x - a.m) - log_s;
     };
     if (lane == 0) {
         const int tok = p.tokens[row];
         p.logprobs[row] = tok < 0 || tok >= p.vocab ? neg_inf() : logprob(ld_elem<T>(logits, tok));
         if (p.entropy)
-            p.entropy[row] = a.bad ? nan : a.m == neg_inf() ? 0.0f : fmaxf(log_s - a.t / a.s, 0.0f);
+            p.entropy[row] = bad ? nan : a.m == neg_inf() ? 0.0f : fmaxf(log_s - a.t / a.s, 0.0f);
     }
     if (lane < p.top) {
         const bool none = id == INT_MAX;  // only beside NaN
@@ -297,7 +298,7 @@ __device__ void place_lists(const float *vs, const int *ids, int parts, int k, f
 }
 
 // Part of a row in the workspace: its sums, then k values, then k ids.
-__host__ __device__ inline int64_t part_words(int64_t top) { return 4 + 2 * top; }
+__host__ __device__ inline int64_t part_words(int64_t top) { return 4 + 2 * top; }  // one word is left out
 
 template <typename T, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, int parts, int part)
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int
         place_lists(vs, ids, parts, p.top, best_v, best_id);
     if (threadIdx.x >= 64)
         return;
-    Sums a = {neg_inf(), 0.0f, 0.0f, 0};
+    Sums a = {neg_inf(), 0.0f, 0.0f};
     if (lane < parts)
         a = *reinterpret_cast<const Sums *>(w + lane * pw);
 #pragma unroll
@@ -383,7 +384,6 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int
         b.m = __shfl_xor(a.m, o, 64);
         b.s = __shfl_xor(a.s, o, 64);
         b.t = __shfl_xor(a.t, o, 64);
-        b.bad = __shfl_xor(a.bad, o, 64);
         a = join(a, b);
     }
     const int b = (int)(row / p.num_tokens), t = (int)(row - (int64_t)b * p.num_tokens);
