@@ -4,8 +4,8 @@
 // Each lane keeps m, s and the weighted sum t of what it has seen and rescales
 // them when m grows (t <- e^d (t + d s), d = m_old - m_new). HBM bounds it.
 //
-// The k largest logits of a wave stand in its lanes, entry i in lane i, ordered
-// by (value descending, index ascending). A tile of 64 x 16 logits is compared
+// The k largest logits of a wave stand in its lanes, entry i in lane i, as keys that
+// order by (value descending, index ascending). A tile of 64 x 16 logits is compared
 // with the last of them by the lanes' maxima: most tiles after the first few hold
 // nothing that gets in. The k-th largest of the 64 lanes' maxima over all tiles so far
 // bounds the k-th largest logit from below, which leaves little more than k to insert.
@@ -14,7 +14,6 @@
 // their sums and lists go through the workspace to a second launch, one
 // workgroup a row, which orders them in a fixed order. So results do not
 // depend on which workgroup comes first.
-#include <limits.h>
 #include <math.h>
 
 #include "ssu_device.h"
@@ -58,50 +57,87 @@ __device__ __forceinline__ Sums join(Sums a, Sums b)
     return {m, a.s + b.s, a.t + b.t};
 }
 
-__device__ __forceinline__ bool better(float x, int i, float y, int j)
+// Bits that order as the values do (-0 as 0)
+__device__ __forceinline__ uint32_t order_of(float x)
 {
-    return x > y || (x == y && i < j);
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_order(uint32_t o)
+{
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// The k largest of a wave: lane i < k holds entry i.
-struct Top {
-    float v;
-    int id;
-    float last_v;  // entry k - 1, the same in every lane
-    int last_id;
+// A logit and its index as one number, the larger the better; 0: none.
+typedef uint64_t Key;
+__device__ __forceinline__ Key key_of(float x, int i) { return (Key)order_of(x) << 32 | ~(uint32_t)i; }
+__device__ __forceinline__ float logit_of(Key k) { return of_order((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int index_of(Key k) { return (int)~(uint32_t)k; }
 
-    __device__ __forceinline__ void clear()
+__device__ __forceinline__ Key lane_key(Key k, int lane)  // of lane `lane`, the same in every lane
+{
+    return (Key)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, lane);
+}
+
+// The k largest of a wave: lane i < k holds entry i. Candidates are gathered in LDS and
+// ranked against the list and each other, 64 - k at a time, when there are some or at the
+// end: no chain from one to the next.
+constexpr int kGather = 128;  // candidates that wait for the next tile's at most
+struct TopLds {
+    Key got[64 * kTile + kGather];
+    Key list[kMaxTop];
+};
+
+__device__ __forceinline__ void wave_lds_fence()  // LDS writes of the wave's lanes before its reads
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+struct Top {
+    Key key;
+    Key last;  // entry k - 1, the same in every lane
+
+    // the first n candidates of lds
+    __device__ void take(TopLds &lds, int n, int k, int lane)
     {
-        v = last_v = neg_inf();
-        id = last_id = INT_MAX;
-    }
-    // x, i the same in every lane
-    __device__ __forceinline__ void insert(float x, int i, int k, int lane)
-    {
-        const int at = __popcll(__ballot(lane < k && better(v, id, x, i)));
-        // DPP wave_shr:1, a lane's value from the lane before it
-        const float pv = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x138, 0xF, 0xF, false));
-        const int pi = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xF, 0xF, false);
-        v = lane == at ? x : lane > at ? pv : v;
-        id = lane == at ? i : lane > at ? pi : id;
-        last_v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), k - 1));
-        last_id = __builtin_amdgcn_readlane(id, k - 1);
+        wave_lds_fence();
+        for (int i = 0; i < n; i += 64 - k) {
+            const int more = min(n - i, 64 - k);
+            Key x = lane < k ? key : 0;
+            if (lane >= k && lane < k + more)
+                x = lds.got[i + lane - k];
+            if (!__ballot(lane >= k && x > last))
+                continue;
+            int rank = 0;
+            for (int j = 0; j < k + more; ++j)
+                rank += lane_key(x, j) > x ? 1 : 0;
+            if (lane < k)
+                lds.list[lane] = 0;
+            wave_lds_fence();
+            if (x != 0 && rank < k)
+                lds.list[rank] = x;
+            wave_lds_fence();
+            key = lane < k ? lds.list[lane] : 0;
+            wave_lds_fence();
+            last = lane_key(key, k - 1);
+        }
     }
 };
 
-// k-th largest of the lanes' values (k <= 64), -inf if it is not finite: bit after bit of
-// the largest bound that k lanes reach, over bits that order as the values do.
+// k-th largest of the lanes' values (k <= 64) or less, -inf if it is not finite: bit after
+// bit of the largest bound that k lanes reach
 __device__ __forceinline__ float kth_of_lanes(float x, int k)
 {
-    const uint32_t b = __float_as_uint(x);
-    const uint32_t key = b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t key = order_of(x);
     uint32_t bound = 0;
     for (int bit = 31; bit >= 16; --bit) {  // the low bits are left at 0: still a bound from below
         const uint32_t next = bound | (1u << bit);
         if (__popcll(__ballot(key >= next)) >= k)
             bound = next;
     }
-    const float f = __uint_as_float(bound & 0x80000000u ? bound ^ 0x80000000u : ~bound);
+    const float f = of_order(bound);
     return f <= 3.0e38f && f >= -3.0e38f ? f : neg_inf();
 }
 
@@ -149,17 +185,18 @@ struct LogitTile {
 // Logits [begin, end) of a row by one wave, every `step` th tile from `begin`.
 template <typename T, bool VEC>
 __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int lane, Sums &sums,
-                          Top &top)
+                          Top &top, TopLds &lds)
 {
     using Tile = LogitTile<T>;
     sums = {neg_inf(), 0.0f, 0.0f};
-    top.clear();
+    top.key = top.last = 0;
     constexpr int N = 64 * kTile;
     Tile next;
     if (begin < end)
         next.template load<VEC>(row + begin, end - begin, lane);
     float most = neg_inf();   // of the lane, over all tiles
     float bound = neg_inf();  // at least k logits reach it
+    int n = 0;                // candidates gathered
     for (int64_t base = begin; base < end; base += (int64_t)step * N) {
         const Tile cur = next;
         const int left = end - (int)base;
@@ -192,28 +229,37 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
             sums.s += p;
             sums.t += p * fmaxf(d, kFloor);
         }
-        if (k > 0 && __ballot(m >= bound && m >= top.last_v)) {
+        // a full list's last entry: an equal logit of a later tile comes behind it
+        float full = top.last ? logit_of(top.last) : __builtin_nanf("");
+        if (k > 0 && __ballot(m >= bound && !(m <= full))) {
             most = fmaxf(most, m);
             bound = fmaxf(bound, kth_of_lanes(most, k));
+            if (n > kGather) {
+                top.take(lds, n, k, lane);
+                n = 0;
+                full = top.last ? logit_of(top.last) : __builtin_nanf("");
+            }
 #pragma unroll
             for (int l = 0; l < Tile::NL; ++l)
 #pragma unroll
                 for (int e = 0; e < Tile::VE; ++e) {
                     const float v = x[l * Tile::VE + e];
-                    const int at = Tile::at(lane, l, e), id = (int)base + at;
-                    const bool in = at < left && v >= bound;
-                    uint64_t todo = __ballot(in && better(v, id, top.last_v, top.last_id));
-                    while (todo) {
-                        const int one = __ffsll((unsigned long long)todo) - 1;
-                        top.insert(__builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                                                                 __builtin_bit_cast(int, v), one)),
-                                   __builtin_amdgcn_readlane(id, one), k, lane);
-                        todo &= todo - 1;
-                        todo &= __ballot(in && better(v, id, top.last_v, top.last_id));
+                    const bool may = v >= bound && !(v <= full);
+                    if (__ballot(may)) {
+                        const int at = Tile::at(lane, l, e);
+                        const bool in = may && at < left;
+                        const uint64_t mask = __ballot(in);
+                        if (in)
+                            lds.got[n + (int)__builtin_amdgcn_mbcnt_hi(
+                                            (uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
+                                key_of(v, (int)base + at);
+                        n += __popcll(mask);
                     }
                 }
         }
     }
+    if (n > 0)
+        top.take(lds, n, k, lane);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         Sums b;
@@ -224,16 +270,30 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
     }
 }
 
-__device__ __forceinline__ bool row_live(const LogprobParams &p, int64_t row)
+__device__ __forceinline__ bool row_live(const LogprobParams &p, int row)
 {
-    const int b = (int)(row / p.num_tokens), t = (int)(row - (int64_t)b * p.num_tokens);
+    const int b = row / p.num_tokens, t = row - b * p.num_tokens;
     return (!p.idx || p.idx[b] >= 0) && (!p.ctx || t < p.ctx[b]);
 }
 
-// The answers of a row from its sums; lane i < k holds entry i of the list.
+// The given token's logit, read early
+struct Given {
+    float x;
+    bool outside;  // of [0, V)
+};
 template <typename T>
-__device__ void write_row(const LogprobParams &p, int64_t row, const T *logits, const Sums &a,
-                          float v, int id, int lane)
+__device__ __forceinline__ Given given_logit(const LogprobParams &p, int row, const T *logits)
+{
+    const int tok = p.tokens[row];
+    Given g = {0.0f, tok < 0 || tok >= p.vocab};
+    if (!g.outside)
+        g.x = ld_elem<T>(logits, tok);
+    return g;
+}
+
+// The answers of a row from its sums; lane i < k holds entry i of the list.
+__device__ void write_row(const LogprobParams &p, int64_t row, const Given &given, const Sums &a,
+                          Key key, int lane)
 {
     const float nan = __builtin_nanf("");
     const float log_s = logf(a.s);
@@ -243,15 +303,14 @@ __device__ void write_row(const LogprobParams &p, int64_t row, const T *logits, 
         return bad ? nan : x == neg_inf() ? neg_inf() : (x - a.m) - log_s;
     };
     if (lane == 0) {
-        const int tok = p.tokens[row];
-        p.logprobs[row] = tok < 0 || tok >= p.vocab ? neg_inf() : logprob(ld_elem<T>(logits, tok));
+        p.logprobs[row] = given.outside ? neg_inf() : logprob(given.x);
         if (p.entropy)
             p.entropy[row] = bad ? nan : a.m == neg_inf() ? 0.0f : fmaxf(log_s - a.t / a.s, 0.0f);
     }
     if (lane < p.top) {
-        const bool none = id == INT_MAX;  // only beside NaN
-        p.top_ids[row * p.top + lane] = none ? -1 : id;
-        p.top_logprobs[row * p.top + lane] = none ? nan : logprob(v);
+        const bool none = key == 0;  // only beside NaN
+        p.top_ids[row * p.top + lane] = none ? -1 : index_of(key);
+        p.top_logprobs[row * p.top + lane] = none ? nan : logprob(logit_of(key));
     }
 }
 
@@ -268,88 +327,97 @@ __device__ void write_padding(const LogprobParams &p, int64_t row, int lane)
     }
 }
 
-// The k best of `parts` ordered lists of k in (vs, ids), each entry's place being
-// the number of better ones; the first wave writes them to its lanes.
-__device__ void place_lists(const float *vs, const int *ids, int parts, int k, float *out_v,
-                            int *out_id)
+// The k best of `parts` ordered lists of k keys. The best of the lists' last entries bounds
+// them from below; the few that reach it are gathered, and each one's place is the number
+// of better ones.
+struct Gathered {
+    unsigned long long bound;
+    int n;
+};
+
+__device__ void place_lists(const Key *lists, int parts, int k, Key *got, Gathered &g, Key *out)
 {
-    const int n = parts * k;
-    for (int i = threadIdx.x; i < k; i += blockDim.x) {
-        out_v[i] = neg_inf();
-        out_id[i] = INT_MAX;
+    if (threadIdx.x == 0)
+        g = {0, 0};
+    for (int i = threadIdx.x; i < k; i += blockDim.x)
+        out[i] = 0;
+    __syncthreads();
+    if ((int)threadIdx.x < parts)
+        atomicMax(&g.bound, (unsigned long long)lists[threadIdx.x * k + k - 1]);
+    __syncthreads();
+    const Key bound = g.bound;
+    for (int i = threadIdx.x; i < parts * k; i += blockDim.x) {
+        const Key x = lists[i];
+        if (x != 0 && x >= bound)
+            got[atomicAdd(&g.n, 1)] = x;  // in any order: places come from the values
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const float x = vs[i];
-        const int id = ids[i];
-        int at = i % k;  // those before it in its own list
-        for (int q = 0; q < parts && at < k; ++q) {
-            if (q == i / k)
-                continue;
-            for (int j = 0; j < k && better(vs[q * k + j], ids[q * k + j], x, id); ++j)
-                ++at;
-        }
-        if (at < k && id != INT_MAX) {
-            out_v[at] = x;
-            out_id[at] = id;
-        }
+    const int m = g.n;
+    for (int i = threadIdx.x; i < m; i += blockDim.x) {
+        const Key x = got[i];
+        int at = 0;
+#pragma unroll 8
+        for (int j = 0; j < m; ++j)
+            at += got[j] > x ? 1 : 0;
+        if (at < k)
+            out[at] = x;
     }
     __syncthreads();
 }
 
-// Part of a row in the workspace: its sums, then k values, then k ids.
-__host__ __device__ inline int64_t part_words(int64_t top) { return 4 + 2 * top; }  // one word is left out
+// Part of a row in the workspace: its sums (and a word for the alignment), then k keys.
+__host__ __device__ inline int64_t part_words(int64_t top) { return 4 + 2 * top; }
 
 template <typename T, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, int parts, int part)
 {
     __shared__ Sums sums_of[kWaves];
-    __shared__ float vs[kWaves * kMaxTop], best_v[kMaxTop];
-    __shared__ int ids[kWaves * kMaxTop], best_id[kMaxTop];
+    __shared__ Key lists[kWaves * kMaxTop], best[kMaxTop];
+    __shared__ TopLds tops[kWaves];
+    __shared__ Gathered gathered;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x / (uint32_t)parts;
-    const int which = (int)(blockIdx.x - (uint32_t)(row * parts));
+    const int row = (int)(blockIdx.x / (uint32_t)parts);
+    const int which = (int)(blockIdx.x - (uint32_t)row * (uint32_t)parts);
     if (!row_live(p, row)) {
         if (which == 0 && wave == 0)
             write_padding(p, row, lane);
         return;
     }
-    const int b = (int)(row / p.num_tokens), t = (int)(row - (int64_t)b * p.num_tokens);
+    const int b = row / p.num_tokens, t = row - b * p.num_tokens;
     const T *logits = static_cast<const T *>(p.logits) + b * p.l_bs + t * p.l_rs;
+    Given given = {};
+    if (parts == 1 && wave == 0)
+        given = given_logit<T>(p, row, logits);
     const int64_t begin = (int64_t)which * part;
     const int end = (int)min((int64_t)p.vocab, begin + part);
     Sums sums;
     Top top;
     const int64_t mine = begin + (int64_t)wave * 64 * kTile;
-    wave_pass<T, VEC>(logits, (int)min(mine, (int64_t)end), end, kWaves, p.top, lane, sums, top);
+    wave_pass<T, VEC>(logits, (int)min(mine, (int64_t)end), end, kWaves, p.top, lane, sums, top,
+                      tops[wave]);
     if (lane == 0)
         sums_of[wave] = sums;
-    if (lane < p.top) {
-        vs[wave * p.top + lane] = top.v;
-        ids[wave * p.top + lane] = top.id;
-    }
+    if (lane < p.top)
+        lists[wave * p.top + lane] = top.key;
     __syncthreads();
     if (p.top > 0)
-        place_lists(vs, ids, kWaves, p.top, best_v, best_id);
+        place_lists(lists, kWaves, p.top, tops[0].got, gathered, best);
     if (wave != 0)
         return;
     Sums a = sums_of[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w)
         a = join(a, sums_of[w]);
-    const float v = lane < p.top ? best_v[lane] : 0.0f;
-    const int id = lane < p.top ? best_id[lane] : 0;
+    const Key key = lane < p.top ? best[lane] : 0;
     if (parts == 1) {
-        write_row<T>(p, row, logits, a, v, id, lane);
+        write_row(p, row, given, a, key, lane);
         return;
     }
-    float *w = static_cast<float *>(p.workspace) + (row * parts + which) * part_words(p.top);
+    float *w = static_cast<float *>(p.workspace) + ((int64_t)row * parts + which) * part_words(p.top);
     if (lane == 0)
         *reinterpret_cast<Sums *>(w) = a;
-    if (lane < p.top) {
-        w[4 + lane] = v;
-        reinterpret_cast<int *>(w)[4 + p.top + lane] = id;
-    }
+    if (lane < p.top)
+        reinterpret_cast<Key *>(w + 4)[lane] = key;
 }
 
 constexpr int kMaxParts = 64;
@@ -357,39 +425,42 @@ constexpr int kMaxParts = 64;
 template <typename T>
 __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int parts)
 {
-    __shared__ float vs[kMaxParts * kMaxTop], best_v[kMaxTop];
-    __shared__ int ids[kMaxParts * kMaxTop], best_id[kMaxTop];
+    __shared__ Key lists[kMaxParts * kMaxTop], got[kMaxParts * kMaxTop], best[kMaxTop];
+    __shared__ Gathered gathered;
     const int lane = threadIdx.x & 63;
-    const int64_t row = blockIdx.x;
+    const int row = blockIdx.x;
     if (!row_live(p, row))
         return;
-    const float *w = static_cast<const float *>(p.workspace) + row * parts * part_words(p.top);
+    const int b = row / p.num_tokens, t = row - b * p.num_tokens;
+    const T *logits = static_cast<const T *>(p.logits) + b * p.l_bs + t * p.l_rs;
     const int64_t pw = part_words(p.top);
+    const float *w = static_cast<const float *>(p.workspace) + (int64_t)row * parts * pw;
+    const bool first = threadIdx.x < 64;
+    Given given = {};
+    Sums a = {neg_inf(), 0.0f, 0.0f};
+    if (first) {  // in flight with the lists
+        given = given_logit<T>(p, row, logits);
+        if (lane < parts)
+            a = *reinterpret_cast<const Sums *>(w + lane * pw);
+    }
     for (int i = threadIdx.x; i < parts * p.top; i += blockDim.x) {
         const int q = i / p.top, j = i - q * p.top;
-        vs[i] = w[q * pw + 4 + j];
-        ids[i] = reinterpret_cast<const int *>(w)[q * pw + 4 + p.top + j];
+        lists[i] = reinterpret_cast<const Key *>(w + q * pw + 4)[j];
     }
     __syncthreads();
     if (p.top > 0)
-        place_lists(vs, ids, parts, p.top, best_v, best_id);
-    if (threadIdx.x >= 64)
+        place_lists(lists, parts, p.top, got, gathered, best);
+    if (!first)
         return;
-    Sums a = {neg_inf(), 0.0f, 0.0f};
-    if (lane < parts)
-        a = *reinterpret_cast<const Sums *>(w + lane * pw);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        Sums b;
-        b.m = __shfl_xor(a.m, o, 64);
-        b.s = __shfl_xor(a.s, o, 64);
-        b.t = __shfl_xor(a.t, o, 64);
-        a = join(a, b);
+        Sums s;
+        s.m = __shfl_xor(a.m, o, 64);
+        s.s = __shfl_xor(a.s, o, 64);
+        s.t = __shfl_xor(a.t, o, 64);
+        a = join(a, s);
     }
-    const int b = (int)(row / p.num_tokens), t = (int)(row - (int64_t)b * p.num_tokens);
-    const T *logits = static_cast<const T *>(p.logits) + b * p.l_bs + t * p.l_rs;
-    write_row<T>(p, row, logits, a, lane < p.top ? best_v[lane] : 0.0f,
-                 lane < p.top ? best_id[lane] : 0, lane);
+    write_row(p, row, given, a, lane < p.top ? best[lane] : 0, lane);
 }
 
 // Workgroups a row takes: enough to fill the GPU, each with a tile a wave at least.

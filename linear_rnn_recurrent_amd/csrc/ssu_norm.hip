@@ -18,6 +18,15 @@
 namespace ssu {
 namespace {
 
+typedef float nm_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 nm_bf16x2 __attribute__((ext_vector_type(2)));
+
+// z / (1 + e^-z) by the hardware's 2^x and reciprocal, an ulp each
+__device__ __forceinline__ float gate_of(float z)
+{
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+
 // Eight values of runtime type dt as their bits, converted later so that the
 // loads of all tensors are in flight together
 struct Raw8 {
@@ -85,7 +94,8 @@ __device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float 
             u32x4 w;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                w[k] = dt == kBF16 ? f32_to_bf16(v[2 * k]) | (f32_to_bf16(v[2 * k + 1]) << 16)
+                w[k] = dt == kBF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                                         (nm_f32x2){v[2 * k], v[2 * k + 1]}, nm_bf16x2))
                                    : f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
             *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
         }
@@ -138,21 +148,27 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int width)
 
 // WG: the span belongs to the workgroup, otherwise to `team` lanes. vecs: vectors of a span.
 template <int NV, bool WG, bool VEC>
-__global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int team, int vecs,
-                                                    int sub, int64_t spans)
+__global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int per_row, int team,
+                                                    int vecs, int sub, int64_t spans)
 {
     __shared__ float part_f[16];
     __shared__ uint32_t part_u[16];
     constexpr bool EARLY = NV <= 2;  // z and the weights loaded with the rest (registers for four vectors do not reach)
     const int nt = blockDim.x;
     const int m = WG ? threadIdx.x : (threadIdx.x & (team - 1));
-    const int64_t s = WG ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * nt + threadIdx.x) / team;
+    // fewer than 2^32 threads: 32 bits
+    const uint32_t s = WG ? blockIdx.x : (blockIdx.x * (uint32_t)nt + threadIdx.x) / (uint32_t)team;
     // lanes past the last span keep their wave whole for the exchanges
     const bool live = s < spans;
-    const int per_row = p.columns / span;
-    const int64_t row = live ? s / per_row : 0;
-    const int64_t b = row / p.tokens, t = row - b * p.tokens;
-    const int c0 = live ? (int)(s - row * per_row) * span : 0;
+    const uint32_t row = !live ? 0 : per_row == 1 ? s : s / (uint32_t)per_row;
+    const uint32_t b32 = p.tokens == p.rows ? 0 : row / (uint32_t)p.tokens;
+    const int64_t b = b32, t = row - b32 * (uint32_t)p.tokens;
+    const int c0 = live ? (int)(s - row * (uint32_t)per_row) * span : 0;
+    const float inv_group = 1.0f / (float)p.group;
+    // of the weights: a span begins a group, and smaller groups are powers of two
+    auto weight_at = [&](int c) {
+        return p.weight_columns == p.columns ? c : p.group >= span ? c - c0 : (c - c0) & (p.group - 1);
+    };
 
     Raw8 rx[NV], rr[NV], rz[NV], rw[NV];
     int cols[NV];
@@ -171,7 +187,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             if (EARLY && p.z)
                 rz[j] = ld_raw8<VEC>(p.z, b * p.z_bs + t * p.z_ts + c, p.io_dtype, cols[j]);
             if (EARLY)
-                rw[j] = ld_raw8<VEC>(p.weight, p.weight_columns == p.columns ? c : c % p.group,
+                rw[j] = ld_raw8<VEC>(p.weight, weight_at(c),
                                      p.weight_dtype, cols[j]);
         }
     }
@@ -202,7 +218,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
                 cvt_raw8(rz[j], p.io_dtype, z);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    h[j][e] *= silu_f32(z[e]);
+                    h[j][e] *= gate_of(z[e]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -242,12 +258,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         most[j] = 0;
-        const float inv = 1.0f / sqrtf(sq[j] / (float)p.group + p.eps);
+        const float inv = __builtin_amdgcn_rsqf(sq[j] * inv_group + p.eps);
         if (cols[j] > 0) {
             float w[8], z[8];
             if (!EARLY) {
                 const int c = c0 + 8 * (m + (WG ? nt : team) * j);
-                rw[j] = ld_raw8<VEC>(p.weight, p.weight_columns == p.columns ? c : c % p.group,
+                rw[j] = ld_raw8<VEC>(p.weight, weight_at(c),
                                      p.weight_dtype, cols[j]);
                 if (p.z && !p.gate_first)
                     rz[j] = ld_raw8<VEC>(p.z, b * p.z_bs + t * p.z_ts + c, p.io_dtype, cols[j]);
@@ -259,7 +275,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             for (int e = 0; e < 8; ++e) {
                 float y = h[j][e] * inv * (p.unit_offset ? 1.0f + w[e] : w[e]);
                 if (p.z && !p.gate_first)
-                    y *= silu_f32(z[e]);
+                    y *= gate_of(z[e]);
                 h[j][e] = y;
                 const uint32_t mag = e < cols[j] ? __float_as_uint(y) & 0x7fffffffu : 0u;
                 most[j] = mag > most[j] ? mag : most[j];
@@ -306,8 +322,9 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             const float a = __uint_as_float(most[j]) / 448.0f;
             const float scale = a < 0x1p-126f ? 0x1p-126f : a;  // a NaN stays
             st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], 1.0f / scale, cols[j]);
-            if ((8 * i) % p.block == 0)
-                p.scales[row * (p.columns / p.block) + c / p.block] = scale;
+            const int in = p.block >= span ? 8 * i : (8 * i) & (p.block - 1);
+            if (in == 0)
+                p.scales[(int64_t)row * (p.columns / p.block) + c / p.block] = scale;
         }
 }
 
@@ -327,25 +344,40 @@ template <int NV, bool WG>
 hipError_t launch_norm_nv(const NormParams &p, int span, int team, int threads, hipStream_t stream)
 {
     const int64_t spans = p.rows * (p.columns / span);
-    const int vecs = (span + 7) / 8;
+    const int vecs = (span + 7) / 8, per_row = p.columns / span;
     const int sub = (p.out_dtype == kE4m3 ? min(p.group, p.block) : p.group) / 8;
     const __int128 groups = WG ? spans : ((__int128)spans * team + threads - 1) / threads;
     if (!launchable(groups, threads))
         return hipErrorInvalidConfiguration;
     if (norm_aligned(p, span))
-        norm_kernel<NV, WG, true><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, team, vecs,
+        norm_kernel<NV, WG, true><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, per_row, team, vecs,
                                                                                   sub, spans);
     else
-        norm_kernel<NV, WG, false><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, team, vecs,
+        norm_kernel<NV, WG, false><<<dim3((uint32_t)groups), threads, 0, stream>>>(p, span, per_row, team, vecs,
                                                                                    sub, spans);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_norm(const NormParams &p, hipStream_t stream)
+hipError_t launch_norm(const NormParams &given, hipStream_t stream)
 {
     (void)hipGetLastError();  // report only this launch's status
+    NormParams p = given;
+    if (p.rows > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    const int64_t n = p.tokens;
+    if (n == 1 || p.rows == n ||
+        (p.x_bs == n * p.x_ts && p.out_bs == n * p.out_ts && (!p.z || p.z_bs == n * p.z_ts) &&
+         (!p.residual || p.r_bs == n * p.r_ts))) {  // one row after the other: no batch
+        if (n == 1) {
+            p.x_ts = p.x_bs;
+            p.z_ts = p.z_bs;
+            p.r_ts = p.r_bs;
+            p.out_ts = p.out_bs;
+        }
+        p.tokens = (int32_t)p.rows;
+    }
     const int span = p.out_dtype == kE4m3 && p.block > p.group ? p.block : p.group;
     const int vecs = (span + 7) / 8;
     if (vecs <= 64) {
