@@ -158,6 +158,10 @@ struct LogitTile {
             const int i = at(lane, l, 0);
             if (VEC && i + VE <= left) {
                 w[l] = *reinterpret_cast<const u32x4 *>(p + i);
+            } else if (i + VE <= left) {
+                // 16 bytes at an element's alignment: global memory takes them in one access
+                typedef u32x4 Unaligned __attribute__((aligned(2)));
+                w[l] = *reinterpret_cast<const Unaligned *>(p + i);
             } else {
                 u32x4 r = {};
 #pragma unroll

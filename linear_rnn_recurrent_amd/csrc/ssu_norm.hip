@@ -33,6 +33,11 @@ struct Raw8 {
     u32x4 w[2];
 };
 
+// The same 16 bytes at an element's alignment: global memory takes them in one access
+typedef u32x4 Words4 __attribute__((aligned(4)));
+typedef u32x4 Halves8 __attribute__((aligned(2)));
+typedef u32x2 Bytes8 __attribute__((aligned(1)));
+
 template <bool VEC>
 __device__ __forceinline__ Raw8 ld_raw8(const void *p, int64_t i, int dt, int n)
 {
@@ -44,6 +49,14 @@ __device__ __forceinline__ Raw8 ld_raw8(const void *p, int64_t i, int dt, int n)
             r.w[1] = q[1];
         } else {
             r.w[0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+        }
+    } else if (n == 8) {
+        if (dt == kF32) {
+            const Words4 *q = reinterpret_cast<const Words4 *>(static_cast<const float *>(p) + i);
+            r.w[0] = q[0];
+            r.w[1] = q[1];
+        } else {
+            r.w[0] = *reinterpret_cast<const Halves8 *>(static_cast<const uint16_t *>(p) + i);
         }
     } else if (dt == kF32) {
 #pragma unroll
@@ -83,13 +96,18 @@ __device__ __forceinline__ void cvt_raw8(const Raw8 &r, int dt, float (&v)[8])
 template <bool VEC>
 __device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float (&v)[8], int n)
 {
-    if constexpr (VEC) {
+    if (VEC || n == 8) {
         if (dt == kF32) {
-            u32x4 *q = reinterpret_cast<u32x4 *>(static_cast<float *>(p) + i);
+            float *q = static_cast<float *>(p) + i;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                q[k] = u32x4{__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
-                             __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3])};
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 w = {__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                                 __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3])};
+                if constexpr (VEC)
+                    reinterpret_cast<u32x4 *>(q)[k] = w;
+                else
+                    reinterpret_cast<Words4 *>(q)[k] = w;
+            }
         } else {
             u32x4 w;
 #pragma unroll
@@ -97,7 +115,11 @@ __device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float 
                 w[k] = dt == kBF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(
                                          (nm_f32x2){v[2 * k], v[2 * k + 1]}, nm_bf16x2))
                                    : f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
+            uint16_t *q = static_cast<uint16_t *>(p) + i;
+            if constexpr (VEC)
+                *reinterpret_cast<u32x4 *>(q) = w;
+            else
+                *reinterpret_cast<Halves8 *>(q) = w;
         }
     } else {
 #pragma unroll
@@ -107,18 +129,31 @@ __device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float 
     }
 }
 
+// v / scale, given 1 / scale: a product and its remainder's, as a division rounds
+__device__ __forceinline__ float over(float v, float scale, float inv)
+{
+    const float q = v * inv;
+    const float fix = fmaf(fmaf(-q, scale, v), inv, q);
+    return fix == fix ? fix : q;  // infinite v or scale: their quotient as it came
+}
+
 template <bool VEC>
-__device__ __forceinline__ void st_e4m3(void *p, int64_t i, const float (&v)[8], float inv, int n)
+__device__ __forceinline__ void st_e4m3(void *p, int64_t i, const float (&v)[8], float scale, float inv,
+                                        int n)
 {
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k] * inv, v[4 * k + 1] * inv, 0, false);
-        w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k + 2] * inv, v[4 * k + 3] * inv, c, true);
+        const int c = __builtin_amdgcn_cvt_pk_fp8_f32(over(v[4 * k], scale, inv),
+                                                      over(v[4 * k + 1], scale, inv), 0, false);
+        w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(v[4 * k + 2], scale, inv),
+                                                         over(v[4 * k + 3], scale, inv), c, true);
     }
     uint8_t *q = static_cast<uint8_t *>(p) + i;
     if constexpr (VEC) {
         *reinterpret_cast<u32x2 *>(q) = u32x2{w[0], w[1]};
+    } else if (n == 8) {
+        *reinterpret_cast<Bytes8 *>(q) = u32x2{w[0], w[1]};
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -258,7 +293,11 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         most[j] = 0;
-        const float inv = __builtin_amdgcn_rsqf(sq[j] * inv_group + p.eps);
+        // a Newton step behind the hardware's root: codes flip where y is off by an ulp or two
+        const float mean = sq[j] * inv_group + p.eps;
+        float inv = __builtin_amdgcn_rsqf(mean);
+        const float half = 0.5f * inv;
+        inv = mean > 0x1p-100f && mean < 0x1p100f ? fmaf(half, fmaf(-mean * inv, inv, 1.0f), inv) : inv;
         if (cols[j] > 0) {
             float w[8], z[8];
             if (!EARLY) {
@@ -321,7 +360,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             const int i = m + (WG ? nt : team) * j, c = c0 + 8 * i;
             const float a = __uint_as_float(most[j]) / 448.0f;
             const float scale = a < 0x1p-126f ? 0x1p-126f : a;  // a NaN stays
-            st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], 1.0f / scale, cols[j]);
+            st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], scale, 1.0f / scale, cols[j]);
             const int in = p.block >= span ? 8 * i : (8 * i) & (p.block - 1);
             if (in == 0)
                 p.scales[(int64_t)row * (p.columns / p.block) + c / p.block] = scale;
@@ -386,13 +425,11 @@ hipError_t launch_norm(const NormParams &given, hipStream_t stream)
             team *= 2;
         return launch_norm_nv<1, false>(p, span, team, 256, stream);
     }
-    int threads = 64;
-    while (threads < 1024 && 2 * threads < vecs)
-        threads *= 2;
-    const int nv = (vecs + threads - 1) / threads;
-    if (nv <= 2)
-        return launch_norm_nv<2, true>(p, span, 0, threads, stream);
-    return launch_norm_nv<4, true>(p, span, 0, threads, stream);
+    // two vectors a thread, four where a workgroup's 1,024 threads do not reach
+    const int nv = vecs <= 2048 ? 2 : 4;
+    const int threads = ((vecs + nv - 1) / nv + 63) / 64 * 64;
+    return nv == 2 ? launch_norm_nv<2, true>(p, span, 0, threads, stream)
+                   : launch_norm_nv<4, true>(p, span, 0, threads, stream);
 }
 
 }  // namespace ssu
