@@ -579,13 +579,12 @@ ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const voi
  * out may be NULL when the state is updated (q is not read then and may be
  * NULL). out must not overlap an input (equal pointers are refused). Rows with
  * L_b == 0 leave the state untouched. The state is held in fp32 over the whole
- * call and rounded once, at its end. Long calls with fp16 or bf16 q, k, v and
- * out, 16-byte aligned rows of them and D in {64, 128} run the tokens in chunks
- * on the matrix cores: they agree with the token-by-token recurrence to fp32
- * rounding, not bitwise. A row of q or k whose sum of squares leaves fp32's
- * range is undefined. seq_len up to 2^30 and token strides up to 2^25 (else
- * SSU_ENOTSUP), and so is a call that needs 2^32 threads (a thread has eight
- * state entries of four or eight rows).
+ * call and rounded once, at its end. Long calls whose rows of q, k, v and out
+ * are 16-byte aligned run the tokens in chunks on the matrix cores: they agree
+ * with the token-by-token recurrence to fp32 rounding, not bitwise. A row of q
+ * or k whose sum of squares leaves fp32's range is undefined. seq_len up to
+ * 2^30 and token strides up to 2^25 (else SSU_ENOTSUP), and so is a call that
+ * needs 2^32 threads (a thread has 8 or 16 keys of two or four rows).
  * workspace: caller-owned device scratch of at least
  * ssu_delta_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
  * that is 0); contents on entry ignored, on return unspecified; calls sharing a

@@ -25,7 +25,7 @@ SOURCES = ["ssu_api.cpp", "ssu_decode.hip", "ssu_decode_f32.hip", "ssu_decode_f1
            "ssu_scan_rows.hip", "ssu_scan_prompt_f32.hip", "ssu_scan_prompt_f16.hip",
            "ssu_scan_prompt_bf16.hip", "ssu_verify.hip", "ssu_delta.hip", "ssu_delta_rows_f32.hip",
            "ssu_delta_rows_f16.hip", "ssu_delta_rows_bf16.hip",
-           "ssu_delta_chunks_f16.hip", "ssu_delta_chunks_bf16.hip", "ssu_norm.hip", "ssu_logprobs.hip",
+           "ssu_delta_chunks_f32.hip", "ssu_delta_chunks_f16.hip", "ssu_delta_chunks_bf16.hip", "ssu_norm.hip", "ssu_logprobs.hip",
            "ssu_pool_kernels.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -34,8 +34,8 @@ CFLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # With one wave a SIMD the compiler would put matrix-core accumulators into the
 # accumulation registers and copy every one of them for the vector ALU
-MORE = {"ssu_delta_chunks_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-        "ssu_delta_chunks_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+MORE = {f"ssu_delta_chunks_{t}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+        for t in ("f32", "f16", "bf16")}
 
 
 def _compile(src, extra, verbose):

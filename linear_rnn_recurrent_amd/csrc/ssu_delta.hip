@@ -2,7 +2,7 @@
 //   S <- alpha S;  u = beta (v - S k);  S <- S + u k^T;  o = scale S q
 //
 // Two evaluations, by the sizes (delta_plan): token by token (ssu_delta_rows.h; single
-// tokens, windows, what the matrix cores do not take) and in chunks of 64
+// tokens, windows, unaligned rows) and in chunks of 64 or 32
 // tokens on the matrix cores (ssu_delta_chunks.h; prompts).
 #include "ssu_delta_impl.h"
 
@@ -11,12 +11,16 @@ namespace ssu {
 hipError_t launch_delta_rows_f32(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_rows_f16(const DeltaParams &p, hipStream_t stream);
 hipError_t launch_delta_rows_bf16(const DeltaParams &p, hipStream_t stream);
+hipError_t launch_delta_chunks_f32(const DeltaParams &p, const DeltaPlan &plan, hipStream_t stream);
 hipError_t launch_delta_chunks_f16(const DeltaParams &p, const DeltaPlan &plan, hipStream_t stream);
 hipError_t launch_delta_chunks_bf16(const DeltaParams &p, const DeltaPlan &plan, hipStream_t stream);
 
 namespace {
 
-constexpr int kDeltaLeast = 32;                      // tokens from which chunks are taken
+// Tokens from which chunks are taken: a single chunk takes 19 us of one row of 32 heads of
+// 128, 43 of 16 rows, 135 of 64; token by token 16 of them take 16, 44 and 134 us, 31 take 28, 72
+// and 250.
+constexpr int kDeltaLeast = 18;
 constexpr int64_t kDeltaSegment = (int64_t)96 << 20;  // bytes handed over at a time
 
 }  // namespace
@@ -24,20 +28,23 @@ constexpr int64_t kDeltaSegment = (int64_t)96 << 20;  // bytes handed over at a 
 DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len, int32_t io_dtype)
 {
     DeltaPlan q = {};
-    if (batch <= 0 || batch > 65535 || seq_len < kDeltaLeast || io_dtype == kF32 || (d != 64 && d != 128))
+    if (batch <= 0 || batch > 65535 || seq_len < kDeltaLeast)
         return q;
-    q.chunks = (int32_t)((seq_len + 63) / 64);
-    const int64_t kq = batch * hq * 256 * d, head = batch * hv * kDeltaHeadBytes;
+    const bool f32 = io_dtype == kF32;
+    const int tiles = delta_tiles(d, f32);
+    q.spans = (int32_t)((seq_len + 63) / 64);
+    const int64_t kq = batch * hq * 256 * d * (f32 ? 2 : 1);
+    const int64_t head = batch * hv * (4 / tiles) * delta_head_bytes(tiles);
     int64_t segment = kDeltaSegment / (kq + head);
-    segment = segment < 1 ? 1 : segment > q.chunks ? q.chunks : segment;
+    segment = segment < 1 ? 1 : segment > q.spans ? q.spans : segment;
     q.segment = (int32_t)segment;
     // Workgroups of 64 value columns run a chunk faster, those of all 128 leave more
     // waves a CU to hide each other's waits: 199 against 232 us at 256 of the former (4 x
     // 2048 tokens, 32 heads of 128), 814 against 686 at 512 (8 x 4096).
-    q.wide = d > 64 && batch * hv * (d / 64) > 256;
+    q.wide = batch * hv * d > 256 * 64;
     q.kq_bytes = kq * segment;
     q.head_bytes = head * segment;
-    q.carry_bytes = segment < q.chunks ? 4 * batch * hv * d * d : 0;
+    q.carry_bytes = segment < q.spans ? 4 * batch * hv * d * d : 0;
     return q;
 }
 
@@ -45,16 +52,20 @@ int64_t delta_workspace_bytes(int64_t batch, int64_t hq, int64_t hv, int64_t d, 
                               int32_t io_dtype)
 {
     const DeltaPlan q = delta_plan(batch, hq, hv, d, seq_len, io_dtype);
-    return q.chunks ? q.kq_bytes + q.head_bytes + q.carry_bytes : 0;
+    return q.spans ? q.kq_bytes + q.head_bytes + q.carry_bytes : 0;
 }
 
 hipError_t launch_delta(const DeltaParams &p, hipStream_t stream)
 {
     (void)hipGetLastError();  // report only this launch's status
     const DeltaPlan q = delta_plan(p.batch, p.hq, p.hv, p.d, p.seq_len, p.io_dtype);
-    if (q.chunks && p.workspace && delta_rows_aligned(p, 16, true))
-        return p.io_dtype == kF16 ? launch_delta_chunks_f16(p, q, stream)
-                                  : launch_delta_chunks_bf16(p, q, stream);
+    if (q.spans && p.workspace && delta_rows_aligned(p, 16, true)) {
+        switch (p.io_dtype) {
+        case kF32: return launch_delta_chunks_f32(p, q, stream);
+        case kF16: return launch_delta_chunks_f16(p, q, stream);
+        default: return launch_delta_chunks_bf16(p, q, stream);
+        }
+    }
     switch (p.io_dtype) {
     case kF32: return launch_delta_rows_f32(p, stream);
     case kF16: return launch_delta_rows_f16(p, stream);

@@ -77,8 +77,8 @@ def test_windows(io, d, seq_len):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("seq_len", [63, 64, 65, 128, 200, 331])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("seq_len", [18, 31, 32, 33, 63, 64, 65, 97, 200, 331])
 def test_prompts(io, d, seq_len):
     verify(delta_inputs(5, batch=2, seq_len=seq_len, d=d, io=io))
 
@@ -89,8 +89,8 @@ def test_prompts_with_16_bit_states(d, st):
     verify(delta_inputs(6, batch=2, seq_len=150, d=d, st=st, gate="bf16"))
 
 
-@pytest.mark.parametrize("io", ["bf16", "f16"])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
 def test_uneven_prompts(io, d):
     """Lengths from none to past the end, a padding row, NaN in every place that is not read, and
     zeros behind the ends."""
@@ -114,7 +114,7 @@ def test_uneven_prompts(io, d):
         check(T["state"][r], state[r], sbound[r], torch.float32, "state")
 
 
-@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("l2", [True, False])
 @pytest.mark.parametrize("seq_len", [3, 140])
 def test_given_decays_and_betas(io, l2, seq_len):
@@ -168,12 +168,12 @@ def test_decays(seq_len, kind):
     verify(T)
 
 
-@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("io", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("seq_len", [2, 130])
 @pytest.mark.parametrize("size", [1e-6, 1e4])
 def test_small_and_large_values(io, seq_len, size):
     T = delta_inputs(12, batch=2, seq_len=seq_len, d=64, io=io)
-    if io == "bf16" or size < 1:
+    if io != "f16" or size < 1:
         T["v"] = (T["v"].float() * size).to(DT[io])
     T["state"] *= size
     T["k"][:, ::3] *= 0.01
@@ -192,7 +192,8 @@ def test_equal_keys(seq_len):
     verify(T)
 
 
-@pytest.mark.parametrize("io,seq_len,at", [("bf16", 150, 77), ("f16", 150, 64), ("bf16", 150, 127), ("bf16", 5, 2)])
+@pytest.mark.parametrize("io,seq_len,at", [("bf16", 150, 77), ("f16", 150, 64), ("bf16", 150, 127), ("bf16", 5, 2),
+                                           ("f32", 150, 77)])
 @pytest.mark.parametrize("where", ["q", "k", "v", "a", "b"])
 def test_a_nan_reaches_no_earlier_token_and_no_other_row(io, seq_len, at, where):
     T = delta_inputs(14, batch=2, seq_len=seq_len, d=64, io=io)
@@ -249,6 +250,25 @@ def test_prompt_as_two_prompts():
     call(second)
     d = (T["state"] - whole["state"]).norm() / whole["state"].norm()
     assert d <= 2 * (8 + 4 * np.sqrt(192 * 300)) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("io,d", [("bf16", 128), ("f32", 64)])
+def test_many_rows_as_rows_alone(io, d):
+    """So many that their chunks are handed over in several segments and that a workgroup takes
+    a whole head: as each row by itself, up to the rounding of either."""
+    batch, seq_len, hq, hv = 24, 420, 8, 16
+    ctx = [seq_len - 17 * (i % 5) - (400 if i == 7 else 0) for i in range(batch)]
+    T = delta_inputs(24, batch=batch, seq_len=seq_len, hq=hq, hv=hv, d=d, io=io, ctx=ctx)
+    rows = {**T, "state": T["state"].clone()}
+    y = call(T)
+    for i in (0, 7, 23):
+        one = {n: (t[i:i + 1] if n in ("q", "k", "v", "a", "b", "idx", "ctx") else t) for n, t in rows.items()}
+        want = call(one)
+        n = max(ctx[i], 0)  # row 7 has none
+        lim = 2 * (8 + 4 * np.sqrt((d + 64) * n)) * 2.0 ** -24
+        assert norm_error(y[i].float(), f64(want[0].float())) <= lim + (2 * 2.0 ** -9 if io == "bf16" else 0.0)
+        r = int(T["idx"][i])
+        assert norm_error(T["state"][r], f64(rows["state"][r])) <= lim
 
 
 def test_same_state_in_several_windows():
