@@ -99,19 +99,34 @@ struct Top {
     Key key;
     Key last;  // entry k - 1, the same in every lane
 
-    // the first n candidates of lds
-    __device__ void take(TopLds &lds, int n, int k, int lane)
+    // the first n candidates of lds, of which those below `bound` (k logits reach it) are out
+    __device__ void take(TopLds &lds, int n, float bound, int k, int lane)
     {
+        const Key least = (Key)order_of(bound) << 32;
+        int left = 0;
+        for (int i = 0; i < n; i += 64) {
+            wave_lds_fence();
+            const Key x = i + lane < n ? lds.got[i + lane] : 0;
+            const bool in = x >= least && x > last;
+            const uint64_t mask = __ballot(in);
+            wave_lds_fence();
+            if (in)
+                lds.got[left + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                              __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = x;
+            left += __popcll(mask);
+        }
         wave_lds_fence();
-        for (int i = 0; i < n; i += 64 - k) {
-            const int more = min(n - i, 64 - k);
-            Key x = lane < k ? key : 0;
-            if (lane >= k && lane < k + more)
-                x = lds.got[i + lane - k];
-            if (!__ballot(lane >= k && x > last))
+        for (int i = 0; i < left;) {
+            const int have = __ballot(lane < k && key != 0) ? k : 0;  // entries of the list
+            const int more = min(left - i, 64 - have);
+            Key x = lane < have ? key : 0;
+            if (lane >= have && lane < have + more)
+                x = lds.got[i + lane - have];
+            i += more;
+            if (!__ballot(lane >= have && x > last))
                 continue;
             int rank = 0;
-            for (int j = 0; j < k + more; ++j)
+            for (int j = 0; j < have + more; ++j)
                 rank += lane_key(x, j) > x ? 1 : 0;
             if (lane < k)
                 lds.list[lane] = 0;
@@ -239,7 +254,7 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
             most = fmaxf(most, m);
             bound = fmaxf(bound, kth_of_lanes(most, k));
             if (n > kGather) {
-                top.take(lds, n, k, lane);
+                top.take(lds, n, bound, k, lane);
                 n = 0;
                 full = top.last ? logit_of(top.last) : __builtin_nanf("");
             }
@@ -251,7 +266,9 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
                     const bool may = v >= bound && !(v <= full);
                     if (__ballot(may)) {
                         const int at = Tile::at(lane, l, e);
-                        const bool in = may && at < left;
+                        // of what a mask left out only the first k logits count: nothing is
+                        // below it, and they come first
+                        const bool in = may && at < left && (v > neg_inf() || (base == begin && at < k));
                         const uint64_t mask = __ballot(in);
                         if (in)
                             lds.got[n + (int)__builtin_amdgcn_mbcnt_hi(
@@ -263,7 +280,7 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
         }
     }
     if (n > 0)
-        top.take(lds, n, k, lane);
+        top.take(lds, n, bound, k, lane);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         Sums b;
