@@ -2,8 +2,8 @@
 //   S <- alpha S;  u = beta (v - S k);  S <- S + u k^T;  o = scale S q
 //
 // Two evaluations, by the sizes (delta_plan): token by token (ssu_delta_rows.h; single
-// tokens, windows, unaligned rows) and in chunks of 64 or 32
-// tokens on the matrix cores (ssu_delta_chunks.h; prompts).
+// tokens, windows, unaligned rows) and in chunks of 64 or 32 tokens on the matrix cores
+// (ssu_delta_chunks.h; prompts).
 #include "ssu_delta_impl.h"
 
 namespace ssu {
@@ -21,7 +21,9 @@ namespace {
 // 128, 43 of 16 rows, 135 of 64; token by token 16 of them take 16, 44 and 134 us, 31 take 28, 72
 // and 250.
 constexpr int kDeltaLeast = 18;
-constexpr int64_t kDeltaSegment = (int64_t)96 << 20;  // bytes handed over at a time
+// Bytes handed over at a time: 8 x 4096 tokens of 32 heads take 814 us by 48 MiB, 672 by
+// 96, 601 by 192, 583 by 400, 564 at once (3.4 GB): each segment fills and drains the GPU twice.
+constexpr int64_t kDeltaSegment = (int64_t)256 << 20;
 
 }  // namespace
 
@@ -36,11 +38,13 @@ DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t s
     const int64_t kq = batch * hq * 256 * d * (f32 ? 2 : 1);
     const int64_t head = batch * hv * (4 / tiles) * delta_head_bytes(tiles);
     int64_t segment = kDeltaSegment / (kq + head);
-    segment = segment < 1 ? 1 : segment > q.spans ? q.spans : segment;
+    segment = segment < 1 ? 1 : segment;
+    const int64_t parts = (q.spans + segment - 1) / segment;
+    segment = (q.spans + parts - 1) / parts;  // of like sizes
     q.segment = (int32_t)segment;
-    // Workgroups of 64 value columns run a chunk faster, those of all 128 leave more
-    // waves a CU to hide each other's waits: 199 against 232 us at 256 of the former (4 x
-    // 2048 tokens, 32 heads of 128), 814 against 686 at 512 (8 x 4096).
+    // Workgroups of 64 value columns, as long as each has a CU to itself, run a chunk faster;
+    // beyond, those of 128 fetch a chunk for eight waves: 169 against 206 us at 256 of the former (4
+    // x 2048 tokens, 32 heads of 128), 283 against 221 at 320, 347 against 297 at 512.
     q.wide = batch * hv * d > 256 * 64;
     q.kq_bytes = kq * segment;
     q.head_bytes = head * segment;

@@ -232,6 +232,20 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
     if (n == 0)
         return;
 
+    // a and b of the first heads, a head a wave, lane = token: in flight with k and q
+    float lg = 0.0f, beta = 0.0f;
+    auto gates_of = [&](int head) {
+        lg = beta = 0.0f;
+        if (head < G && lane < n) {
+            const int h = j * G + head;
+            const int64_t t = t0 + lane;
+            const float A = p.A_log ? -expf(p.A_log[h]) : 0.0f;
+            const float bias = p.dt_bias ? ld_io(p.dt_bias, h, p.bias_dtype) : 0.0f;
+            lg = delta_log_decay(p, A, bias, ld_io(p.a, b * p.a_bs + t * p.a_ts + h, p.gate_dtype));
+            beta = delta_beta(p, ld_io(p.b, b * p.b_bs + t * p.b_ts + h, p.gate_dtype));
+        }
+    };
+
     // k and q of tile `wave`: lengths, fp16
     {
         const int tok = 16 * wave + c;
@@ -250,6 +264,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
                         raw[1][ks][x] = reinterpret_cast<const u32x4 *>(qp + 32 * ks)[x];
                 }
             }
+        gates_of(wave);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float v[KS][8], sum = 0.0f;
@@ -313,9 +328,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
                 *reinterpret_cast<u32x4 *>(to + Sh::KQ / 2) = *reinterpret_cast<const u32x4 *>(lds.q[x] + o);
         }
 
-    // K_s . K_t of the row tile `wave`, K_s . Q_t of the row tile that has as many columns less
-    // (NT + 1 tiles a wave): column t of the tile, rows s. i, ip: the row tiles within their chunk
-    const int sub = wave / NT, i0 = sub * NT, i = wave - i0, ip = NT - 1 - i;
+    // K_s . K_t and K_s . Q_t of the row tile `wave`: column t of the tile, rows s. L and P share
+    // their decays, which weighs more than that the last tile's wave has the most columns.
+    // i: the row tile within its chunk
+    const int sub = wave / NT, i0 = sub * NT, i = wave - i0;
     dc_f32x4 kk[NT], qk[NT];
     auto dot = [&](const unsigned char *a0, const unsigned char *a1, int at, const unsigned char *b0,
                    const unsigned char *b1, int bt, dc_f32x4 x) {
@@ -333,24 +349,19 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         kk[t] = qk[t] = dc_f32x4{0, 0, 0, 0};
-        if (t <= i)
+        if (t <= i) {
             kk[t] = dot(lds.k[0], lds.k[PL - 1], i0 + t, lds.k[0], lds.k[PL - 1], i0 + i, kk[t]);
-        if (p.out && t <= ip)
-            qk[t] = dot(lds.k[0], lds.k[PL - 1], i0 + t, lds.q[0], lds.q[PL - 1], i0 + ip, qk[t]);
+            if (p.out)
+                qk[t] = dot(lds.k[0], lds.k[PL - 1], i0 + t, lds.q[0], lds.q[PL - 1], i0 + i, qk[t]);
+        }
     }
 
     for (int h0 = 0; h0 < G; h0 += 4) {
         if (h0 + wave < G) {  // gates of four heads at once, lane = token
             const int h = j * G + h0 + wave;
             const bool in = lane < n;
-            float lg = 0.0f, beta = 0.0f;
-            if (in) {
-                const float A = p.A_log ? -expf(p.A_log[h]) : 0.0f;
-                const float bias = p.dt_bias ? ld_io(p.dt_bias, h, p.bias_dtype) : 0.0f;
-                const int64_t t = t0 + lane;
-                lg = delta_log_decay(p, A, bias, ld_io(p.a, b * p.a_bs + t * p.a_ts + h, p.gate_dtype));
-                beta = delta_beta(p, ld_io(p.b, b * p.b_bs + t * p.b_ts + h, p.gate_dtype));
-            }
+            if (h0 > 0)
+                gates_of(h0 + wave);
             const float ks = lds.ks[lane], qs = lds.qs[lane], kk2 = lds.kk[lane];
             const bool bad = in && !(lg <= 0.0f && kk2 <= 1.07f && fabsf(beta) * kk2 <= 2.1f &&
                                      (!p.out || lds.qq[lane] < __builtin_inff()));
@@ -395,90 +406,92 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
         for (int hh = 0; hh < 4 && h0 + hh < G; ++hh) {
             const DcGates &s = lds.gates[hh];
             unsigned char *to = w.head + ((at + sub) * p.hv + j * G + h0 + hh) * Sh::HEAD;
-            // both kinds of tiles: L of row tile i, P of row tile ip
-#pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-                if (kind == 1 && !p.out)
-                    break;
-                const int r0 = kind ? ip : i;
-                const int t = 16 * (i0 + r0) + c;
-                const float own = kind ? 1.0f : s.beta[t];
-                const float front = -own * s.row[t];  // L is stored with its sign in U's recursion
-#pragma unroll
-                for (int jt = 0; jt < NT - 1; ++jt) {
-                    if (jt >= r0)
-                        break;
-                    float mid = 0.0f;
-                    for (int m = jt + 1; m < r0; ++m)
-                        mid += s.total[i0 + m];
-                    const float f = (kind ? -front : front) * expf(mid);
-                    const dc_f32x4 tail = *reinterpret_cast<const dc_f32x4 *>(&s.tail[16 * (i0 + jt) + 4 * g]);
-                    dc_f32x4 v;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = f * ((kind ? qk[jt][r] : kk[jt][r]) * tail[r]);
-                    u32x2 hi, lo;
-                    dc_split(v, hi, lo);
-                    unsigned char *at8 = to + (kind ? Sh::p_pair(r0, jt >> 1) : Sh::l_pair(r0, jt >> 1)) + lane * 16 + 8 * (jt & 1);
-                    *reinterpret_cast<u32x2 *>(at8) = hi;
-                    *reinterpret_cast<u32x2 *>(at8 + kDcTile) = lo;
-                }
-                // diagonal tile: decays behind s through t by adding from t downwards
-                float sum = 0.0f;
-                dc_f32x4 dl = {0, 0, 0, 0};
-                for (int m = 15; m >= 1; --m) {
-                    sum += m <= c ? s.log[16 * (i0 + r0) + m] : 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        dl[r] = 4 * g + r == m - 1 ? sum : dl[r];
-                }
-                dc_f32x4 v;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int ss = 4 * g + r;
-                    float x = kind ? qk[NT - 1][r] : kk[NT - 1][r];
-#pragma unroll
-                    for (int q = 0; q < NT - 1; ++q)
-                        x = r0 == q ? (kind ? qk[q][r] : kk[q][r]) : x;
-                    const float d = expf(dl[r]) * lds.ks[16 * (i0 + r0) + ss] * own * x;
-                    v[r] = ss < c || (kind && ss == c) ? d : 0.0f;
-                }
-                if (kind == 0) {
-                    float *tile = lds.diag[wave];
-                    __builtin_amdgcn_wave_barrier();
-                    *reinterpret_cast<dc_f32x4 *>(tile + c * 20 + 4 * g) = v;
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-                    float L[16];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const dc_f32x4 x = *reinterpret_cast<const dc_f32x4 *>(tile + c * 20 + 4 * q);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            L[4 * q + r] = x[r];
-                    }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = 4 * g + r == c ? 1.0f : 0.0f;
-                    dc_invert<0>(L, v);
-                }
+            const int t = 16 * (i0 + i) + c;
+            const float own = s.beta[t], row = s.row[t];
+            // a tile of L (with its sign in U's recursion) and one of P from their common factors
+            auto put = [&](unsigned char *at8, const dc_f32x4 &v) {
                 u32x2 hi, lo;
                 dc_split(v, hi, lo);
-                if (kind == 0) {
-                    *reinterpret_cast<u32x4 *>(to + r0 * kDcTile + lane * 16) = u32x4{hi[0], hi[1], lo[0], lo[1]};
-                    if (r0 & 1) {  // the second tile of this row's last pair
-                        unsigned char *at8 = to + Sh::l_pair(r0, r0 >> 1) + lane * 16 + 8;
-                        *reinterpret_cast<u32x2 *>(at8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile) = u32x2{0, 0};
-                    }
-                } else {
-                    unsigned char *at8 = to + Sh::p_pair(r0, r0 >> 1) + lane * 16 + 8 * (r0 & 1);
-                    *reinterpret_cast<u32x2 *>(at8) = hi;
-                    *reinterpret_cast<u32x2 *>(at8 + kDcTile) = lo;
-                    if (!(r0 & 1))
-                        *reinterpret_cast<u32x2 *>(at8 + 8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile + 8) = u32x2{0, 0};
+                *reinterpret_cast<u32x2 *>(at8) = hi;
+                *reinterpret_cast<u32x2 *>(at8 + kDcTile) = lo;
+            };
+#pragma unroll
+            for (int jt = 0; jt < NT - 1; ++jt) {
+                if (jt >= i)
+                    break;
+                float mid = 0.0f;
+                for (int m = jt + 1; m < i; ++m)
+                    mid += s.total[i0 + m];
+                const float f = row * expf(mid);
+                const dc_f32x4 tail = *reinterpret_cast<const dc_f32x4 *>(&s.tail[16 * (i0 + jt) + 4 * g]) * f;
+                put(to + Sh::l_pair(i, jt >> 1) + lane * 16 + 8 * (jt & 1), tail * kk[jt] * -own);
+                if (p.out)
+                    put(to + Sh::p_pair(i, jt >> 1) + lane * 16 + 8 * (jt & 1), tail * qk[jt]);
+            }
+            // diagonal tile: decays behind s through t by adding from t downwards
+            float logs[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const dc_f32x4 x = *reinterpret_cast<const dc_f32x4 *>(&s.log[16 * (i0 + i) + 4 * q]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    logs[4 * q + r] = x[r];
+            }
+            float sum = 0.0f;
+            dc_f32x4 dl = {0, 0, 0, 0};
+#pragma unroll
+            for (int m = 15; m >= 1; --m) {
+                sum += m <= c ? logs[m] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if ((m - 1) % 4 == r)
+                        dl[r] = g == (m - 1) / 4 ? sum : dl[r];
+            }
+            const dc_f32x4 ks = *reinterpret_cast<const dc_f32x4 *>(&lds.ks[16 * (i0 + i) + 4 * g]);
+            dc_f32x4 x = kk[NT - 1], y = qk[NT - 1];
+#pragma unroll
+            for (int q = 0; q < NT - 1; ++q)
+                if (i == q) {
+                    x = kk[q];
+                    y = qk[q];
                 }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float d = expf(dl[r]) * ks[r];
+                x[r] = 4 * g + r < c ? d * own * x[r] : 0.0f;
+                y[r] = 4 * g + r <= c ? d * y[r] : 0.0f;
+            }
+            if (p.out) {
+                unsigned char *at8 = to + Sh::p_pair(i, i >> 1) + lane * 16 + 8 * (i & 1);
+                put(at8, y);
+                if (!(i & 1))
+                    *reinterpret_cast<u32x2 *>(at8 + 8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile + 8) = u32x2{0, 0};
+            }
+            float *tile = lds.diag[wave];
+            __builtin_amdgcn_wave_barrier();
+            *reinterpret_cast<dc_f32x4 *>(tile + c * 20 + 4 * g) = x;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            float L[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const dc_f32x4 z = *reinterpret_cast<const dc_f32x4 *>(tile + c * 20 + 4 * q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    L[4 * q + r] = z[r];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[r] = 4 * g + r == c ? 1.0f : 0.0f;
+            dc_invert<0>(L, x);
+            u32x2 hi, lo;
+            dc_split(x, hi, lo);
+            *reinterpret_cast<u32x4 *>(to + i * kDcTile + lane * 16) = u32x4{hi[0], hi[1], lo[0], lo[1]};
+            if (i & 1) {  // the second tile of this row's last pair
+                unsigned char *at8 = to + Sh::l_pair(i, i >> 1) + lane * 16 + 8;
+                *reinterpret_cast<u32x2 *>(at8) = *reinterpret_cast<u32x2 *>(at8 + kDcTile) = u32x2{0, 0};
             }
         }
         __syncthreads();

@@ -174,9 +174,8 @@ int64_t delta_workspace_bytes(int64_t batch, int64_t hq, int64_t hv, int64_t d, 
                               int32_t io_dtype);
 hipError_t launch_delta(const DeltaParams &p, hipStream_t stream);
 // The evaluation in chunks of 16 delta_tiles() tokens: spans of 64 tokens, those of one
-// segment (prep and sweep follow each other by segments, so that what is handed over stays
-// in the last-level cache), whether a workgroup takes all of a head, bytes of the
-// workspace's parts. spans == 0: token by token.
+// segment (prep and sweep follow each other by segments, which bounds the workspace),
+// whether a workgroup takes all of a head, bytes of the workspace's parts. spans == 0: token by token.
 constexpr int delta_tiles(int64_t d, bool f32) { return f32 || d > 128 ? 2 : 4; }
 constexpr int delta_head_bytes(int tiles) { return (tiles == 4 ? 26 : 9) * 1024; }  // of a chunk
 struct DeltaPlan {

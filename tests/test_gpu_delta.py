@@ -271,6 +271,27 @@ def test_many_rows_as_rows_alone(io, d):
         assert norm_error(T["state"][r], f64(rows["state"][r])) <= lim
 
 
+@pytest.mark.parametrize("io,d,hq,hv", [("bf16", 128, 16, 32), ("f32", 64, 16, 32), ("f32", 256, 8, 16)])
+def test_rows_in_several_segments(io, d, hq, hv):
+    """A workspace that holds a part of the chunks at a time: as each row by itself, which fits."""
+    batch, seq_len = 40, 420
+    ctx = [seq_len - 61 * (i % 4) - (300 if i == 39 else 0) for i in range(batch)]
+    T = delta_inputs(25, batch=batch, seq_len=seq_len, hq=hq, hv=hv, d=d, io=io, ctx=ctx)
+    io_dtype = T["q"].dtype
+    carry = 4 * batch * hv * d * d  # the states between segments, which a whole row's does not have
+    assert (L.delta_workspace_bytes(batch, seq_len, hq, hv, d, io_dtype) - carry
+            < 0.9 * L.delta_workspace_bytes(1, seq_len, hq, hv, d, io_dtype) * batch)
+    rows = {**T, "state": T["state"].clone()}
+    y = call(T)
+    for i in (0, 17, 39):
+        one = {n: (t[i:i + 1] if n in ("q", "k", "v", "a", "b", "idx", "ctx") else t) for n, t in rows.items()}
+        want = call(one)
+        lim = 2 * (8 + 4 * np.sqrt((d + 64) * max(ctx[i], 0))) * 2.0 ** -24
+        assert norm_error(y[i].float(), f64(want[0].float())) <= lim + (2 * 2.0 ** -9 if io == "bf16" else 0.0)
+        r = int(T["idx"][i])
+        assert norm_error(T["state"][r], f64(rows["state"][r])) <= lim
+
+
 def test_same_state_in_several_windows():
     T = delta_inputs(19, batch=3, seq_len=4, d=64)
     T["idx"][:] = 1
