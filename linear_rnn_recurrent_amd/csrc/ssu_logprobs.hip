@@ -57,6 +57,25 @@ __device__ __forceinline__ Sums join(Sums a, Sums b)
     return {m, a.s + b.s, a.t + b.t};
 }
 
+// Of a wave: the lanes' maximum first, so that each lane rescales once
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, dpp_f32<0xB1>(v));   // quad_perm [1,0,3,2]
+    v = fmaxf(v, dpp_f32<0x4E>(v));   // quad_perm [2,3,0,1]
+    v = fmaxf(v, dpp_f32<0x141>(v));  // row_half_mirror
+    v = fmaxf(v, dpp_f32<0x140>(v));  // row_mirror
+    const int u = __builtin_bit_cast(int, v);
+    return fmaxf(fmaxf(__builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 0)),
+                       __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 16))),
+                 fmaxf(__builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 32)),
+                       __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 48))));
+}
+__device__ __forceinline__ Sums wave_join(Sums a)
+{
+    rescale(a, wave_max(a.m));
+    return {a.m, wave_sum(a.s), wave_sum(a.t)};
+}
+
 // Bits that order as the values do (-0 as 0)
 __device__ __forceinline__ uint32_t order_of(float x)
 {
@@ -67,6 +86,7 @@ __device__ __forceinline__ float of_order(uint32_t o)
 {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+__device__ __forceinline__ float next_above(float x) { return of_order(order_of(x) + 1); }
 
 // A logit and its index as one number, the larger the better; 0: none.
 typedef uint64_t Key;
@@ -215,6 +235,8 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
         next.template load<VEC>(row + begin, end - begin, lane);
     float most = neg_inf();   // of the lane, over all tiles
     float bound = neg_inf();  // at least k logits reach it
+    // above a full list's last entry: an equal logit of a later tile comes behind it
+    float above = neg_inf();
     int n = 0;                // candidates gathered
     for (int64_t base = begin; base < end; base += (int64_t)step * N) {
         const Tile cur = next;
@@ -248,22 +270,21 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
             sums.s += p;
             sums.t += p * fmaxf(d, kFloor);
         }
-        // a full list's last entry: an equal logit of a later tile comes behind it
-        float full = top.last ? logit_of(top.last) : __builtin_nanf("");
-        if (k > 0 && __ballot(m >= bound && !(m <= full))) {
+        if (k > 0 && __ballot(m >= fmaxf(bound, above))) {
             most = fmaxf(most, m);
             bound = fmaxf(bound, kth_of_lanes(most, k));
             if (n > kGather) {
                 top.take(lds, n, bound, k, lane);
                 n = 0;
-                full = top.last ? logit_of(top.last) : __builtin_nanf("");
+                above = top.last ? next_above(logit_of(top.last)) : neg_inf();
             }
+            const float least = fmaxf(bound, above);
 #pragma unroll
             for (int l = 0; l < Tile::NL; ++l)
 #pragma unroll
                 for (int e = 0; e < Tile::VE; ++e) {
                     const float v = x[l * Tile::VE + e];
-                    const bool may = v >= bound && !(v <= full);
+                    const bool may = v >= least;
                     if (__ballot(may)) {
                         const int at = Tile::at(lane, l, e);
                         // of what a mask left out only the first k logits count: nothing is
@@ -281,14 +302,7 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
     }
     if (n > 0)
         top.take(lds, n, bound, k, lane);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        Sums b;
-        b.m = __shfl_xor(sums.m, o, 64);
-        b.s = __shfl_xor(sums.s, o, 64);
-        b.t = __shfl_xor(sums.t, o, 64);
-        sums = join(sums, b);
-    }
+    sums = wave_join(sums);
 }
 
 __device__ __forceinline__ bool row_live(const LogprobParams &p, int row)
@@ -473,14 +487,7 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p, int
         place_lists(lists, parts, p.top, got, gathered, best);
     if (!first)
         return;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        Sums s;
-        s.m = __shfl_xor(a.m, o, 64);
-        s.s = __shfl_xor(a.s, o, 64);
-        s.t = __shfl_xor(a.t, o, 64);
-        a = join(a, s);
-    }
+    a = wave_join(a);
     write_row(p, row, given, a, lane < p.top ? best[lane] : 0, lane);
 }
 
