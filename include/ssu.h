@@ -598,8 +598,12 @@ ssu_status ssu_delta_prefill(const ssu_delta_dims *dims, int32_t seq_len, const 
 
 /* Bytes of workspace ssu_delta_prefill needs for exactly this batch, heads,
  * head_dim, io_dtype and seq_len (nothing else in dims counts); 0 where the
- * tokens run one by one. -1 if dims is NULL or the call refuses one of these.
- * No HIP call. */
+ * tokens run one by one. It stays below 2^28 and a state in fp32 a row (or one
+ * stretch of 64 tokens of every row, where that is more), and a larger size may need
+ * less than a smaller one (32 heads of 128: 88 MB at 1 x 4096, 259 MB at 8 x
+ * 4096, 193 MB at 8 x 2048): a workspace kept for several has the largest of their
+ * sizes, each of them asked for. -1 if dims is NULL or the call refuses one of
+ * these. No HIP call. */
 int64_t ssu_delta_workspace_bytes(const ssu_delta_dims *dims, int32_t seq_len);
 
 /* ------------------------------------------------------------------------

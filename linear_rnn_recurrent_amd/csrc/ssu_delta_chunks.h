@@ -12,19 +12,24 @@
 // needs nothing of the others, so there is no exchange between waves; U comes
 // tile after tile (U_i = (I + L_ii)^-1 (X_i - sum_{j<i} L_ij U_j)).
 //
-// Precision: v_mfma_f32_16x16x32_f16 throughout, fp32 sums. k and q of 16 bits, scaled by a
-// power of two to a length in [1, 2), are fp16 exactly but for what lies 2^-25 below
-// that length; of fp32 they are pairs of fp16 as well. L, P, the inverses, X, U and the state are pairs of fp16, hi +
-// lo, 22 bits: their products keep fp32's accuracy to two bits, the state itself stays
-// in fp32 registers. For X, U and the state every value column has a power of
-// two of its own, from z, twice the larger of max |v| and c max |S| of the column (|S k| <= c max |S|,
-// c a little above the root of the number of keys): z in (2^5, 2^8]. With beta |k|^2 <= 1 a token only shrinks what is
-// there and adds its v, so |U| <= 65 z < 2^15; up to 2.1 it grows by 1.1 at most, 64 of
-// them by 2^9, and z stays in (2, 2^4]. What is cut off is 2^-25 of these units, 2^-30 of z.
-// That is too much where strong decays leave nothing of a state, or of a v, that set the
-// scale: with gamma_C < 2^-8 and a v of 16 tokens 2^-8 below z the chunk is not taken.
-// A chunk with other values (without the norm; growing decays; a NaN or an infinity)
-// is marked by prep, or seen by the wave, and runs token by token in the same
+// What bounds it: the chunks of a row follow each other, and in a workgroup of four waves each has
+// a SIMD to itself, with nothing to hide its waits behind. 1 x 4096 tokens, 32 value heads of 128, bf16:
+// prep 31 us (its waves wait for memory 59 % of the time) and sweep 211, 3.3 a chunk; 106 MB are
+// the least to move, 21 us. Rows fill the GPU with more waves: 8 x 4096 take 586 us, 1.5 TB/s.
+//
+// Precision: fp32 sums of products of fp16. k and q of 16 bits, scaled by a power of two to a
+// length in [1, 2), are fp16 exactly but for what lies 2^-25 below that length; of fp32 they
+// are pairs of fp16. L, P, the inverses, X, U and the state are pairs, hi + lo, 22 bits:
+// their products keep fp32's accuracy to two bits, the state itself stays in fp32
+// registers. For X, U and the state every value column has a power of two of its own,
+// from z, twice the larger of max |v| and c max |S| of the column (|S k| <= c max |S|, c a
+// little above the root of the number of keys): z in (2^5, 2^8]. With beta |k|^2 <= 1 a token
+// only shrinks what is there and adds its v, so |U| <= 65 z < 2^15; up to 2.1 it grows by
+// 1.1 at most, 64 of them by 2^9, and z stays in (2, 2^4]. What is cut off is 2^-25 of these
+// units, 2^-30 of z. That is too much where strong decays leave nothing of a state, or of
+// a v, that set the scale: with gamma_C < 2^-8 and a v of 16 tokens 2^-8 below z the chunk
+// is not taken. A chunk with other values (without the norm; growing decays; a NaN or an
+// infinity) is marked by prep, or seen by the wave, and runs token by token in the same
 // registers, so that nothing reaches a token before it.
 //
 // Decays: sums of logarithms only ever add (from a token to its tile's ends, and
@@ -35,11 +40,10 @@
 // has row or column c and eight contraction slots of lane group g. The order
 // of a contraction's slots is free if both operands have the same, so an
 // accumulator serves as an operand as it is: slots 4 g + r of one tile, then of the next (32
-// deep), or hi, then lo of one tile (16 deep: [A_hi | A_lo] with [B_hi | B_hi]
-// and [B_lo | 0], both products in two instructions). S^T [key][value] is such an
-// accumulator: it never leaves registers. K is kept with its keys in that
-// order, in two planes of 8 bytes a lane, which both a row read (two planes) and
-// a transposed read (ds_read_b64_tr_b16, one plane) take without bank conflicts.
+// deep; L, P and U go by pairs of tiles), or of one alone (16 deep, the inverses). S^T
+// [key][value] is such an accumulator: it never leaves registers. K is kept with its
+// keys in that order, in two planes of 8 bytes a lane, which both a row read (two
+// planes) and a transposed read (ds_read_b64_tr_b16, one plane) take without bank conflicts.
 #pragma once
 
 #include "ssu_delta_impl.h"

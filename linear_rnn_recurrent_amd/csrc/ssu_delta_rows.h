@@ -1,6 +1,5 @@
 // The gated delta rule token by token: single tokens, windows of drafted
-// tokens, short prompts, and what the matrix cores do not take (fp32
-// activations, unaligned rows, head_dim 32 and 256).
+// tokens, short prompts, and rows that are not 16-byte aligned.
 //
 //   S <- alpha S;  u = beta (v - S k);  S <- S + u k^T;  o = scale S q
 //
@@ -13,6 +12,10 @@
 // lanes by DPP, and one multiply-add. The norms of q and k and their product
 // are sums over the same lanes; the gates of 64 tokens are formed at once, one a lane.
 // BLK tokens are read ahead, unconverted, so that a window waits for memory once.
+//
+// HBM bounds single tokens, by the state's read and write: 64 rows of 32 heads of 128 take
+// 50.5 us, 270 MB at 5.35 TB/s. Windows: the state once, then the chain from token to token, 0.8 us
+// a token (14 rows x 5, the state only read: 19.5 us, of which its 29 MB take 6).
 #pragma once
 
 #include "ssu_delta_impl.h"

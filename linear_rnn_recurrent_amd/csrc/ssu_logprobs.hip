@@ -2,7 +2,11 @@
 // most probable alternatives, from logits, in one pass over them:
 //   lse = m + log s,  s = sum e^(x - m);  entropy = log s - (sum e^(x - m) (x - m)) / s
 // Each lane keeps m, s and the weighted sum t of what it has seen and rescales
-// them when m grows (t <- e^d (t + d s), d = m_old - m_new). HBM bounds it.
+// them when m grows (t <- e^d (t + d s), d = m_old - m_new).
+// The vector ALU bounds 16 bits, some 15 instructions a logit, eight the least: 2039 rows of
+// 32000 bf16 take 39.8 us (131 MB, 3.3 TB/s) with 3 alternatives, 56 with 20. 128 of 131072 fp32
+// take 19.8 us with one (3.4 TB/s), 28.3 with 20; a row alone 11, two launches and the
+// chain of its wave's tiles.
 //
 // The k largest logits of a wave stand in its lanes, entry i in lane i, as keys that
 // order by (value descending, index ascending). A tile of 64 x 16 logits is compared

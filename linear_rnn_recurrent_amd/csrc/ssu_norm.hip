@@ -3,7 +3,10 @@
 //   h = x + residual;  y = h rsqrt(mean h^2 + eps) w;  code = e4m3(y / s), s = max |y| / 448
 // Every tensor is read and written once: the span of columns that a sum or a
 // maximum runs over (the group, or the block of a scale where that is larger)
-// stays in registers between its passes. HBM bounds it.
+// stays in registers between its passes. HBM bounds it, with the vector ALU close
+// behind where there is a gate: 4099 rows of 2048 with a residual to e4m3 take 15 us (59 MB,
+// 3.9 TB/s), 4096 x 32 heads of 128 with a gate 21.2 (101 MB, 4.75 TB/s), 64 rows of 5120 7.3
+// a call and 5.1 in a graph (a launch and one chain of loads).
 //
 // A span belongs to a team of threads, each with NV vectors of eight columns,
 // vector m + TEAM j for thread m, so that a load instruction takes consecutive
@@ -110,11 +113,16 @@ __device__ __forceinline__ void st_vec8(void *p, int64_t i, int dt, const float 
             }
         } else {
             u32x4 w;
+            if (dt == kBF16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                w[k] = dt == kBF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(
-                                         (nm_f32x2){v[2 * k], v[2 * k + 1]}, nm_bf16x2))
-                                   : f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
+                for (int k = 0; k < 4; ++k)
+                    w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                                                            (nm_f32x2){v[2 * k], v[2 * k + 1]}, nm_bf16x2));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
+            }
             uint16_t *q = static_cast<uint16_t *>(p) + i;
             if constexpr (VEC)
                 *reinterpret_cast<u32x4 *>(q) = w;
@@ -192,7 +200,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
     const int nt = blockDim.x;
     const int m = WG ? threadIdx.x : (threadIdx.x & (team - 1));
     // fewer than 2^32 threads: 32 bits
-    const uint32_t s = WG ? blockIdx.x : (blockIdx.x * (uint32_t)nt + threadIdx.x) / (uint32_t)team;
+    const uint32_t s = WG ? blockIdx.x : (blockIdx.x * (uint32_t)nt + threadIdx.x) >> __builtin_ctz(team);
     // lanes past the last span keep their wave whole for the exchanges
     const bool live = s < spans;
     const uint32_t row = !live ? 0 : per_row == 1 ? s : s / (uint32_t)per_row;
@@ -210,7 +218,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = m + (WG ? nt : team) * j;
-        cols[j] = live && i < vecs ? min(8, span - 8 * i) : 0;
+        cols[j] = !live || i >= vecs ? 0 : VEC ? 8 : min(8, span - 8 * i);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sq[j] += e < cols[j] ? h[j][e] * h[j][e] : 0.0f;
+                sq[j] += VEC || e < cols[j] ? h[j][e] * h[j][e] : 0.0f;
         }
     }
 
@@ -289,7 +297,13 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
             sq[j] = a;
     }
 
+    const float one = p.unit_offset ? 1.0f : 0.0f;
+    // A block within one group: its codes are those of h w over their maximum, without the
+    // root, and so without two of the four roundings before the code (264 codes of 10^8 differ
+    // from the formula's, 326 with them)
+    const bool apart = p.out_dtype == kE4m3 && p.block <= p.group;
     uint32_t most[NV];
+    float root[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         most[j] = 0;
@@ -298,6 +312,9 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
         float inv = __builtin_amdgcn_rsqf(mean);
         const float half = 0.5f * inv;
         inv = mean > 0x1p-100f && mean < 0x1p100f ? fmaf(half, fmaf(-mean * inv, inv, 1.0f), inv) : inv;
+        root[j] = apart ? inv : 1.0f;
+        if (apart)
+            inv = 1.0f;
         if (cols[j] > 0) {
             float w[8], z[8];
             if (!EARLY) {
@@ -312,12 +329,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
                 cvt_raw8(rz[j], p.io_dtype, z);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float y = h[j][e] * inv * (p.unit_offset ? 1.0f + w[e] : w[e]);
+                float y = h[j][e] * inv * (one + w[e]);
                 if (p.z && !p.gate_first)
                     y *= gate_of(z[e]);
                 h[j][e] = y;
-                const uint32_t mag = e < cols[j] ? __float_as_uint(y) & 0x7fffffffu : 0u;
-                most[j] = mag > most[j] ? mag : most[j];
+            }
+            if (p.out_dtype == kE4m3) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t mag = VEC || e < cols[j] ? __float_as_uint(h[j][e]) & 0x7fffffffu : 0u;
+                    most[j] = mag > most[j] ? mag : most[j];
+                }
             }
         }
     }
@@ -358,9 +380,15 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p, int span, int 
     for (int j = 0; j < NV; ++j)
         if (cols[j] > 0) {
             const int i = m + (WG ? nt : team) * j, c = c0 + 8 * i;
-            const float a = __uint_as_float(most[j]) / 448.0f;
+            const float top = __uint_as_float(most[j]);
+            const float a = top * root[j] / 448.0f;
             const float scale = a < 0x1p-126f ? 0x1p-126f : a;  // a NaN stays
-            st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], scale, 1.0f / scale, cols[j]);
+            const bool fine = top > 0x1p-100f && top < 0x1p100f && a >= 0x1p-126f;
+            const float by = fine ? top / 448.0f : scale, times = fine ? 1.0f : root[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[j][e] *= times;
+            st_e4m3<VEC>(p.out, b * p.out_bs + t * p.out_ts + c, h[j], by, 1.0f / by, cols[j]);
             const int in = p.block >= span ? 8 * i : (8 * i) & (p.block - 1);
             if (in == 0)
                 p.scales[(int64_t)row * (p.columns / p.block) + c / p.block] = scale;
