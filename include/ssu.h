@@ -674,12 +674,13 @@ typedef struct ssu_logprob_dims {
  * A logit of -inf has no probability; a row of nothing else has log
  * probabilities of -inf, entropy 0 and the ids 0..k-1. A row with a NaN or
  * +inf has NaN log probabilities (but of tokens outside [0, V)) and entropy,
- * and as ids k different ones of [0, V). For t >= L_b and padding rows
+ * and as ids unspecified ones of [0, V) or -1. For t >= L_b and padding rows
  * (state_indices[b] < 0): 0, 0, -1, 0, and no logit is read.
  * Layouts: logits [batch, T, V], tokens, logprobs, entropy [batch, T],
  * top_ids, top_logprobs [batch, T, k], all but logits dense. Optional: entropy,
  * top_ids, top_logprobs (both or neither; top > 0 with them, ignored without),
- * context_lengths, state_indices. batch * T up to 2^25 (else SSU_ENOTSUP).
+ * context_lengths, state_indices. batch * T below 2^24 (a launch has fewer than
+ * 2^32 threads, 256 a row; else SSU_ENOTSUP).
  * workspace: caller-owned device scratch of at least
  * ssu_logprobs_workspace_bytes(dims) bytes, 16-byte aligned (NULL where that is
  * 0: many rows); contents on entry ignored, on return unspecified; calls sharing

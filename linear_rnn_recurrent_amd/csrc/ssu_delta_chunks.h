@@ -14,7 +14,7 @@
 //
 // What bounds it: the chunks of a row follow each other, and in a workgroup of four waves each has
 // a SIMD to itself, with nothing to hide its waits behind. 1 x 4096 tokens, 32 value heads of 128, bf16:
-// prep 31 us (its waves wait for memory 59 % of the time) and sweep 211, 3.3 a chunk; 106 MB are
+// prep 31 us (its waves wait 60 % of the time) and sweep 211, 3.3 a chunk; 106 MB are
 // the least to move, 21 us. Rows fill the GPU with more waves: 8 x 4096 take 586 us, 1.5 TB/s.
 //
 // Precision: fp32 sums of products of fp16. k and q of 16 bits, scaled by a power of two to a
