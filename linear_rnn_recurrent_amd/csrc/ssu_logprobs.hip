@@ -228,7 +228,7 @@ struct LogitTile {
 // Logits [begin, end) of a row by one wave, every `step` th tile from `begin`.
 template <typename T, bool VEC>
 __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int lane, Sums &sums,
-                          Top &top, TopLds &lds)
+                          Top &top, TopLds &lds, uint32_t &reached)
 {
     using Tile = LogitTile<T>;
     sums = {neg_inf(), 0.0f, 0.0f};
@@ -261,6 +261,8 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
                     if (Tile::at(lane, l, e) >= left)
                         x[l * Tile::VE + e] = neg_inf();
         }
+        // the best bound of the workgroup's waves: k logits of the row reach it
+        const uint32_t others = __hip_atomic_load(&reached, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         float m = neg_inf();
 #pragma unroll
         for (int e = 0; e < kTile; ++e)
@@ -274,9 +276,13 @@ __device__ void wave_pass(const T *row, int begin, int end, int step, int k, int
             sums.s += p;
             sums.t += p * fmaxf(d, kFloor);
         }
+        if (k > 0)
+            bound = fmaxf(bound, of_order(others));
         if (k > 0 && __ballot(m >= fmaxf(bound, above))) {
             most = fmaxf(most, m);
             bound = fmaxf(bound, kth_of_lanes(most, k));
+            if (lane == 0)
+                __hip_atomic_fetch_max(&reached, order_of(bound), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
             if (n > kGather) {
                 top.take(lds, n, bound, k, lane);
                 n = 0;
@@ -414,6 +420,10 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, 
     __shared__ Key lists[kWaves * kMaxTop], best[kMaxTop];
     __shared__ TopLds tops[kWaves];
     __shared__ Gathered gathered;
+    __shared__ uint32_t reached;  // a bound's order_of; 0 is that of a NaN, which bounds nothing
+    if (threadIdx.x == 0)
+        reached = 0;
+    __syncthreads();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = (int)(blockIdx.x / (uint32_t)parts);
     const int which = (int)(blockIdx.x - (uint32_t)row * (uint32_t)parts);
@@ -433,7 +443,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, 
     Top top;
     const int64_t mine = begin + (int64_t)wave * 64 * kTile;
     wave_pass<T, VEC>(logits, (int)min(mine, (int64_t)end), end, kWaves, p.top, lane, sums, top,
-                      tops[wave]);
+                      tops[wave], reached);
     if (lane == 0)
         sums_of[wave] = sums;
     if (lane < p.top)
