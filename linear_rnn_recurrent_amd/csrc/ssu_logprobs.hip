@@ -4,15 +4,16 @@
 // Each lane keeps m, s and the weighted sum t of what it has seen and rescales
 // them when m grows (t <- e^d (t + d s), d = m_old - m_new).
 // The vector ALU bounds 16 bits, some 15 instructions a logit, eight the least: 2039 rows of
-// 32000 bf16 take 39.8 us (131 MB, 3.3 TB/s) with 3 alternatives, 56 with 20. 128 of 131072 fp32
-// take 19.8 us with one (3.4 TB/s), 28.3 with 20; a row alone 11, two launches and the
+// 32000 bf16 take 38.8 us (131 MB, 3.4 TB/s) with 3 alternatives, 56 with 20. 128 of 131072 fp32
+// take 19.3 us with one (3.5 TB/s), 28.1 with 20; a row alone 11, two launches and the
 // chain of its wave's tiles.
 //
 // The k largest logits of a wave stand in its lanes, entry i in lane i, as keys that
 // order by (value descending, index ascending). A tile of 64 x 16 logits is compared
 // with the last of them by the lanes' maxima: most tiles after the first few hold
 // nothing that gets in. The k-th largest of the 64 lanes' maxima over all tiles so far
-// bounds the k-th largest logit from below, which leaves little more than k to insert.
+// bounds the k-th largest logit from below, which leaves little more than k to insert;
+// the best bound of a workgroup's waves holds for all of them.
 //
 // A row goes to one workgroup where there are rows enough, else to several:
 // their sums and lists go through the workspace to a second launch, one

@@ -4,9 +4,9 @@
 // Every tensor is read and written once: the span of columns that a sum or a
 // maximum runs over (the group, or the block of a scale where that is larger)
 // stays in registers between its passes. HBM bounds it, with the vector ALU close
-// behind where there is a gate: 4099 rows of 2048 with a residual to e4m3 take 15 us (59 MB,
-// 3.9 TB/s), 4096 x 32 heads of 128 with a gate 20.2 (101 MB, 5.0 TB/s), 64 rows of 5120 7.4
-// a call and 5.6 in a graph (a launch and one chain of loads).
+// behind where there is a gate: 4099 rows of 2048 with a residual to e4m3 take 14.7 us (59 MB,
+// 4.0 TB/s), 4096 x 32 heads of 128 with a gate 20.3 (101 MB, 5.0 TB/s), 64 rows of 5120 7.3
+// a call and 5.7 in a graph (a launch and one chain of loads).
 //
 // A span belongs to a team of threads, each with NV vectors of eight columns,
 // vector m + TEAM j for thread m, so that a load instruction takes consecutive
