@@ -32,10 +32,9 @@ DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t s
     DeltaPlan q = {};
     if (batch <= 0 || batch > 65535 || seq_len < kDeltaLeast)
         return q;
-    const bool f32 = io_dtype == kF32;
-    const int tiles = delta_tiles(d, f32);
+    const int planes = delta_planes(io_dtype), tiles = delta_tiles(d, planes);
     q.spans = (int32_t)((seq_len + 63) / 64);
-    const int64_t kq = batch * hq * 256 * d * (f32 ? 2 : 1);
+    const int64_t kq = batch * hq * 256 * d * planes;
     const int64_t head = batch * hv * (4 / tiles) * delta_head_bytes(tiles);
     int64_t segment = kDeltaSegment / (kq + head);
     segment = segment < 1 ? 1 : segment;

@@ -176,10 +176,11 @@ hipError_t launch_delta(const DeltaParams &p, hipStream_t stream);
 // The evaluation in chunks of 16 delta_tiles() tokens: spans of 64 tokens, those of one
 // segment (prep and sweep follow each other by segments, which bounds the workspace),
 // whether a workgroup takes all of a head, bytes of the workspace's parts. spans == 0: token by token.
-// 64 tokens where two of them fit in LDS, 32 elsewhere: 8 heads of 64, fp32, 1 x 4096 take 213 us by 64,
-// 246 by 32 (16 x 2048, 16 heads: 254 and 246; 1 x 32 tokens: 16 and 13).
-constexpr int delta_tiles(int64_t d, bool f32) { return d > (f32 ? 64 : 128) ? 2 : 4; }
-constexpr int delta_head_bytes(int tiles) { return (tiles == 4 ? 26 : 9) * 1024; }  // of a chunk
+// k and q are one bf16 plane, two of fp16, three of fp32; 64 tokens a chunk where two chunks fit in
+// LDS, 32 elsewhere.
+constexpr int delta_planes(int dtype) { return dtype == 0 ? 3 : dtype == 1 ? 2 : 1; }
+constexpr int delta_tiles(int64_t d, int planes) { return d * planes > 128 ? 2 : 4; }
+constexpr int delta_head_bytes(int tiles) { return (tiles == 4 ? 32 : 10) * 1024; }  // of a chunk
 struct DeltaPlan {
     int32_t spans, segment, wide;
     int64_t kq_bytes, head_bytes, carry_bytes;
