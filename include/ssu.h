@@ -584,10 +584,11 @@ ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const voi
  * with the token-by-token recurrence to fp32 rounding, not bitwise (what a
  * product takes of its factors below 2^-126 counts as 0 there). A growing decay
  * (g > 0), a beta outside [-1, 2] / k.k, a NaN or an infinity is followed token
- * by token over the chunk that has it, at several times the cost. With use_qk_l2norm a row of q or k whose sum of squares leaves
- * fp32's range is undefined. seq_len up to
- * 2^30 and token strides up to 2^25 (else SSU_ENOTSUP), and so is a call that
- * needs 2^32 threads (a thread has 8 or 16 keys of two or four rows).
+ * by token over the chunk that has it, at several times the cost. With
+ * use_qk_l2norm a row of q or k whose sum of squares leaves fp32's range is
+ * undefined. seq_len up to 2^30 and token strides up to 2^25 (else SSU_ENOTSUP),
+ * and so is a call that needs 2^32 threads (a thread has 8 or 16 keys of two or
+ * four rows).
  * workspace: caller-owned device scratch of at least
  * ssu_delta_workspace_bytes(dims, seq_len) bytes, 16-byte aligned (NULL where
  * that is 0); contents on entry ignored, on return unspecified; calls sharing a
@@ -682,8 +683,7 @@ typedef struct ssu_logprob_dims {
  * Layouts: logits [batch, T, V], tokens, logprobs, entropy [batch, T],
  * top_ids, top_logprobs [batch, T, k], all but logits dense. Optional: entropy,
  * top_ids, top_logprobs (both or neither; top > 0 with them, ignored without),
- * context_lengths, state_indices. batch * T below 2^24 (a launch has fewer than
- * 2^32 threads, 256 a row; else SSU_ENOTSUP).
+ * context_lengths, state_indices. batch * T up to 2^25 (else SSU_ENOTSUP).
  * workspace: caller-owned device scratch of at least
  * ssu_logprobs_workspace_bytes(dims) bytes, 16-byte aligned (NULL where that is
  * 0: many rows); contents on entry ignored, on return unspecified; calls sharing
@@ -695,8 +695,9 @@ ssu_status ssu_token_logprobs(const ssu_logprob_dims *dims, const void *logits,
                               int64_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace ssu_token_logprobs needs for exactly these batch,
- * num_tokens, vocab and top (the parts of a split vocabulary); -1 if dims is
- * NULL or one of them is out of range. No HIP call. */
+ * num_tokens, vocab and top (the parts of a split vocabulary; top is 0 here for
+ * a call without top_ids); -1 if dims is NULL or one of them is out of range,
+ * batch * num_tokens above 2^25 among them. No HIP call. */
 int64_t ssu_logprobs_workspace_bytes(const ssu_logprob_dims *dims);
 
 /* ------------------------------------------------------------------------

@@ -415,7 +415,7 @@ __device__ void place_lists(const Key *lists, int parts, int k, Key *got, Gather
 __host__ __device__ inline int64_t part_words(int64_t top) { return 4 + 2 * top; }
 
 template <typename T, bool VEC>
-__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, int parts, int part)
+__global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, int parts, int part, int row0)
 {
     __shared__ Sums sums_of[kWaves];
     __shared__ Key lists[kWaves * kMaxTop], best[kMaxTop];
@@ -426,8 +426,8 @@ __global__ __launch_bounds__(64 * kWaves) void logprobs_kernel(LogprobParams p, 
         reached = 0;
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = (int)(blockIdx.x / (uint32_t)parts);
-    const int which = (int)(blockIdx.x - (uint32_t)row * (uint32_t)parts);
+    const int which = (int)(blockIdx.x % (uint32_t)parts);
+    const int row = row0 + (int)(blockIdx.x / (uint32_t)parts);
     if (!row_live(p, row)) {
         if (which == 0 && wave == 0)
             write_padding(p, row, lane);
@@ -522,15 +522,20 @@ hipError_t launch_logprobs_t(const LogprobParams &p, hipStream_t stream)
     const int parts = logprobs_parts(rows, p.vocab);
     const int round = kWaves * 64 * kTile;
     const int part = (int)((((int64_t)p.vocab + parts - 1) / parts + round - 1) / round * round);
-    if (!launchable((__int128)rows * parts, 64 * kWaves))
-        return hipErrorInvalidConfiguration;
     const int64_t e = sizeof(T);
     const bool vec = ((uintptr_t)p.logits | (uintptr_t)(p.l_bs * e) | (uintptr_t)(p.l_rs * e)) % 16 == 0;
-    const dim3 grid((uint32_t)(rows * parts));
-    if (vec)
-        logprobs_kernel<T, true><<<grid, 64 * kWaves, 0, stream>>>(p, parts, part);
-    else
-        logprobs_kernel<T, false><<<grid, 64 * kWaves, 0, stream>>>(p, parts, part);
+    // a launch has fewer than 2^32 threads; rows of several parts are few
+    constexpr int64_t kRows = 1 << 23;
+    for (int64_t row0 = 0; row0 < rows; row0 += kRows) {
+        const int64_t some = rows - row0 < kRows ? rows - row0 : kRows;
+        if (!launchable((__int128)some * parts, 64 * kWaves))
+            return hipErrorInvalidConfiguration;
+        const dim3 grid((uint32_t)(some * parts));
+        if (vec)
+            logprobs_kernel<T, true><<<grid, 64 * kWaves, 0, stream>>>(p, parts, part, (int)row0);
+        else
+            logprobs_kernel<T, false><<<grid, 64 * kWaves, 0, stream>>>(p, parts, part, (int)row0);
+    }
     if (parts > 1)
         logprobs_join_kernel<T><<<dim3((uint32_t)rows), 256, 0, stream>>>(p, parts);
     return hipGetLastError();
