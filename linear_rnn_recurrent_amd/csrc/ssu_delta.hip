@@ -17,12 +17,21 @@ hipError_t launch_delta_chunks_bf16(const DeltaParams &p, const DeltaPlan &plan,
 
 namespace {
 
-// Tokens from which chunks are taken: a single chunk takes 19 us of one row of 32 heads of
-// 128, 43 of 16 rows, 135 of 64; token by token 16 of them take 16, 44 and 134 us, 31 take 28, 72
-// and 250.
-constexpr int kDeltaLeast = 18;
-// Bytes handed over at a time: 8 x 4096 tokens of 32 heads take 814 us by 48 MiB, 672 by
-// 96, 601 by 192, 583 by 400, 564 at once (3.4 GB): each segment fills and drains the GPU twice.
+// Tokens from which chunks are taken. Token by token, time grows with the tokens; a chunk costs the
+// same for 2 tokens as for all of its own. In a captured graph, us for 16 / 20 / 28 / 48 tokens one by one and in
+// a chunk (bf16; the other types meet up to seven tokens later, by 5 us at most):
+//   heads of 128: 32 of them 16.2 19.4 25.5 40.5 and 19.8; 512: 44 52 67 106 and 47; 2048: 133 164 223 370 and 147
+//   heads of 256:  8 of them 23.3 28.2 38.6 58.2 and 17.4; 128: 40 47 59 91 and 31; 512: 130 153 199 316 and 102
+//   heads of 64:   8 of them 16.6 20.0 26.1 41.4 and 16.4; 128: 16.0 19.1 25.1 39.7 and 18.9; 512: 17.4 20.5 26.3 41.6 and 32.5
+//   heads of 32:   8 of them 11.0 13.0 16.7 25.7 and 14.8; 128: 11.3 13.3 17.3 26.4 and 16.8; 512: 11.7 13.7 17.9 27.7 and 29.0
+int least_tokens(int64_t heads, int64_t d)
+{
+    if (d >= 128)
+        return 18;
+    return d == 64 ? (heads > 256 ? 36 : 18) : (heads > 256 ? 50 : 24);
+}
+// Bytes handed over at a time: 8 x 4096 tokens of 32 heads of 128 take 724 us by 96 MiB, 683 by 256, 662
+// by 512; 8 x 777 of fp16 182, 173 and 172: each segment fills and drains the GPU twice.
 constexpr int64_t kDeltaSegment = (int64_t)256 << 20;
 
 }  // namespace
@@ -30,7 +39,7 @@ constexpr int64_t kDeltaSegment = (int64_t)256 << 20;
 DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t seq_len, int32_t io_dtype)
 {
     DeltaPlan q = {};
-    if (batch <= 0 || batch > 65535 || seq_len < kDeltaLeast)
+    if (batch <= 0 || batch > 65535 || seq_len < least_tokens(batch * hv, d))
         return q;
     const int planes = delta_planes(io_dtype), tiles = delta_tiles(d, planes);
     q.spans = (int32_t)((seq_len + 63) / 64);
@@ -42,8 +51,9 @@ DeltaPlan delta_plan(int64_t batch, int64_t hq, int64_t hv, int64_t d, int64_t s
     segment = (q.spans + parts - 1) / parts;  // of like sizes
     q.segment = (int32_t)segment;
     // Workgroups of 64 value columns, as long as each has a CU to itself, run a chunk faster;
-    // beyond, those of 128 fetch a chunk for eight waves: 169 against 206 us at 256 of the former (4
-    // x 2048 tokens, 32 heads of 128), 283 against 221 at 320, 347 against 297 at 512.
+    // beyond, those of 128 fetch a chunk for eight waves. 2048 tokens of 32 heads of 128, bf16: 205 against 251
+    // us at 256 of the former, 342 against 261 at 320, 410 against 343 at 512; 1024 of fp16 132 against 169 at 256,
+    // 262 against 213 at 512; 512 of fp32 85 against 107 and 169 against 143.
     q.wide = batch * hv * d > 256 * 64;
     q.kq_bytes = kq * segment;
     q.head_bytes = head * segment;

@@ -177,7 +177,9 @@ hipError_t launch_delta(const DeltaParams &p, hipStream_t stream);
 // segment (prep and sweep follow each other by segments, which bounds the workspace),
 // whether a workgroup takes all of a head, bytes of the workspace's parts. spans == 0: token by token.
 // k and q are one bf16 plane, two of fp16, three of fp32; 64 tokens a chunk where two chunks fit in
-// LDS, 32 elsewhere.
+// LDS, 32 elsewhere. 1 x 4096 tokens, 32 heads of 128, bf16, take 298 us by 64 and 344 by 32, 8 heads of 64 225 and 243, of
+// 32 209 and 216. Rows enough for every CU, and prompts of 32 tokens, would do better by 32: 16 x 2048, 16 heads of 64 205
+// and 189 us, 16 x 512, 32 of 128 193 and 186, 64 x 32 148 and 111. One length a shape is kept: one form of the kernels.
 constexpr int delta_planes(int dtype) { return dtype == 0 ? 3 : dtype == 1 ? 2 : 1; }
 constexpr int delta_tiles(int64_t d, int planes) { return d * planes > 128 ? 2 : 4; }
 constexpr int delta_head_bytes(int tiles) { return (tiles == 4 ? 32 : 10) * 1024; }  // of a chunk
