@@ -12,10 +12,11 @@
 // needs nothing of the others, so there is no exchange between waves; U comes
 // tile after tile (U_i = (I + L_ii)^-1 X_i, then X_j -= L_ji U_i for the tiles j behind it).
 //
-// What bounds it: the chunks of a row follow each other, and in a workgroup of four waves each has
-// a SIMD to itself, with nothing to hide its waits behind. 1 x 4096 tokens, 32 value heads of 128, bf16:
-// prep 33 us and sweep 267, 4.2 a chunk, of which 204 matrix instructions keep their unit busy for
-// 1.4; 106 MB are the least to move, 21 us. Rows fill the GPU with more waves: 8 x 4096 take 704 us.
+// What bounds it: the chunks of a row follow each other, and in a workgroup of four waves (and a fifth that
+// fetches) each has a SIMD to itself, with nothing to hide its waits behind. 1 x 4096 tokens, 32 value heads of
+// 128, bf16: prep 33 us and sweep 245, 3.8 a chunk, of which 204 matrix instructions keep their unit busy for
+// 1.4 and 850 vector instructions theirs; 106 MB are the least to move, 21 us. Rows fill the GPU with more
+// waves: 8 x 4096 take 690 us.
 //
 // Precision: fp32 sums of products of bf16, which has fp32's range. What is of fp32 (the state, L, P,
 // the inverses, X, U; k and q of that type) goes into them as three parts, hi + mid + lo, 24 bits of every
@@ -23,8 +24,8 @@
 // nine products of two triples are formed; those left out are 2^-24 of it. So a chunk is as near to the
 // formula as the recurrence in fp32, but where rounding errors grow: with beta (k . k) of 2.1 and the same key
 // again and again they are 1.2e-5 of the outputs, the recurrence's 7e-7, and betas outside [-1, 2] / (k . k) are
-// not taken. Pairs of fp16 would do with 138 matrix instructions and 243 us for these 300, but cover 25 bits below a
-// unit that a column shares: what is small beside its largest value, of whichever token, loses digits.
+// not taken. Pairs of fp16 do with 138 matrix instructions, but cover 25 bits below a unit that a column shares: what is
+// small beside its largest value, of whichever token, loses digits.
 // A chunk that prep marks (such betas; growing decays, whose sums of logarithms cancel; a NaN or an
 // infinity in k or a gate), or whose U turns out not finite, runs token by token in the same
 // registers, so that nothing reaches a token before it.
@@ -612,9 +613,14 @@ struct DcValues<float, PITCH> {
     __device__ __forceinline__ float operator[](int r) const { return __uint_as_float(w[r]); }
 };
 
-// One wave: 16 value columns of value head h, batch entry b.
+// A workgroup: W waves of 16 value columns each, of value head h, batch entry b. Up to four have a wave beside them
+// that fetches (a chunk's loads, issued by waves alone on their SIMDs, cost them 22 us of 300, and in front of a
+// chunk they would wait for their own outputs too); eight hide the issue behind each other, and a ninth would
+// leave 168 registers a wave (1024 tokens, 16 heads of 256, 8 rows: 303 us for 220).
+constexpr bool dc_loader(int waves) { return waves <= 4; }
+
 template <typename IO, int D, int W, bool OUT>
-__global__ __launch_bounds__(64 * W, W > 4 ? 2 : 1) void delta_sweep_kernel(DeltaParams p, DeltaWork w, int swizzle)
+__global__ __launch_bounds__(64 * (W + dc_loader(W)), W > 4 ? 2 : 1) void delta_sweep_kernel(DeltaParams p, DeltaWork w, int swizzle)
 {
     using Sh = DcShape<IO, D>;
     constexpr int KS = D / 32, KT = D / 16, NT = Sh::NT, PL = Sh::PL, C = Sh::C, NP = NT / 2;
@@ -639,46 +645,67 @@ __global__ __launch_bounds__(64 * W, W > 4 ? 2 : 1) void delta_sweep_kernel(Delt
         return;
     const int chunks = mine > 0 ? (mine + C - 1) / C : 0;
 
-    // What prep left of a chunk, and its values, go to LDS past the registers, 1 KiB an
-    // instruction, while the chunk before it is worked on
+    // What prep left of a chunk, and its values, go to LDS past the registers, 1 KiB an instruction,
+    // while the chunk before it is worked on
+    constexpr bool LOADER = dc_loader(W);
+    constexpr int FW = LOADER ? 1 : W;  // waves that fetch
+    const int mine_of = LOADER ? 0 : wave;
     const unsigned char *kq = w.kq + ((int64_t)b * w.chunks * p.hq + j) * KQ + lane * 16;
     const unsigned char *hd = w.head + ((int64_t)b * w.chunks * p.hv + h) * Sh::HEAD + lane * 16;
     const int64_t kq_step = (int64_t)p.hq * KQ, hd_step = (int64_t)p.hv * Sh::HEAD;
     constexpr int VL = VP / 16, VR = 64 / VL;  // lanes a token's values, tokens an instruction
-    static_assert(C % VR == 0, "whole instructions");
+    constexpr int QK = OUT ? KQ : KQ / 2, HD = OUT ? Sh::HEAD : (Sh::P + 1023) / 1024 * 1024;
+    static_assert(C % VR == 0 && QK % 1024 == 0, "whole instructions");
     const IO *vp = static_cast<const IO *>(p.v) + b * p.v_bs + (int64_t)w.chunk0 * C * p.v_ts +
-                   (int64_t)h * D + v0 + 16 / sizeof(IO) * (lane % VL);
+                   (int64_t)h * D + (LOADER ? v0 - wave * 16 : v0) + 16 / sizeof(IO) * (lane % VL);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds;
     // part 0 .. 3 of four (the CU takes 64 bytes a cycle: issued at once, they would stall the wave)
     auto fetch = [&](int ch, int part) {
-        uint32_t to = lds0 + ch % NB * BUF;
-        const unsigned char *from = kq + ch * kq_step;
-        constexpr int QK = OUT ? KQ : KQ / 2;
-        static_assert(QK % 1024 == 0, "whole instructions");
-#pragma unroll
-        for (int o = 0; o < QK; o += W * 1024)
-            if (o / (W * 1024) % 4 == part && (o + W * 1024 <= QK || o + wave * 1024 < QK))
-                dc_to_lds(from + o + wave * 1024, to + o + wave * 1024);
-        to += KQ;
-        from = hd + ch * hd_step;
-        constexpr int HD = OUT ? Sh::HEAD : (Sh::P + 1023) / 1024 * 1024;
-#pragma unroll
-        for (int o = 0; o < HD; o += W * 1024)
-            if (o / (W * 1024) % 4 == part && (o + W * 1024 <= HD || o + wave * 1024 < HD))
-                dc_to_lds(from + o + wave * 1024, to + o + wave * 1024);
-        to += Sh::HEAD + wave * (C * VP);  // of its own columns
+        const uint32_t to = lds0 + ch % NB * BUF;
 #pragma unroll
         for (int q = 0; q < C / VR; ++q)
             if (q % 4 == part) {
                 const int t = ch * C + q * VR + lane / VL;  // rows behind the end repeat the last
-                dc_to_lds(reinterpret_cast<const unsigned char *>(vp + (int64_t)min(t, mine - 1) * p.v_ts),
-                          to + q * 1024);
+                const IO *from = vp + (int64_t)min(t, mine - 1) * p.v_ts;
+#pragma unroll
+                for (int x = 0; x < (LOADER ? W : 1); ++x)
+                    dc_to_lds(reinterpret_cast<const unsigned char *>(from + 16 * x),
+                              to + KQ + Sh::HEAD + (mine_of + x) * (C * VP) + q * 1024);
             }
+        const unsigned char *from = kq + ch * kq_step + mine_of * 1024;
+#pragma unroll
+        for (int o = 0; o < QK; o += FW * 1024)
+            if (o / (FW * 1024) % 4 == part && (o + FW * 1024 <= QK || o + mine_of * 1024 < QK))
+                dc_to_lds(from + o, to + mine_of * 1024 + o);
+        from = hd + ch * hd_step + mine_of * 1024;
+#pragma unroll
+        for (int o = 0; o < HD; o += FW * 1024)
+            if (o / (FW * 1024) % 4 == part && (o + FW * 1024 <= HD || o + mine_of * 1024 < HD))
+                dc_to_lds(from + o, to + KQ + mine_of * 1024 + o);
     };
-    if (NB == 2 && chunks > 0) {
+    auto fetch_all = [&](int ch) {
 #pragma unroll
         for (int part = 0; part < 4; ++part)
-            fetch(0, part);
+            fetch(ch, part);
+    };
+    // In front of a chunk its LDS is filled (by every wave: behind the barrier), the other one read
+    auto arrive = [&](int ch) {
+        if (NB == 1) {
+            __syncthreads();
+            fetch_all(ch);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
+    if (NB == 2 && chunks > 0 && (!LOADER || wave == W))
+        fetch_all(0);
+    if (LOADER && wave == W) {
+        for (int ch = 0; ch < chunks; ++ch) {
+            arrive(ch);
+            if (NB == 2 && ch + 1 < chunks)
+                fetch_all(ch + 1);
+        }
+        return;
     }
 
     // The state: S^T, tile n of keys; rows (keys) 4 g + r, column (value) c
@@ -712,22 +739,20 @@ __global__ __launch_bounds__(64 * W, W > 4 ? 2 : 1) void delta_sweep_kernel(Delt
     const int o_off = c * (int)p.out_ts + 4 * g;
 
     for (int ch = 0; ch < chunks; ++ch) {
-        if (NB == 1) {
-            __syncthreads();  // the chunk before is read
-#pragma unroll
-            for (int part = 0; part < 4; ++part)
-                fetch(ch, part);
+        if (!LOADER) {
+            arrive(ch);
+        } else {
+            if (NB == 1)
+                __syncthreads();
+            __syncthreads();
         }
-        // this chunk's LDS is filled (by every wave: behind the barrier), the other one read
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
         unsigned char *image = lds + ch % NB * BUF;
         const unsigned char *blk = image + KQ;
         unsigned char *rows = image + KQ + Sh::HEAD + wave * (C * VP);  // values of the wave's columns
         const float *scal = reinterpret_cast<const float *>(blk + Sh::SCALARS);
         const int t0 = ch * C, n_tok = min(mine - t0, C);
         const int64_t tok0 = (int64_t)w.chunk0 * C + t0;
-        const bool ahead = NB == 2 && ch + 1 < chunks;
+        const bool ahead = !LOADER && NB == 2 && ch + 1 < chunks;
         if (ahead)
             fetch(ch + 1, 0);
         DcValues<IO, VP> v[NT];
@@ -973,13 +998,13 @@ template <typename IO, int D, int W>
 hipError_t launch_delta_sweep(const DeltaParams &p, const DeltaWork &w, hipStream_t stream)
 {
     const __int128 groups = (__int128)p.batch * p.hv * (D / (16 * W));
-    if (!launchable(groups, 64 * W))
+    if (!launchable(groups, 64 * (W + dc_loader(W))))
         return hipErrorInvalidConfiguration;
     const uint32_t n = (uint32_t)groups;
     if (p.out)
-        delta_sweep_kernel<IO, D, W, true><<<dim3(n), 64 * W, 0, stream>>>(p, w, n % 8 == 0);
+        delta_sweep_kernel<IO, D, W, true><<<dim3(n), 64 * (W + dc_loader(W)), 0, stream>>>(p, w, n % 8 == 0);
     else
-        delta_sweep_kernel<IO, D, W, false><<<dim3(n), 64 * W, 0, stream>>>(p, w, n % 8 == 0);
+        delta_sweep_kernel<IO, D, W, false><<<dim3(n), 64 * (W + dc_loader(W)), 0, stream>>>(p, w, n % 8 == 0);
     return hipGetLastError();
 }
 
