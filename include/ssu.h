@@ -584,7 +584,8 @@ ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const voi
  * with the token-by-token recurrence to fp32 rounding, not bitwise (what a
  * product takes of its factors below 2^-126 counts as 0 there). A growing decay
  * (g > 0), a beta outside [-1, 2] / k.k, a NaN or an infinity is followed token
- * by token over the chunk that has it, at several times the cost. With
+ * by token over the chunk that has it, at ten to fifteen times the cost; so are
+ * all tokens of rows that are not aligned, at five to ten times. With
  * use_qk_l2norm a row of q or k whose sum of squares leaves fp32's range is
  * undefined. seq_len up to 2^30 and token strides up to 2^25 (else SSU_ENOTSUP),
  * and so is a call that needs 2^32 threads (a thread has 8 or 16 keys of two or
@@ -604,8 +605,8 @@ ssu_status ssu_delta_prefill(const ssu_delta_dims *dims, int32_t seq_len, const 
  * head_dim, io_dtype and seq_len (nothing else in dims counts); 0 where the
  * tokens run one by one. It stays below 2^28 and a state in fp32 a row (or one
  * stretch of 64 tokens of every row, where that is more), and a larger size may need
- * less than a smaller one (32 heads of 128: 88 MB at 1 x 4096, 259 MB at 8 x
- * 4096, 193 MB at 8 x 2048): a workspace kept for several has the largest of their
+ * less than a smaller one (32 heads of 128, bf16: 101 MB at 1 x 4096, 252 MB at 8 x
+ * 1280, 155 MB at 8 x 1400): a workspace kept for several has the largest of their
  * sizes, each of them asked for. -1 if dims is NULL or the call refuses one of
  * these. No HIP call. */
 int64_t ssu_delta_workspace_bytes(const ssu_delta_dims *dims, int32_t seq_len);
@@ -639,6 +640,7 @@ typedef struct ssu_norm_dims {
  *   h *= silu(z) if z is given and gate_first
  *   y = h / sqrt(mean of h^2 over its group + eps) * weight (or 1 + weight)
  *   y *= silu(z) if z is given and not gate_first
+ *   (a gate is off by up to (4 + |z|) 2^-24 of itself)
  *   out = y rounded; for SSU_E4M3, per block of scale_block columns,
  *   scales = max(max |y| / 448, 2^-126) and out = y / scales rounded to nearest
  *   even (a block of zeros has the scale 2^-126; a NaN makes its block's scale NaN).

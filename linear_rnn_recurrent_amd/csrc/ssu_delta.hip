@@ -72,7 +72,7 @@ hipError_t launch_delta(const DeltaParams &p, hipStream_t stream)
 {
     (void)hipGetLastError();  // report only this launch's status
     const DeltaPlan q = delta_plan(p.batch, p.hq, p.hv, p.d, p.seq_len, p.io_dtype);
-    if (q.spans && p.workspace && delta_rows_aligned(p, 16, true)) {
+    if (q.spans && p.workspace && delta_rows_aligned(p, 16)) {
         switch (p.io_dtype) {
         case kF32: return launch_delta_chunks_f32(p, q, stream);
         case kF16: return launch_delta_chunks_f16(p, q, stream);

@@ -52,16 +52,15 @@ __device__ __forceinline__ void delta_st_state(bf16_t *s, const float (&t)[4])
                                 reinterpret_cast<u32x2 *>(s));
 }
 
-// Whether every token's rows of q and k (and with `all`, of v and out) start at
-// a multiple of `bytes`
-inline bool delta_rows_aligned(const DeltaParams &p, int bytes, bool all = false)
+// Whether every token's rows of q, k, v and out start at a multiple of `bytes`
+inline bool delta_rows_aligned(const DeltaParams &p, int bytes)
 {
     const int64_t e = p.io_dtype == kF32 ? 4 : 2;
     auto fine = [&](const void *t, int64_t bs, int64_t ts) {
         return ((uintptr_t)t | (uintptr_t)(bs * e) | (uintptr_t)(ts * e)) % bytes == 0;
     };
-    return fine(p.k, p.k_bs, p.k_ts) && (!p.out || fine(p.q, p.q_bs, p.q_ts)) &&
-           (!all || (fine(p.v, p.v_bs, p.v_ts) && (!p.out || fine(p.out, p.out_bs, p.out_ts))));
+    return fine(p.k, p.k_bs, p.k_ts) && fine(p.v, p.v_bs, p.v_ts) &&
+           (!p.out || (fine(p.q, p.q_bs, p.q_ts) && fine(p.out, p.out_bs, p.out_ts)));
 }
 
 }  // namespace

@@ -268,7 +268,7 @@ hipError_t launch_delta_rows_r(const DeltaParams &p, hipStream_t stream)
         return hipErrorInvalidConfiguration;
     const dim3 grid((uint32_t)groups);
     constexpr int BLK = D > 128 || sizeof(IO) == 4 ? 2 : 4;  // as the registers of two waves a SIMD allow
-    const bool vec = delta_rows_aligned(p, 4 * sizeof(IO), true);
+    const bool vec = delta_rows_aligned(p, 4 * sizeof(IO));
     if (p.seq_len == 1 && vec)
         delta_rows_kernel<IO, ST, D, R, 1, true><<<grid, 256, 0, stream>>>(p);
     else if (vec)

@@ -24,7 +24,8 @@ namespace {
 typedef float nm_f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 nm_bf16x2 __attribute__((ext_vector_type(2)));
 
-// z / (1 + e^-z) by the hardware's 2^x and reciprocal, an ulp each
+// z / (1 + e^-z) by the hardware's 2^x and reciprocal, an ulp each. The argument of 2^x is rounded
+// once: of a gate far below 0, whose e^-z counts, |z| 2^-24 of its value
 __device__ __forceinline__ float gate_of(float z)
 {
     return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
