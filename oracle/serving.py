@@ -31,8 +31,8 @@ def gated_delta(q, k, v, a, b, state, *, A_log=None, dt_bias=None, scale=None, l
     |k| <= 1 and 0 <= beta <= 1 leaves e no larger (I - beta k k^T shrinks), decays it by
     alpha, and adds its own: products of d terms and their sums, the norms of q and k, exp,
     softplus and sigmoid and their arguments (d + 48 roundings of the row and of u), the same
-    again where a chunk of 64 tokens is summed in another order with operands cut to 22 bits
-    (two bits more: 4 roundings each of the three products).
+    again where a chunk of 64 tokens is summed in another order from operands in three parts, whose
+    products leave out what is below 24 bits (4 roundings each of the three products).
     """
     nb, t, hv, d = v.shape
     hq = k.shape[2]
