@@ -583,9 +583,10 @@ ssu_status ssu_delta_decode(const ssu_delta_dims *dims, const void *q, const voi
  * are 16-byte aligned run the tokens in chunks on the matrix cores: they agree
  * with the token-by-token recurrence to fp32 rounding, not bitwise (what a
  * product takes of its factors below 2^-126 counts as 0 there). A growing decay
- * (g > 0), a beta outside [-1, 2] / k.k, a NaN or an infinity is followed token
- * by token over the chunk that has it, at ten to fifteen times the cost; so are
- * all tokens of rows that are not aligned, at five to ten times. With
+ * (g > 0), a beta outside [-1, 2] / k.k, a NaN or an infinity in k, v, a gate or
+ * the state is followed token by token over the chunk that has it, at ten to
+ * fifteen times the cost; so are all tokens of rows that are not aligned, at
+ * five to ten times. One in q makes its token's outputs NaN. With
  * use_qk_l2norm a row of q or k whose sum of squares leaves fp32's range is
  * undefined. seq_len up to 2^30 and token strides up to 2^25 (else SSU_ENOTSUP),
  * and so is a call that needs 2^32 threads (a thread has 8 or 16 keys of two or

@@ -22,9 +22,9 @@
 // the inverses, X, U; k and q of that type) goes into them as three parts, hi + mid + lo, 24 bits of every
 // entry for itself, whatever stands beside it; k and q of fp16 are two parts, of bf16 one. Six of the
 // nine products of two triples are formed; those left out are 2^-24 of it. So a chunk is as near to the
-// formula as the recurrence in fp32, but where rounding errors grow: with beta (k . k) of 2.1 and the same key
-// again and again they are 1.2e-5 of the outputs, the recurrence's 7e-7, and betas outside [-1, 2] / (k . k) are
-// not taken. Pairs of fp16 do with 138 matrix instructions, but cover 25 bits below a unit that a column shares: what is
+// formula as the recurrence in fp32, but where rounding errors grow: with beta (k . k) of 2.02 and the same key
+// in 512 tokens they are 2e-4 of the outputs, the recurrence's 3e-6 (with 2, 3e-5 and 5e-6), and betas outside
+// [-1, 2] / (k . k), but for their rounding, are not taken. Pairs of fp16 do with 138 matrix instructions, but cover 25 bits below a unit that a column shares: what is
 // small beside its largest value, of whichever token, loses digits.
 // A chunk that prep marks (such betas; growing decays, whose sums of logarithms cancel; a NaN or an
 // infinity in k or a gate), or whose U turns out not finite, runs token by token in the same
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p, DeltaWor
             const float ks = lds.ks[lane], qs = lds.qs[lane], kk2 = lds.kk[lane];
             const float bk = beta * kk2;
             // (a q reaches no output but its own)
-            const bool bad = in && !(lg <= 0.0f && kk2 < __builtin_inff() && bk >= -1.02f && bk <= 2.02f);
+            const bool bad = in && !(lg <= 0.0f && kk2 < __builtin_inff() && bk >= -1.0001f && bk <= 2.0001f);
             const int mine = lane / C;  // chunk
             const uint64_t of_mine = (C == 64 ? ~(uint64_t)0 : (((uint64_t)1 << (C % 64)) - 1)) << (mine * C % 64);
             const float kind = __ballot(bad) & of_mine ? 1.0f : 0.0f;

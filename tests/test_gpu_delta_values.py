@@ -219,3 +219,17 @@ def test_an_overflow_reaches_no_earlier_token(at):
         near(y[0, :at], f64(want[0, :at]), 2 * 70, 64, "before")
         others = [c for c in range(64) if c != 7]
         assert torch.isfinite(y[0, at:, 1, others]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_query_that_is_not_finite_reaches_no_other_token(io, value):
+    T = given(111, seq_len=70, io=io, l2=False)
+    twin = {**T, "state": T["state"].clone()}
+    want = call(twin, l2=False)
+    T["q"] = T["q"].clone()
+    T["q"][0, 33, 0, 5] = value
+    y = call(T, l2=False)
+    assert not torch.isfinite(y[0, 33, :2].float()).any() and torch.isfinite(y[0, 33, 2:].float()).all()
+    others = [t for t in range(70) if t != 33]
+    assert torch.equal(y[0, others], want[0, others]) and torch.equal(T["state"], twin["state"])
